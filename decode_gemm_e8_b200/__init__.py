@@ -25,6 +25,8 @@ E8_EP_BLOCK_GROUPS = 64
 E8_EP_TABLE_WORDS = 770
 E8_GEMM_AUTO, E8_GEMM_ACT_RHT, E8_GEMM_DECODED_W, E8_GEMM_ACT_RHT_SMEM, E8_GEMM_SIMT = range(5)
 E8_OP_ENCODE = 100
+E8_DT_BF16, E8_DT_F16, E8_DT_F32 = range(3)
+E8_MOE_MAX_TOKENS, E8_MOE_MAX_EXPERTS, E8_MOE_MAX_TOPK = 64, 512, 16
 
 # every symbol include/e8.h declares
 EXPORTED = ("e8_codebook_build", "e8_codebook_free", "e8_codebook_export", "e8_rht_forward",
@@ -39,7 +41,10 @@ EXPORTED = ("e8_codebook_build", "e8_codebook_free", "e8_codebook_export", "e8_r
             "e8_version",
             "e8_ep_num_blocks", "e8_ep_max_words", "e8_ep_actual_bpp",
             "e8_ep_encode_workspace_bytes", "e8_ep_gemm_workspace_bytes", "e8_ep_encode",
-            "e8_ep_estimate_bpp", "e8_ep_choose_delta", "e8_ep_decode_to_bf16", "e8_ep_gemm")
+            "e8_ep_estimate_bpp", "e8_ep_choose_delta", "e8_ep_decode_to_bf16", "e8_ep_gemm",
+            "e8_mx4_code_bytes", "e8_mx4_scale_bytes", "e8_mx4_encode", "e8_mx4_decode_to_bf16",
+            "e8_mx4_gemm_codes", "e8_mx4_gemm", "e8_mx4_gemm_codes_workspace_bytes",
+            "e8_mx4_gemm_workspace_bytes", "e8_mx4_moe", "e8_mx4_moe_workspace_bytes")
 
 _lib = None
 
@@ -108,6 +113,17 @@ def load_library(path: str = LIB_PATH):
                                 P], c.c_int),
         "e8_ep_decode_to_bf16": ([P, P, I64, P, P, P, I64, I64, P, P], c.c_int),
         "e8_ep_gemm": ([P, P, I64, P, I64, P, P, P, I64, I64, P, P, c.c_size_t, P], c.c_int),
+        "e8_mx4_code_bytes": ([I64, I64], I64),
+        "e8_mx4_scale_bytes": ([I64, I64], I64),
+        "e8_mx4_encode": ([P, P, c.c_int, I64, I64, I64, I64, P, P, P], c.c_int),
+        "e8_mx4_decode_to_bf16": ([P, P, P, I64, I64, I64, P, P], c.c_int),
+        "e8_mx4_gemm_codes": ([P, P, P, I64, P, P, I64, I64, P, P, c.c_size_t, P], c.c_int),
+        "e8_mx4_gemm": ([P, P, c.c_int, I64, I64, P, P, I64, I64, P, P, c.c_size_t, P], c.c_int),
+        "e8_mx4_gemm_codes_workspace_bytes": ([I64, I64, I64], c.c_size_t),
+        "e8_mx4_gemm_workspace_bytes": ([I64, I64, I64], c.c_size_t),
+        "e8_mx4_moe": ([P, P, I64, I64, P, I64, c.c_int, c.c_int, P, P, I64, P, P, P, P, P, P,
+                        c.c_size_t, P], c.c_int),
+        "e8_mx4_moe_workspace_bytes": ([I64, I64, I64, c.c_int, I64], c.c_size_t),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -523,3 +539,184 @@ def e8_ep_gemm(cb: Codebook, X, m: EpMatrix, Y=None, workspace=None, stream=None
     _check(rc, "e8_ep_gemm")
     return Y
 
+
+
+# --------------------------------------------- microscaled 4-bit float form --
+class Mx4Matrix:
+    """A [rows, K] matrix (or a batch of them) in blocks of 32 e2m1 values with a
+    power-of-two scale each, as e8_mx4_encode writes it: codes uint8
+    [(batch,) rows, 16 ceil(K / 32)] and scales uint8 [(batch,) bytes in tiles]."""
+
+    def __init__(self, codes, scales, rows: int, K: int, batch: int | None = None):
+        self.codes, self.scales = codes, scales
+        self.rows, self.K, self.batch = int(rows), int(K), None if batch is None else int(batch)
+        lib = load_library()
+        n = 1 if self.batch is None else self.batch
+        if codes.numel() != n * lib.e8_mx4_code_bytes(self.rows, self.K) or \
+                scales.numel() != n * lib.e8_mx4_scale_bytes(self.rows, self.K):
+            raise E8Error(E8_EINVAL, "Mx4Matrix")
+
+
+def _mx4_dtype(X) -> int:
+    import torch
+    return {torch.bfloat16: E8_DT_BF16, torch.float16: E8_DT_F16,
+            torch.float32: E8_DT_F32}.get(X.dtype, -1)
+
+
+def _mx4_check(cb: Codebook, where: str, *tensors):
+    """Device tensors of the codebook's device, densely laid out."""
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda or t.device.index != cb.device:
+            raise E8Error(E8_EDEVICE, where)
+        if not t.is_contiguous():
+            raise E8Error(E8_EINVAL, where)
+
+
+def _mx4_out(out, shape, dtype, like, stream, where):
+    """The caller's output after a check, or a new one owned by the stream that writes it."""
+    import torch
+    if out is not None:
+        if tuple(out.shape) != tuple(shape) or out.dtype != dtype:
+            raise E8Error(E8_EINVAL, where)
+        return out
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def e8_mx4_encode(cb: Codebook, X, out: Mx4Matrix | None = None, stream=None) -> Mx4Matrix:
+    """X bf16 / fp16 / fp32 [rows, K] or [batch, rows, K] (CUDA) -> Mx4Matrix.
+
+    The last dimension must be dense; rows may be further apart (a slice of a wider
+    matrix), matrices rows * row stride apart."""
+    import torch
+    if X.dim() not in (2, 3):
+        raise E8Error(E8_EINVAL, "e8_mx4_encode")
+    batch = X.shape[0] if X.dim() == 3 else None
+    rows, K = X.shape[-2:]
+    ldx = _mx4_row_stride(cb, X, "e8_mx4_encode")
+    if batch is not None and batch > 1 and rows > 0:
+        if rows == 1:
+            ldx = X.stride(0)
+        elif X.stride(0) != rows * ldx:
+            raise E8Error(E8_EINVAL, "e8_mx4_encode")
+    lib = load_library()
+    n = 1 if batch is None else batch
+    lead = () if batch is None else (batch,)
+    if out is None:
+        cs, sb = lib.e8_mx4_code_bytes(rows, K), lib.e8_mx4_scale_bytes(rows, K)
+        if cs < 0:
+            raise E8Error(E8_EINVAL, "e8_mx4_encode")
+        codes = _mx4_out(None, lead + (rows, cs // max(rows, 1)), torch.uint8, X, stream, "")
+        scales = _mx4_out(None, lead + (sb,), torch.uint8, X, stream, "")
+        out = Mx4Matrix(codes, scales, rows, K, batch)
+    elif (out.rows, out.K, out.batch) != (rows, K, batch):
+        raise E8Error(E8_EINVAL, "e8_mx4_encode")
+    _mx4_check(cb, "e8_mx4_encode", out.codes, out.scales)
+    _check(lib.e8_mx4_encode(cb.handle, _ptr(X), _mx4_dtype(X), n, rows, K, ldx, _ptr(out.codes),
+                             _ptr(out.scales), _stream(stream)), "e8_mx4_encode")
+    return out
+
+
+def _mx4_row_stride(cb: Codebook, X, where: str) -> int:
+    if not X.is_cuda or X.device.index != cb.device:
+        raise E8Error(E8_EDEVICE, where)
+    rows, K = X.shape[-2:]
+    if K > 1 and X.stride(-1) != 1:
+        raise E8Error(E8_EINVAL, where)
+    return K if X.numel() == 0 or rows == 1 else X.stride(-2)
+
+
+def e8_mx4_decode_to_bf16(cb: Codebook, m: Mx4Matrix, out=None, stream=None):
+    """bf16 [(batch,) rows, K] values of an Mx4Matrix."""
+    import torch
+    shape = (m.rows, m.K) if m.batch is None else (m.batch, m.rows, m.K)
+    out = _mx4_out(out, shape, torch.bfloat16, m.codes, stream, "e8_mx4_decode_to_bf16")
+    _mx4_check(cb, "e8_mx4_decode_to_bf16", m.codes, m.scales, out)
+    _check(load_library().e8_mx4_decode_to_bf16(
+        cb.handle, _ptr(m.codes), _ptr(m.scales), 1 if m.batch is None else m.batch, m.rows, m.K,
+        _ptr(out), _stream(stream)), "e8_mx4_decode_to_bf16")
+    return out
+
+
+def e8_mx4_gemm(cb: Codebook, X, m: Mx4Matrix, Y=None, workspace=None, stream=None):
+    """Y bf16 [M, N] = X [M, K] (bf16, fp16 or fp32, encoded on the way) times m transposed."""
+    import torch
+    if X.dim() != 2 or X.shape[1] != m.K or m.batch is not None:
+        raise E8Error(E8_EINVAL, "e8_mx4_gemm")
+    M = X.shape[0]
+    ldx = _mx4_row_stride(cb, X, "e8_mx4_gemm")
+    lib = load_library()
+    Y = _mx4_out(Y, (M, m.rows), torch.bfloat16, X, stream, "e8_mx4_gemm")
+    ws = workspace if workspace is not None else _mx4_out(
+        None, (max(16, lib.e8_mx4_gemm_workspace_bytes(M, m.rows, m.K)),), torch.uint8, X, stream, "")
+    _mx4_check(cb, "e8_mx4_gemm", m.codes, m.scales, Y, ws)
+    _check(lib.e8_mx4_gemm(cb.handle, _ptr(X), _mx4_dtype(X), M, ldx, _ptr(m.codes), _ptr(m.scales),
+                           m.rows, m.K, _ptr(Y), _ptr(ws), ws.numel(), _stream(stream)),
+           "e8_mx4_gemm")
+    return Y
+
+
+def e8_mx4_gemm_codes(cb: Codebook, a: Mx4Matrix, m: Mx4Matrix, Y=None, workspace=None, stream=None):
+    """Y bf16 [M, N] = a [M, K] times m [N, K] transposed, both encoded."""
+    import torch
+    if a.K != m.K or a.batch is not None or m.batch is not None:
+        raise E8Error(E8_EINVAL, "e8_mx4_gemm_codes")
+    lib = load_library()
+    Y = _mx4_out(Y, (a.rows, m.rows), torch.bfloat16, a.codes, stream, "e8_mx4_gemm_codes")
+    ws = workspace if workspace is not None else _mx4_out(
+        None, (max(16, lib.e8_mx4_gemm_codes_workspace_bytes(a.rows, m.rows, m.K)),), torch.uint8,
+        a.codes, stream, "")
+    _mx4_check(cb, "e8_mx4_gemm_codes", a.codes, a.scales, m.codes, m.scales, Y, ws)
+    _check(lib.e8_mx4_gemm_codes(cb.handle, _ptr(a.codes), _ptr(a.scales), a.rows, _ptr(m.codes),
+                                 _ptr(m.scales), m.rows, m.K, _ptr(Y), _ptr(ws), ws.numel(),
+                                 _stream(stream)), "e8_mx4_gemm_codes")
+    return Y
+
+
+def e8_mx4_moe(cb: Codebook, X, router, w13: Mx4Matrix, w2: Mx4Matrix, topk: int,
+               renormalize: bool = True, Y=None, experts=None, probs=None, workspace=None,
+               stream=None):
+    """Y bf16 [T, H] of a mixture-of-experts layer for T <= 64 tokens.
+
+    X bf16 [T, H]; router bf16 [E, H]; w13: E matrices [2 I, H] whose even rows are
+    the gate's and odd rows the up-projection's; w2: E matrices [H, I].  experts
+    (int32 [T, topk]) and probs (fp32 [T, topk]) are filled when given."""
+    import torch
+    where = "e8_mx4_moe"
+    if X.dim() != 2 or router.dim() != 2 or X.dtype != torch.bfloat16 or \
+            router.dtype != torch.bfloat16 or w13.batch is None or w2.batch is None:
+        raise E8Error(E8_EINVAL, where)
+    (T, H), E, inner = X.shape, router.shape[0], w2.K
+    if (router.shape[1], w13.batch, w2.batch, w13.rows, w13.K, w2.rows) != \
+            (H, E, E, 2 * inner, H, H):
+        raise E8Error(E8_EINVAL, where)
+    lib = load_library()
+    for t, kind in ((experts, torch.int32), (probs, torch.float32)):
+        if t is not None and (tuple(t.shape) != (T, topk) or t.dtype != kind):
+            raise E8Error(E8_EINVAL, where)
+    Y = _mx4_out(Y, (T, H), torch.bfloat16, X, stream, where)
+    ws = workspace if workspace is not None else _mx4_out(
+        None, (max(16, lib.e8_mx4_moe_workspace_bytes(T, H, E, int(topk), inner)),), torch.uint8, X,
+        stream, "")
+    _mx4_check(cb, where, X, router, w13.codes, w13.scales, w2.codes, w2.scales, Y, experts, probs,
+               ws)
+    _check(lib.e8_mx4_moe(cb.handle, _ptr(X), T, H, _ptr(router), E, int(topk), int(bool(renormalize)),
+                          _ptr(w13.codes), _ptr(w13.scales), inner, _ptr(w2.codes), _ptr(w2.scales),
+                          _ptr(Y), _ptr(experts), _ptr(probs), _ptr(ws), ws.numel(),
+                          _stream(stream)), where)
+    return Y
+
+
+def e8_mx4_moe_pack(cb: Codebook, gate, up, down):
+    """Expert weights gate, up [E, I, H] and down [E, H, I] (bf16, fp16 or fp32, CUDA) ->
+    (w13, w2) of e8_mx4_moe: gate and up rows interleaved, then encoded."""
+    import torch
+    if gate.dim() != 3 or gate.shape != up.shape or \
+            tuple(down.shape) != (gate.shape[0], gate.shape[2], gate.shape[1]):
+        raise E8Error(E8_EINVAL, "e8_mx4_moe_pack")
+    both = torch.stack((gate, up), 2).flatten(1, 2)
+    return e8_mx4_encode(cb, both), e8_mx4_encode(cb, down.contiguous())

@@ -220,6 +220,32 @@ cudaError_t launch_ep_decode(const uint16_t* words, int64_t n_words, const uint3
                              const float* t, const uint16_t* tables, int64_t N, int64_t K,
                              uint16_t* out, uint32_t* status, int sm_count, cudaStream_t st);
 
+// Microscaled 4-bit form (e8_mx4.cu, e8_mx4_gemm.cu).  dtype: E8_DT_*.
+cudaError_t launch_mx4_encode(const void* X, int dtype, int64_t batch, int64_t rows, int64_t K,
+                              int64_t ldx, uint8_t* codes, uint8_t* scales, cudaStream_t st);
+cudaError_t launch_mx4_decode(const uint8_t* codes, const uint8_t* scales, int64_t batch,
+                              int64_t rows, int64_t K, uint16_t* out, cudaStream_t st);
+size_t mx4_gemm_workspace(int64_t M, int64_t N, int64_t K);
+cudaError_t launch_mx4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int64_t M,
+                            const uint8_t* w_codes, const uint8_t* w_scales, int64_t N, int64_t K,
+                            uint16_t* Y, void* ws, uint32_t* status, int sm_count,
+                            cudaStream_t st);
+
+// Mixture-of-experts layer for a few tokens (e8_moe.cu).
+struct MoeArgs {
+  const uint16_t* X;        // bf16 [T][H]
+  const uint16_t* router;   // bf16 [E][H]
+  const uint8_t *w13_codes, *w13_scales, *w2_codes, *w2_scales;
+  uint16_t* Y;              // bf16 [T][H]
+  int32_t* experts;         // [T][topk] or null
+  float* probs;             // [T][topk] or null
+  void* workspace;
+  int T, H, E, topk, renorm, I;
+  uint32_t* status;
+};
+size_t moe_workspace(int64_t T, int64_t H, int64_t E, int topk, int64_t I);
+cudaError_t launch_moe(const MoeArgs& a, int sm_count, cudaStream_t st);
+
 // Dense Y[M][N] fp32 = X[M][K] bf16 * W[N][K]^T bf16 on tcgen05.
 cudaError_t launch_dense_gemm(const uint16_t* X, int64_t M, const uint16_t* W, int64_t N,
                               int64_t K, float* Y, uint32_t* status, int sm_count,

@@ -1,0 +1,63 @@
+// Microscaled 4-bit form (blocks of 32 e2m1 values, one power-of-two scale):
+// layout rules and number helpers shared by its kernels.
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "e8_common.cuh"
+
+namespace e8 {
+namespace mx4 {
+
+// Bytes of one row of codes: 16 for each block of 32.
+__host__ __device__ __forceinline__ int64_t code_stride(int64_t K) { return (K + 31) / 32 * 16; }
+// Tiles of 128 columns in a row of scale tiles.
+__host__ __device__ __forceinline__ int64_t scale_tiles(int64_t K) { return (K + 127) / 128; }
+__host__ __device__ __forceinline__ int64_t scale_bytes(int64_t rows, int64_t K) {
+  return (rows + 127) / 128 * scale_tiles(K) * 512;
+}
+// Byte offset of the four scales of row `row` in column tile `kq`.
+__host__ __device__ __forceinline__ int64_t scale_at(int64_t row, int64_t kq, int64_t kqs) {
+  return ((row >> 7) * kqs + kq) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4;
+}
+
+// Scale byte of a block whose largest magnitude is `amax` (>= 0, maybe inf or
+// NaN): the exponent field less 2, clamped at 0; 255 when amax is not finite.
+__device__ __forceinline__ uint32_t scale_byte(float amax) {
+  const uint32_t e = __float_as_uint(amax) >> 23;
+  return e == 255u ? 255u : (e > 2u ? e - 2u : 0u);
+}
+// 2^-(byte - 127), a normal number for every byte the encoder computes (<= 252).
+__device__ __forceinline__ float inv_scale(uint32_t byte) {
+  return __uint_as_float((254u - byte) << 23);
+}
+// 2^(byte - 127): subnormal for byte 0, NaN for byte 255.
+__device__ __forceinline__ float scale_value(uint32_t byte) {
+  return byte == 0u ? __uint_as_float(0x00400000u)
+                    : (byte == 255u ? __uint_as_float(0x7FC00000u) : __uint_as_float(byte << 23));
+}
+
+// Eight floats -> eight e2m1 codes (element 0 in the low nibble), nearest even,
+// saturating.
+__device__ __forceinline__ uint32_t pack8(const float (&v)[8]) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}\n"
+      : "=r"(r)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  return r;
+}
+
+// Value of one code (low four bits of c) as fp32: the two exponent bits and the
+// mantissa bit at the top of fp32's fields read as value * 2^-126, exactly.
+__device__ __forceinline__ float code_value(uint32_t c) {
+  return __uint_as_float(((c & 8u) << 28) | ((c & 7u) << 22)) * 0x1p126f;
+}
+
+}  // namespace mx4
+}  // namespace e8

@@ -390,6 +390,97 @@ int e8_ep_gemm(const e8_codebook* cb, const uint16_t* X, int64_t M, const uint16
                int64_t n_words, const uint32_t* offsets, const float* t, const uint16_t* tables,
                int64_t N, int64_t K, float* Y, void* workspace, size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Microscaled 4-bit floating point (OCP Microscaling Formats 1.0, MXFP4): a
+ * second compressed form beside the E8 codes, without a transform.  Along K,
+ * every block of 32 values shares one power-of-two scale:
+ *   - a = max|x| over the block, E = clamp(floor(log2 a) - 2, -127, 125)
+ *     (E = -127 for a block of zeros), scale byte E + 127;
+ *   - code = x / 2^E rounded to nearest even onto the e2m1 values
+ *     {0, 0.5, 1, 1.5, 2, 3, 4, 6}, saturating at 6, with x's sign;
+ *   - a block with an infinity or a NaN gets scale byte 255, and all its values
+ *     read back as NaN (a product with it is NaN);
+ *   - a last block shorter than 32 is filled with zeros.
+ * Layout of one [rows][K] matrix:
+ *   - codes uint8 [rows][16 ceil(K / 32)]: value 2i in the low nibble of byte i;
+ *   - scales: tiles of 128 rows by 4 blocks (128 columns), 512 bytes each, the
+ *     ceil(K / 128) tiles of a row of tiles one after the other; inside a tile
+ *     row r, block b is byte 16 (r mod 32) + 4 (r / 32) + b.  Bytes of rows and
+ *     blocks outside the matrix are zero (a product reads the ones of blocks).
+ *     This is the order the tensor cores take scales in.
+ * A batch of matrices is stored matrix after matrix, each with its own tiles.
+ * The codebook handle selects the device and carries the status word.
+ * Code and scale buffers must be 16-byte (for e8_mx4_moe 32-byte) aligned. */
+#define E8_DT_BF16 0
+#define E8_DT_F16 1
+#define E8_DT_F32 2
+
+/* Bytes of the codes and of the scales of one [rows][K] matrix; -1 for an
+ * invalid shape (rows < 0, K < 1, rows or K above 2^31 - 1). */
+int64_t e8_mx4_code_bytes(int64_t rows, int64_t K);
+int64_t e8_mx4_scale_bytes(int64_t rows, int64_t K);
+
+/* Encoder: X [batch][rows][K] of type dtype (E8_DT_*), row stride ldx >= K
+ * elements, matrix stride rows * ldx -> codes and scales as above.  X needs
+ * only its element's alignment.  No workspace. */
+int e8_mx4_encode(const e8_codebook* cb, const void* X, int dtype, int64_t batch, int64_t rows,
+                  int64_t K, int64_t ldx, uint8_t* codes, uint8_t* scales, void* stream);
+
+/* Decoder: codes and scales -> out bf16 [batch][rows][K] (exact for every scale
+ * byte the encoder writes).  No workspace. */
+int e8_mx4_decode_to_bf16(const e8_codebook* cb, const uint8_t* codes, const uint8_t* scales,
+                          int64_t batch, int64_t rows, int64_t K, uint16_t* out, void* stream);
+
+/* Product of two encoded matrices: Y bf16 [M][N] = bf16_rne(sum_k A[m][k] W[n][k]),
+ * products exact, sums in fp32, for A [M][K] and W [N][K] in the form above.
+ * workspace: at least e8_mx4_gemm_codes_workspace_bytes(M, N, K) bytes, contents
+ * ignored; the K range of an output may be split, its partial sums are added in
+ * a fixed order (results do not vary from run to run). */
+int e8_mx4_gemm_codes(const e8_codebook* cb, const uint8_t* a_codes, const uint8_t* a_scales,
+                      int64_t M, const uint8_t* w_codes, const uint8_t* w_scales, int64_t N,
+                      int64_t K, uint16_t* Y, void* workspace, size_t ws_bytes, void* stream);
+
+/* The same for activations X [M][K] of type dtype, row stride ldx >= K elements,
+ * which are encoded into the workspace first (16-byte aligned or not).
+ * workspace: at least e8_mx4_gemm_workspace_bytes(M, N, K) bytes. */
+int e8_mx4_gemm(const e8_codebook* cb, const void* X, int dtype, int64_t M, int64_t ldx,
+                const uint8_t* w_codes, const uint8_t* w_scales, int64_t N, int64_t K,
+                uint16_t* Y, void* workspace, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of the two products (0 if the arguments are invalid or
+ * nothing is needed). */
+size_t e8_mx4_gemm_codes_workspace_bytes(int64_t M, int64_t N, int64_t K);
+size_t e8_mx4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
+/* A whole mixture-of-experts layer for a few tokens, weights in the form above,
+ * activations not quantised to 4 bits:
+ *   logits = X router^T, products exact and summed in 64 bits (the choice of
+ *     experts does not depend on how the sum is split);
+ *   the topk largest logits of each token, ties to the lowest expert, NaN last;
+ *   p = softmax over all experts, divided by its sum over the chosen ones when
+ *     renormalize is not 0;
+ *   h = silu(gate_e x) * (up_e x), Y = bf16_rne(sum over chosen e of p_e down_e h).
+ * X bf16 [T][H]; router bf16 [E][H]; w13: batch of E matrices [2 I][H], row 2i
+ * the gate's row i and row 2i + 1 the up-projection's; w2: batch of E matrices
+ * [H][I]; Y bf16 [T][H].  Optional outputs (NULL to skip): experts int32
+ * [T][topk], by falling logit, and probs fp32 [T][topk].
+ * X enters the products as two 8-bit floats that hold it exactly within 2^-17 of
+ * its block's largest value, h with 8 significant bits; all sums are fp32, added
+ * in a fixed order.  An expert that no token chose is not read.
+ * Shapes: 0 <= T <= E8_MOE_MAX_TOKENS, 1 <= topk <= min(E, E8_MOE_MAX_TOPK),
+ * E <= E8_MOE_MAX_EXPERTS, H and I positive multiples of 128, H <= 32768, I <= 65536.  workspace: at
+ * least e8_mx4_moe_workspace_bytes(...) bytes, contents ignored; it must not be
+ * used by other work until the stream passes this call. */
+#define E8_MOE_MAX_TOKENS 64
+#define E8_MOE_MAX_EXPERTS 512
+#define E8_MOE_MAX_TOPK 16
+int e8_mx4_moe(const e8_codebook* cb, const uint16_t* X, int64_t T, int64_t H,
+               const uint16_t* router, int64_t E, int topk, int renormalize,
+               const uint8_t* w13_codes, const uint8_t* w13_scales, int64_t I,
+               const uint8_t* w2_codes, const uint8_t* w2_scales, uint16_t* Y, int32_t* experts,
+               float* probs, void* workspace, size_t ws_bytes, void* stream);
+size_t e8_mx4_moe_workspace_bytes(int64_t T, int64_t H, int64_t E, int topk, int64_t I);
+
 /* Failure-detection check (diagnostic): launches one thread that waits on a
  * barrier nothing ever signals, gives up after wait_ms (1..5000) milliseconds
  * and sets the timeout bit of the codebook's status word, the same way every

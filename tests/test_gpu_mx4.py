@@ -1,0 +1,186 @@
+"""Microscaled 4-bit form on the GPU: codes, scales and values bit for bit against the
+oracle, products against binary64."""
+import numpy as np
+import pytest
+import torch
+
+import decode_gemm_e8_b200 as e8
+from oracle import mx4_oracle as mx
+from tests.gpu_util import dev
+
+pytestmark = pytest.mark.gpu
+
+DTYPES = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
+
+
+@pytest.fixture(scope="module")
+def cbk():
+    cb = e8.Codebook(0)
+    yield cb
+    cb.free()
+
+
+def _data(rows, K, dtype, seed, pad=0):
+    """[rows, K] slice of a wider device tensor, and its values in binary64."""
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(rows, K + pad, generator=g) * torch.exp(2 * torch.randn(rows, 1, generator=g))
+    if rows > 2:
+        x[1] = 0
+        x[2, : min(K, 40)] *= 2.0 ** -20
+    # halfway points of the grid, so that ties are met
+    x[0, : min(K, 8)] = torch.tensor([4.0, 0.25, 0.75, 1.25, 1.75, 2.5, 3.5, -5.0])[: min(K, 8)]
+    x = x.to(DTYPES[dtype]).to(dev())[:, :K]
+    return x, x.cpu().double().numpy()
+
+
+SHAPES = [(1, 1, 0), (1, 32, 0), (1, 4096, 0), (3, 31, 0), (5, 33, 3), (129, 255, 0), (128, 256, 8),
+          (37, 257, 0), (200, 1000, 24), (2, 16384, 0), (300, 264, 1)]
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("rows,K,pad", SHAPES)
+def test_encode_and_decode_are_exact(cbk, rows, K, pad, dtype):
+    x, v = _data(rows, K, dtype, rows * 7 + K, pad)
+    m = e8.e8_mx4_encode(cbk, x)
+    c, b = mx.quantise(v)
+    p, t = mx.pack(c, b)
+    assert np.array_equal(m.codes.cpu().numpy(), p)
+    assert np.array_equal(m.scales.cpu().numpy(), t)
+    out = e8.e8_mx4_decode_to_bf16(cbk, m)
+    assert np.array_equal(out.cpu().double().numpy(), mx.values(c, b, K))
+
+
+def test_encode_of_a_batch(cbk):
+    x = torch.randn(3, 130, 200, device=dev()).bfloat16()
+    m = e8.e8_mx4_encode(cbk, x)
+    for i in range(3):
+        one = e8.e8_mx4_encode(cbk, x[i])
+        assert torch.equal(one.codes, m.codes[i]) and torch.equal(one.scales, m.scales[i])
+    assert torch.equal(e8.e8_mx4_decode_to_bf16(cbk, m)[2],
+                       e8.e8_mx4_decode_to_bf16(cbk, one))
+    # matrices of one row that lie further apart
+    y = torch.randn(4, 2, 64, device=dev())[:, :1]
+    n = e8.e8_mx4_encode(cbk, y)
+    assert torch.equal(n.codes[3], e8.e8_mx4_encode(cbk, y[3]).codes)
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_extreme_values(cbk, dtype):
+    x = torch.zeros(8, 96)
+    x[0, 5] = float("inf")
+    x[1, 40] = float("nan")
+    x[2] = torch.finfo(DTYPES[dtype]).max
+    x[3] = torch.finfo(DTYPES[dtype]).smallest_normal
+    x[4, :50] = torch.finfo(DTYPES[dtype]).smallest_normal * torch.arange(50) / 16
+    x[5] = -0.0
+    x[6, 64:] = -float("inf")
+    x = x.to(DTYPES[dtype]).to(dev())
+    c, b = mx.quantise(x.cpu().double().numpy())
+    m = e8.e8_mx4_encode(cbk, x)
+    p, t = mx.pack(c, b)
+    assert np.array_equal(m.codes.cpu().numpy(), p) and np.array_equal(m.scales.cpu().numpy(), t)
+    out = e8.e8_mx4_decode_to_bf16(cbk, m).cpu().double().numpy()
+    assert np.array_equal(out, mx.values(c, b, 96), equal_nan=True)
+
+
+def _check_product(Y, a, w):
+    """bf16 rounding of the output: half a step, 2^-8 of the value; fp32 sums of K
+    exact products: K additions off by at most 2^-23 of the magnitudes' sum."""
+    ref, mag = a @ w.T, np.abs(a) @ np.abs(w).T
+    y = Y.cpu().double().numpy()
+    K = a.shape[1]
+    assert np.array_equal(np.isnan(y), np.isnan(ref))
+    fine = ~np.isnan(ref)
+    tol = 2.0 ** -8 * np.abs(ref) + K * 2.0 ** -23 * mag + 1e-37
+    assert (np.abs(y - ref)[fine] <= tol[fine]).all()
+    n = np.linalg.norm(ref[fine])
+    assert np.linalg.norm((y - ref)[fine]) <= 2.0 ** -8 * n + 1e-37
+
+
+PRODUCTS = [(1, 1, 1), (1, 128, 128), (1, 4096, 4096), (2, 130, 96), (7, 257, 160), (16, 384, 1024),
+            (17, 129, 2080), (33, 512, 4104), (64, 300, 65), (65, 256, 512), (100, 1000, 777),
+            (128, 128, 256), (129, 640, 300), (200, 513, 1056), (256, 256, 256), (257, 511, 513),
+            (300, 4099, 264), (333, 700, 4104), (512, 1024, 768), (1000, 520, 1000)]
+
+
+@pytest.mark.parametrize("M,N,K", PRODUCTS)
+def test_product(cbk, M, N, K):
+    dtype = ("bf16", "f16", "f32")[(M + N + K) % 3]
+    x, v = _data(M, K, dtype, M + N, pad=(M % 3) * 5)
+    w, wv = _data(N, K, "f32", K)
+    m = e8.e8_mx4_encode(cbk, w)
+    Y = e8.e8_mx4_gemm(cbk, x, m)
+    _check_product(Y, mx.roundtrip(v), mx.roundtrip(wv))
+    again = e8.e8_mx4_gemm_codes(cbk, e8.e8_mx4_encode(cbk, x), m)
+    assert torch.equal(Y, again)
+    assert e8.e8_sync_status(cbk) == e8.E8_OK
+
+
+def test_products_with_extreme_scales_and_nan(cbk):
+    x, _ = _data(40, 320, "f32", 1)
+    w, _ = _data(150, 320, "f32", 2)
+    x[3] *= 2.0 ** -100
+    x[4, 100] = float("nan")
+    x[5] *= 2.0 ** 60
+    w[7] *= 2.0 ** 50
+    w[9, 3] = float("inf")
+    w[11] = 0
+    Y = e8.e8_mx4_gemm(cbk, x, e8.e8_mx4_encode(cbk, w))
+    _check_product(Y, mx.roundtrip(x.cpu().numpy()), mx.roundtrip(w.cpu().numpy()))
+
+
+def test_rows_and_columns_stay_apart(cbk):
+    """A NaN row of X or W touches its own row or column of Y alone, and nothing behind Y
+    is written."""
+    M, N, K = 70, 200, 416
+    x, _ = _data(M, K, "bf16", 3)
+    w, _ = _data(N, K, "bf16", 4)
+    m = e8.e8_mx4_encode(cbk, w)
+    clean = e8.e8_mx4_gemm(cbk, x, m)
+    x2 = x.clone()
+    x2[11] = float("nan")
+    buf = torch.full((M + 4, N), 7.0, dtype=torch.bfloat16, device=dev())
+    e8.e8_mx4_gemm(cbk, x2, m, Y=buf[:M])
+    keep = torch.arange(M, device=dev()) != 11
+    assert torch.equal(buf[:M][keep], clean[keep]) and buf[11].isnan().all()
+    assert (buf[M:] == 7).all()
+
+
+def test_empty_and_refused(cbk):
+    w = e8.e8_mx4_encode(cbk, torch.randn(16, 64, device=dev()))
+    assert e8.e8_mx4_gemm(cbk, torch.empty(0, 64, device=dev()), w).shape == (0, 16)
+    none = e8.e8_mx4_encode(cbk, torch.empty(0, 64, device=dev()))
+    assert e8.e8_mx4_gemm(cbk, torch.randn(3, 64, device=dev()), none).shape == (3, 0)
+    x = torch.randn(3, 64, device=dev())
+    for bad in (lambda: e8.e8_mx4_encode(cbk, x.double()), lambda: e8.e8_mx4_encode(cbk, x.T),
+                lambda: e8.e8_mx4_gemm(cbk, x[:, :63], w), lambda: e8.e8_mx4_gemm(cbk, x.cpu(), w),
+                lambda: e8.e8_mx4_encode(cbk, x[:1].expand(3, 64)),
+                lambda: e8.e8_mx4_gemm(cbk, x, w, Y=torch.empty(3, 16, device=dev())),
+                lambda: e8.e8_mx4_gemm(cbk, x, w, workspace=torch.empty(16, dtype=torch.uint8, device=dev()))):
+        with pytest.raises(e8.E8Error):
+            bad()
+
+
+def test_streams_and_graph(cbk):
+    """Calls on another stream, and a captured call replayed on new inputs."""
+    x, _ = _data(20, 512, "bf16", 5)
+    w = e8.e8_mx4_encode(cbk, _data(300, 512, "f32", 6)[0])
+    want = e8.e8_mx4_gemm(cbk, x, w)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = e8.e8_mx4_gemm(cbk, x, w, stream=s)
+    s.synchronize()
+    assert torch.equal(got, want)
+    static = x.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        y = e8.e8_mx4_gemm(cbk, static, w)
+        z = e8.e8_mx4_decode_to_bf16(cbk, e8.e8_mx4_encode(cbk, y))
+    for seed in (8, 9):
+        static.copy_(_data(20, 512, "bf16", seed)[0])
+        g.replay()
+        torch.cuda.synchronize()
+        ref = e8.e8_mx4_gemm(cbk, static, w)
+        assert torch.equal(y, ref)
+        assert torch.equal(z, e8.e8_mx4_decode_to_bf16(cbk, e8.e8_mx4_encode(cbk, ref)))
