@@ -220,15 +220,18 @@ cudaError_t launch_ep_decode(const uint16_t* words, int64_t n_words, const uint3
                              const float* t, const uint16_t* tables, int64_t N, int64_t K,
                              uint16_t* out, uint32_t* status, int sm_count, cudaStream_t st);
 
-// Microscaled 4-bit form (e8_mx4.cu, e8_mx4_gemm.cu).  dtype: E8_DT_*.
+// Microscaled 4-bit form (e8_mx4.cu, e8_mx4_gemm.cu).  dtype: E8_DT_*; release:
+// the next kernel of the stream, launched programmatically, may start at once;
+// early: the weights may be read before the preceding kernel has ended.
 cudaError_t launch_mx4_encode(const void* X, int dtype, int64_t batch, int64_t rows, int64_t K,
-                              int64_t ldx, uint8_t* codes, uint8_t* scales, cudaStream_t st);
+                              int64_t ldx, uint8_t* codes, uint8_t* scales, int release,
+                              cudaStream_t st);
 cudaError_t launch_mx4_decode(const uint8_t* codes, const uint8_t* scales, int64_t batch,
                               int64_t rows, int64_t K, uint16_t* out, cudaStream_t st);
 size_t mx4_gemm_workspace(int64_t M, int64_t N, int64_t K);
 cudaError_t launch_mx4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int64_t M,
                             const uint8_t* w_codes, const uint8_t* w_scales, int64_t N, int64_t K,
-                            uint16_t* Y, void* ws, uint32_t* status, int sm_count,
+                            uint16_t* Y, void* ws, uint32_t* status, int sm_count, int early,
                             cudaStream_t st);
 
 // Mixture-of-experts layer for a few tokens (e8_moe.cu).

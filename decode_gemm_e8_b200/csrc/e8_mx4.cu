@@ -63,7 +63,8 @@ template <int DT, bool VEC>
 __global__ void __launch_bounds__(kThreads)
     k_mx4_encode(const typename Elem<DT>::T* __restrict__ X, int64_t rows, int64_t K, int64_t ldx,
                  uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, int64_t jobs,
-                 int64_t chunks, int64_t row_groups) {
+                 int64_t chunks, int64_t row_groups, int release) {
+  if (release) grid_dep_launch();
   const int lane = threadIdx.x & 31;
   const int64_t cs = code_stride(K), kqs = scale_tiles(K), sb = scale_bytes(rows, K);
   const int64_t job = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
@@ -180,7 +181,7 @@ static bool plan(int64_t batch, int64_t rows, int64_t K, bool pad_rows, Jobs* j)
 
 template <int DT>
 static cudaError_t encode_as(const void* X, int64_t batch, int64_t rows, int64_t K, int64_t ldx,
-                             uint8_t* codes, uint8_t* scales, cudaStream_t st) {
+                             uint8_t* codes, uint8_t* scales, int release, cudaStream_t st) {
   using T = typename Elem<DT>::T;
   Jobs j;
   if (!plan(batch, rows, K, true, &j)) return cudaErrorInvalidValue;
@@ -189,20 +190,21 @@ static cudaError_t encode_as(const void* X, int64_t batch, int64_t rows, int64_t
   const bool vec = aligned16(X) && (ldx * (int64_t)sizeof(T)) % 16 == 0;
   if (vec)
     k_mx4_encode<DT, true><<<j.grid, kThreads, 0, st>>>(x, rows, K, ldx, codes, scales, j.jobs,
-                                                        j.chunks, j.row_groups);
+                                                        j.chunks, j.row_groups, release);
   else
     k_mx4_encode<DT, false><<<j.grid, kThreads, 0, st>>>(x, rows, K, ldx, codes, scales, j.jobs,
-                                                         j.chunks, j.row_groups);
+                                                         j.chunks, j.row_groups, release);
   return cudaGetLastError();
 }
 
 }  // namespace mx4
 
 cudaError_t launch_mx4_encode(const void* X, int dtype, int64_t batch, int64_t rows, int64_t K,
-                              int64_t ldx, uint8_t* codes, uint8_t* scales, cudaStream_t st) {
-  if (dtype == 0) return mx4::encode_as<0>(X, batch, rows, K, ldx, codes, scales, st);
-  if (dtype == 1) return mx4::encode_as<1>(X, batch, rows, K, ldx, codes, scales, st);
-  return mx4::encode_as<2>(X, batch, rows, K, ldx, codes, scales, st);
+                              int64_t ldx, uint8_t* codes, uint8_t* scales, int release,
+                              cudaStream_t st) {
+  if (dtype == 0) return mx4::encode_as<0>(X, batch, rows, K, ldx, codes, scales, release, st);
+  if (dtype == 1) return mx4::encode_as<1>(X, batch, rows, K, ldx, codes, scales, release, st);
+  return mx4::encode_as<2>(X, batch, rows, K, ldx, codes, scales, release, st);
 }
 
 cudaError_t launch_mx4_decode(const uint8_t* codes, const uint8_t* scales, int64_t batch,

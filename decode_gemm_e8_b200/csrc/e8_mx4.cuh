@@ -59,5 +59,34 @@ __device__ __forceinline__ float code_value(uint32_t c) {
   return __uint_as_float(((c & 8u) << 28) | ((c & 7u) << 22)) * 0x1p126f;
 }
 
+// ------------------------------------------------------- tensor cores ---
+// Instruction descriptor of tcgen05.mma.kind::mxf4: e2m1 A and B (both K-major),
+// ue8m0 scales, fp32 accumulator, K = 64.  sf: which pair of the four scale
+// bytes of a 32-bit tensor-memory column this step takes (0 or 2), for A and B.
+__host__ __device__ constexpr uint32_t idesc_mxf4(uint32_t M, uint32_t N, uint32_t sf) {
+  return (sf << 4) | (1u << 7) | (1u << 10) | ((N >> 3) << 17) | (1u << 23) | ((M >> 7) << 27) |
+         (sf << 29);
+}
+
+// D[tmem] (+)= (A[smem] scaled) * (B[smem] scaled)^T, scales in tensor memory.
+__device__ __forceinline__ void mma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                         uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;"
+      "\n\t}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+
+// One 512-byte scale tile (32 lanes of 16 bytes) into four columns of tensor
+// memory, repeated in all four lane quarters.
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t smem) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr),
+               "l"(smem_desc(smem, 128, 128, 0))
+               : "memory");
+}
+
 }  // namespace mx4
 }  // namespace e8

@@ -52,7 +52,8 @@ int e8_mx4_encode(const e8_codebook* cb, const void* X, int dtype, int64_t batch
   const int rc = check_device(cb);
   if (rc != E8_OK) return rc;
   return cuda_status(
-      e8::launch_mx4_encode(X, dtype, batch, rows, K, ldx, codes, scales, (cudaStream_t)stream));
+      e8::launch_mx4_encode(X, dtype, batch, rows, K, ldx, codes, scales, 0,
+                            (cudaStream_t)stream));
 }
 
 int e8_mx4_decode_to_bf16(const e8_codebook* cb, const uint8_t* codes, const uint8_t* scales,
@@ -92,7 +93,7 @@ int e8_mx4_gemm_codes(const e8_codebook* cb, const uint8_t* a_codes, const uint8
   const int rc = check_device(cb);
   if (rc != E8_OK) return rc;
   return cuda_status(e8::launch_mx4_gemm(a_codes, a_scales, M, w_codes, w_scales, N, K, Y,
-                                         workspace, cb->status, cb->sm_count,
+                                         workspace, cb->status, cb->sm_count, 0,
                                          (cudaStream_t)stream));
 }
 
@@ -114,10 +115,10 @@ int e8_mx4_gemm(const e8_codebook* cb, const void* X, int dtype, int64_t M, int6
   uint8_t* scales = codes + round256((size_t)e8_mx4_code_bytes(M, K));
   uint8_t* rest = scales + round256((size_t)e8_mx4_scale_bytes(M, K));
   cudaStream_t st = (cudaStream_t)stream;
-  if (e8::launch_mx4_encode(X, dtype, 1, M, K, ldx, codes, scales, st) != cudaSuccess)
+  if (e8::launch_mx4_encode(X, dtype, 1, M, K, ldx, codes, scales, 1, st) != cudaSuccess)
     return E8_ECUDA;
   return cuda_status(e8::launch_mx4_gemm(codes, scales, M, w_codes, w_scales, N, K, Y, rest,
-                                         cb->status, cb->sm_count, st));
+                                         cb->status, cb->sm_count, 1, st));
 }
 
 static bool moe_shape(int64_t T, int64_t H, int64_t E, int topk, int64_t I) {

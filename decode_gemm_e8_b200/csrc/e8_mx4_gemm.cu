@@ -1,73 +1,281 @@
-// Product of two matrices in the microscaled 4-bit form.
+// Product of two matrices in the microscaled 4-bit form, on the tensor cores'
+// own block-scaled 4-bit path (tcgen05.mma.kind::mxf4): codes and scales go from
+// HBM to the tensor cores as they are stored, nothing is decoded.
 //
-// Y[m][n] = bf16(sum_k A[m][k] W[n][k]); a product of two e2m1 values and two
-// powers of two is exact in fp32, the sums are fp32.
+// Y[m][n] = bf16(sum_k A[m][k] W[n][k]).  A product of two e2m1 values and two
+// powers of two is exact in fp32; the accumulator is fp32; the one rounding to
+// fewer bits is that of Y.
 #include "e8_internal.h"
 #include "e8_mx4.cuh"
+#include "e8_tmap.h"
 
 namespace e8 {
 namespace mx4 {
 
-// 64 x 64 outputs a CTA, 4 x 4 a thread, one block of 32 columns at a time.
-__global__ void __launch_bounds__(256)
-    k_mx4_gemm(const uint8_t* __restrict__ A, const uint8_t* __restrict__ As, int64_t M,
-               const uint8_t* __restrict__ W, const uint8_t* __restrict__ Ws, int64_t N, int64_t K,
-               uint16_t* __restrict__ Y) {
-  __shared__ float sa[32][65], sw[32][65];
-  const int64_t cs = code_stride(K), kqs = scale_tiles(K);
-  const int64_t m0 = (int64_t)blockIdx.y * 64, n0 = (int64_t)blockIdx.x * 64;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int lr = threadIdx.x >> 2, lq = threadIdx.x & 3;   // row, 8-value quarter of the block
-  float acc[4][4] = {};
-  for (int64_t b = 0; b < (K + 31) / 32; ++b) {
-#pragma unroll
-    for (int side = 0; side < 2; ++side) {
-      const int64_t row = (side ? n0 : m0) + lr, rows = side ? N : M;
-      uint32_t code = 0, byte = 0;
-      if (row < rows) {
-        code = *reinterpret_cast<const uint32_t*>((side ? W : A) + row * cs + b * 16 + lq * 4);
-        byte = (side ? Ws : As)[scale_at(row, b >> 2, kqs) + (b & 3)];
-      }
-      const float s = scale_value(byte);
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        (side ? sw : sa)[lq * 8 + i][lr] = code_value(code >> (4 * i)) * s;
+// ------------------------------------------------------------ few tokens ---
+// Swapped operands: 128 rows of W are the MMA's M side, bn tokens its N side, so
+// that a single token costs one narrow MMA and the weights are read once.  The
+// K range is split over a cluster of `splits` CTAs when there are fewer row tiles
+// than SMs; every CTA leaves its partial tile in its own shared memory and each
+// then adds up, in rank order, the columns it was given (distributed shared
+// memory), so results do not depend on timing.
+//   warp 0     TMA producer: codes of W (128 x 256 K, 16 KB) and of the tokens
+//              (128-byte swizzle), scale tiles by plain bulk copies
+//   warp 1     tensor-memory allocation; one thread copies the stage's scales to
+//              tensor memory (a slot of its own for each stage, so that no copy
+//              meets an MMA that still reads) and issues the MMAs
+//   warps 2-5  epilogue
+constexpr int kStreamThreads = 192;
+constexpr int kStreamRows = 128;
+constexpr int kBK = 256;               // K of a stage: 128 bytes of codes
+constexpr int kCodeTile = 128 * 128;   // bytes of 128 rows
+constexpr int kMaxStages = 8;
+constexpr int kSfCol = 256;            // first tensor-memory column of the scales
+constexpr int kStreamSmem = 225 * 1024;
+
+struct StreamArgs {
+  const uint8_t *w_scales, *a_scales;
+  uint16_t* Y;
+  int M, N, K;
+  int bn, stages, splits;
+  int early;   // the weights may be read before the preceding kernel has ended
+  uint32_t* status;
+};
+
+__host__ __device__ __forceinline__ int stream_stage_bytes(int bn) {
+  return kCodeTile + bn * 128 + 1024 + 1024 * ((bn + 127) / 128);
+}
+
+__global__ void __launch_bounds__(kStreamThreads, 1)
+    k_mx4_stream(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA,
+                 const __grid_constant__ StreamArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  __shared__ uint64_t full[kMaxStages], empty[kMaxStages], done;
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile uint32_t abort_flag;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int S = a.splits, rank = (int)blockIdx.x % S;
+  const int n0 = (int)blockIdx.x / S * kStreamRows, m0 = (int)blockIdx.y * a.bn;
+  const int nbt = (a.bn + 127) / 128;
+  const int stage_bytes = stream_stage_bytes(a.bn);
+  const int kblocks = (a.K + kBK - 1) / kBK, kqs = (int)scale_tiles(a.K);
+  const int kb0 = (int)((int64_t)kblocks * rank / S);
+  const int nkb = (int)((int64_t)kblocks * (rank + 1) / S) - kb0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < a.stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
     }
-    __syncthreads();
-#pragma unroll 8
-    for (int k = 0; k < 32; ++k) {
-      float a[4], w[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        a[i] = sa[k][ty * 4 + i];
-        w[i] = sw[k][tx * 4 + i];
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], w[j], acc[i][j]);
-    }
-    __syncthreads();
+    mbar_init(&done, 1);
+    abort_flag = 0u;
+    fence_mbar_init();
   }
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int64_t m = m0 + ty * 4 + i, n = n0 + tx * 4 + j;
-      if (m < M && n < N) Y[m * N + n] = (uint16_t)(pack_bf16x2(acc[i][j], 0.0f) & 0xFFFFu);
+  if (warp == 1) {
+    tmem_alloc(&tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  if (!a.early) grid_dep_wait();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      tma_prefetch_desc(&tmW);
+      tma_prefetch_desc(&tmA);
+      // scale tiles of a stage: both 128-column tiles, or the last one alone
+      auto sf_bytes = [&](int kb) { return (uint32_t)min(2, kqs - 2 * kb) * 512u; };
+      auto tok_tiles = [&]() { return min(nbt, (a.M - m0 + 127) / 128); };
+      auto weights = [&](int i, int s) {
+        const int kb = kb0 + i;
+        uint8_t* st = smem + s * stage_bytes;
+        const uint32_t sf = sf_bytes(kb);
+        mbar_arrive_expect_tx(&full[s], (uint32_t)(kCodeTile + a.bn * 128) +
+                                            sf * (1u + (uint32_t)tok_tiles()));
+        tma_load_2d(st, &tmW, &full[s], kb * 128, n0);
+        bulk_load(st + kCodeTile + a.bn * 128,
+                  a.w_scales + ((int64_t)(n0 >> 7) * kqs + 2 * kb) * 512, sf, &full[s]);
+      };
+      auto tokens = [&](int i, int s) {
+        const int kb = kb0 + i;
+        uint8_t* st = smem + s * stage_bytes;
+        tma_load_2d(st + kCodeTile, &tmA, &full[s], kb * 128, m0);
+        for (int t = 0; t < tok_tiles(); ++t)
+          bulk_load(st + kCodeTile + a.bn * 128 + 1024 + t * 1024,
+                    a.a_scales + ((int64_t)((m0 >> 7) + t) * kqs + 2 * kb) * 512, sf_bytes(kb),
+                    &full[s]);
+      };
+      const int head = min(nkb, a.stages);
+      for (int i = 0; i < head; ++i) weights(i, i);
+      if (a.early) grid_dep_wait();
+      for (int i = 0; i < head; ++i) tokens(i, i);
+      int i = head;
+      for (; i < nkb; ++i) {
+        const int s = i % a.stages;
+        if (!mbar_wait_bounded(&empty[s], (uint32_t)(i / a.stages - 1) & 1u, &abort_flag, a.status,
+                               kDevTimeoutEmpty))
+          break;
+        weights(i, s);
+        tokens(i, s);
+      }
+      if (abort_flag) {
+        // copies in flight may still land: give them time before the CTA exits
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 1000000ull) {
+        }
+      }
     }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      for (int i = 0; i < nkb; ++i) {
+        const int s = i % a.stages;
+        if (!mbar_wait_bounded(&full[s], (uint32_t)(i / a.stages) & 1u, &abort_flag, a.status,
+                               kDevTimeoutFull))
+          break;
+        tc_fence_after();
+        const uint32_t w = smem_u32(smem + s * stage_bytes), t = w + kCodeTile;
+        const uint32_t sf = t + (uint32_t)a.bn * 128u;
+        const uint32_t sfa = tmem + kSfCol + (uint32_t)(s * (8 + 8 * nbt)), sfb = sfa + 8;
+        const int steps = min(4, (a.K - (kb0 + i) * kBK + 63) / 64);   // of 64 columns
+        for (int q = 0; q < (steps + 1) / 2; ++q) {
+          copy_scales(sfa + q * 4, sf + q * 512);
+          for (int b = 0; b < nbt; ++b)
+            copy_scales(sfb + (q * nbt + b) * 4, sf + 1024 + b * 1024 + q * 512);
+        }
+        for (int j = 0; j < steps; ++j)
+          mma_mxf4(tmem, smem_desc(w + j * 32, 16, 1024, 2), smem_desc(t + j * 32, 16, 1024, 2),
+                   idesc_mxf4(128, (uint32_t)a.bn, (uint32_t)(j & 1) * 2u), sfa + (j >> 1) * 4,
+                   sfb + (j >> 1) * 4 * nbt, (i > 0 || j > 0) ? 1u : 0u);
+        mma_commit(&empty[s]);
+      }
+      mma_commit(&done);   // also after a wait that gave up: nothing may be in flight at the end
+    }
+  }
+  __syncwarp();
+  // every warp: all MMAs of this CTA have finished
+  const bool ok = mbar_wait_bounded(&done, 0, &abort_flag, a.status, kDevTimeoutMma);
+  __syncwarp();
+  tc_fence_after();
+  const int cols = min(a.bn, a.M - m0);
+  if (S == 1) {
+    if (warp >= 2 && ok) {
+      const int quarter = warp & 3, n = n0 + quarter * 32 + lane;
+      for (int c = 0; c < cols; c += 16) {
+        uint32_t r[16];
+        tmem_ld16(tmem + (uint32_t)c + ((uint32_t)(quarter * 32) << 16), r);
+        tmem_ld_wait();
+        if (n < a.N) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (c + j < cols)
+              a.Y[(size_t)(m0 + c + j) * a.N + n] =
+                  (uint16_t)(pack_bf16x2(__uint_as_float(r[j]), 0.0f) & 0xFFFFu);
+        }
+      }
+    }
+  } else {
+    float* part = reinterpret_cast<float*>(smem);   // [column][128], the ring is free
+    if (warp >= 2) {
+      const int quarter = warp & 3;
+      for (int c = 0; c < cols; c += 16) {
+        uint32_t r[16];
+        tmem_ld16(tmem + (uint32_t)c + ((uint32_t)(quarter * 32) << 16), r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          if (c + j < cols) part[(c + j) * 128 + quarter * 32 + lane] = __uint_as_float(r[j]);
+      }
+    }
+    cluster_arrive();
+    cluster_wait();
+    const int row = (int)threadIdx.x;
+    if (row < kStreamRows && n0 + row < a.N) {
+      for (int c = rank; c < cols; c += S) {
+        const uint32_t at = smem_u32(part + c * 128 + row);
+        float y = ld_shared_cluster_f32(mapa_shared(at, 0));
+        for (int p = 1; p < S; ++p) y += ld_shared_cluster_f32(mapa_shared(at, (uint32_t)p));
+        a.Y[(size_t)(m0 + c) * a.N + n0 + row] = (uint16_t)(pack_bf16x2(y, 0.0f) & 0xFFFFu);
+      }
+    }
+    __syncwarp();
+    cluster_arrive();   // no CTA leaves while another reads its shared memory
+    cluster_wait();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+static cudaError_t launch_stream(const uint8_t* a_codes, const uint8_t* a_scales, int64_t M,
+                                 const uint8_t* w_codes, const uint8_t* w_scales, int64_t N,
+                                 int64_t K, uint16_t* Y, uint32_t* status, int sm_count, int early,
+                                 cudaStream_t st) {
+  StreamArgs a;
+  a.w_scales = w_scales;
+  a.a_scales = a_scales;
+  a.Y = Y;
+  a.M = (int)M;
+  a.N = (int)N;
+  a.K = (int)K;
+  // one token tile up to 256 tokens; more of them start on 256, where scale tiles do
+  a.bn = M >= 256 ? 256 : (int)((M + 15) / 16 * 16);
+  a.stages = kStreamSmem / stream_stage_bytes(a.bn);
+  if (a.stages > kMaxStages) a.stages = kMaxStages;
+  a.early = early;
+  a.status = status;
+  const int64_t tiles_n = (N + kStreamRows - 1) / kStreamRows, tiles_m = (M + a.bn - 1) / a.bn;
+  const int kblocks = (int)((K + kBK - 1) / kBK);
+  int S = 1;
+  while (S < 8 && 2 * S <= kblocks && tiles_n * tiles_m * 2 * S <= sm_count) S *= 2;
+  a.splits = S;
+  if (tiles_m > 65535 || tiles_n * S > INT32_MAX) return cudaErrorInvalidValue;
+  const int64_t cs = code_stride(K);
+  CUtensorMap tw, ta;
+  if (!make_tmap_2d(&tw, w_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)N, (uint64_t)cs, 128,
+                    128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_tmap_2d(&ta, a_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)M, (uint64_t)cs,
+                    (uint32_t)a.bn, 128, CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  cudaError_t e = ensure_smem_limit(k_mx4_stream, kMaxDynSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles_n * S), (unsigned)tiles_m);
+  cfg.blockDim = dim3(kStreamThreads);
+  cfg.dynamicSmemBytes = 1024 + (size_t)a.stages * stream_stage_bytes(a.bn);
+  // room for the partial tile of a split product
+  const size_t part = 1024 + (size_t)a.bn * 512;
+  if (S > 1 && cfg.dynamicSmemBytes < part) cfg.dynamicSmemBytes = part;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)S;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = early ? 2 : 1;
+  e = cudaLaunchKernelEx(&cfg, k_mx4_stream, tw, ta, a);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace mx4
 
 cudaError_t launch_mx4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int64_t M,
                             const uint8_t* w_codes, const uint8_t* w_scales, int64_t N, int64_t K,
-                            uint16_t* Y, void* ws, uint32_t* status, int sm_count,
+                            uint16_t* Y, void* ws, uint32_t* status, int sm_count, int early,
                             cudaStream_t st) {
-  (void)ws; (void)status; (void)sm_count;
-  const int64_t gy = (M + 63) / 64;
-  if (gy > 65535) return cudaErrorInvalidValue;
-  mx4::k_mx4_gemm<<<dim3((unsigned)((N + 63) / 64), (unsigned)gy), 256, 0, st>>>(
-      a_codes, a_scales, M, w_codes, w_scales, N, K, Y);
-  return cudaGetLastError();
+  (void)ws;
+  return mx4::launch_stream(a_codes, a_scales, M, w_codes, w_scales, N, K, Y, status, sm_count,
+                            early, st);
 }
 
 size_t mx4_gemm_workspace(int64_t M, int64_t N, int64_t K) {
