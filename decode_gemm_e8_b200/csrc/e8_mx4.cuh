@@ -80,6 +80,24 @@ __device__ __forceinline__ void mma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint6
       : "memory");
 }
 
+// The same for kind::mxf8f6f4 with e2m1 A (each 16 values in 16 bytes of shared
+// memory, packed in the first 8) and e4m3 B, K = 32; sf: the byte of the scale
+// columns this step takes (0..3).
+__host__ __device__ constexpr uint32_t idesc_mxf4_f8(uint32_t M, uint32_t N, uint32_t sf) {
+  return (sf << 4) | (5u << 7) | (0u << 10) | ((N >> 3) << 17) | (1u << 23) | ((M >> 7) << 27) |
+         (sf << 29);
+}
+__device__ __forceinline__ void mma_mxf8f6f4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                             uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X"
+      " [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+
 // One 512-byte scale tile (32 lanes of 16 bytes) into four columns of tensor
 // memory, repeated in all four lane quarters.
 __device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t smem) {
