@@ -260,11 +260,11 @@ __global__ void __launch_bounds__(1024)
 }
 
 // ---------------------------------------------------------------- products ---
-constexpr int kThreads = 192;
+constexpr int kThreads = 224;
 constexpr int kRows = 128;                 // rows of a unit
 constexpr int kBK = 128;                   // K of a stage
 constexpr int kWBytes = kRows * kBK;       // 16 values in 16 bytes, 8 of them used
-constexpr int kMaxStages = 10;
+constexpr int kMaxStages = 5;                // of 2 kBK columns: one barrier round for 16 KB of weights
 constexpr int kConstCol = 256, kSfCol = 264;   // tensor-memory columns of the scales
 constexpr int kRingBytes = 212 * 1024;
 
@@ -328,11 +328,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ volatile uint32_t abort_flag;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int stage_bytes = kWBytes + g.b_rows * kBK + 1024;
+  const int stage_bytes = 2 * (kWBytes + g.b_rows * kBK + 1024);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < g.stages; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], 2);   // both producers
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(&tmem_slot, 512);
     tmem_relinquish();
   }
-  if (UP && threadIdx.x >= 64) {
+  if (UP && threadIdx.x >= 64 && threadIdx.x < 192) {
     // scales of the activations: 1 for hi rows (even), 2^-4 for lo rows
     reinterpret_cast<uint32_t*>(const_sf)[threadIdx.x - 64] =
         ((threadIdx.x - 64) / 4) & 1 ? 0x7B7B7B7Bu : 0x7F7F7F7Fu;
@@ -372,107 +372,141 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   const int units = nact * g.tiles * g.splits;
 
+  const uint32_t ring = smem_u32(smem), b_bytes = (uint32_t)(g.b_rows * 128);
+  const int kqs = g.K / 128;
   if (warp == 0) {
     if (lane == 0) {
+      // codes and scales of the weights; they do not depend on the preceding kernel
       tma_prefetch_desc(&tmW);
-      tma_prefetch_desc(&tmB);
-    }
-    const int rows = g.tiles * kRows, kqs = g.K / kBK;
-    auto weights = [&](const Unit& u, int k, int s) {
-      if (lane == 0) {
-        uint8_t* st = smem + s * stage_bytes;
-        const uint32_t bytes = UP ? (uint32_t)u.n * 256u : (uint32_t)(u.n + 7) / 8 * 2048u + 512u;
-        // the tensor map unpacks: its bytes are counted as they lie in memory
-        mbar_arrive_expect_tx(&full[s], kWBytes / 2 + 512u + bytes);
-        const int row = u.expert * rows + u.tile * kRows;
-        tma_load_2d(st, &tmW, &full[s], (u.k0 + k) * kBK, row);
-        bulk_load(st + kWBytes + g.b_rows * kBK,
-                  g.w_scales + ((int64_t)(row >> 7) * kqs + u.k0 + k) * 512, 512, &full[s]);
-      }
-      __syncwarp();
-    };
-    auto tokens = [&](const Unit& u, int k, int s) {
-      uint8_t* b = smem + s * stage_bytes + kWBytes;
-      if (UP) {
-        for (int j = lane; j < u.n; j += 32)
-          tma_load_2d(b + j * 256, &tmB, &full[s], (u.k0 + k) * kBK,
-                      lists.slot[u.off + j] / g.topk * 2);
-      } else {
-        if (lane < (u.n + 7) / 8)
-          tma_load_2d(b + lane * 2048, &tmB, &full[s], (u.k0 + k) * kBK, 2 * u.off + lane * 16);
-        if (lane == 0)
-          bulk_load(b + g.b_rows * kBK + 512,
-                    g.h_scales + ((int64_t)u.a * kqs + u.k0 + k) * 512, 512, &full[s]);
-      }
-      __syncwarp();
-    };
-    // the first fills: weights before the activations are ready
-    int fills = 0;
-    if (!UP) {
-      for (int i = blockIdx.x; i < units && fills < g.stages; i += gridDim.x) {
-        const Unit u = unit_at(g, lists, i);
-        for (int k = 0; k < u.nk && fills < g.stages; ++k) weights(u, k, fills++);
-      }
-      grid_dep_wait();
-    }
-    int fill = 0;
-    for (int i = blockIdx.x; i < units; i += gridDim.x) {
-      const Unit u = unit_at(g, lists, i);
+      uint32_t st = ring, ph = 1;
+      int s = 0;
       bool ok = true;
-      for (int k = 0; k < u.nk; ++k, ++fill) {
-        const int s = fill % g.stages;
-        if (fill >= g.stages &&
-            !warp_wait(&empty[s], (uint32_t)(fill / g.stages - 1) & 1u, &abort_flag, g.status,
-                       kDevTimeoutEmpty)) {
-          ok = false;
-          break;
+      for (int i = blockIdx.x; i < units && ok; i += gridDim.x) {
+        const Unit u = unit_at(g, lists, i);
+        const int row = (u.expert * g.tiles + u.tile) * kRows;
+        const uint8_t* sf = g.w_scales + ((int64_t)(row >> 7) * kqs + u.k0) * 512;
+        int x = u.k0 * 128;
+        for (int k = u.nk; k > 0; k -= 2) {
+          if (!mbar_wait_lazy(&empty[s], ph, &abort_flag, g.status, kDevTimeoutEmpty)) {
+            ok = false;
+            break;
+          }
+          // the tensor map unpacks: its bytes are counted as they lie in memory
+          const uint32_t half = k > 1 ? 2u : 1u;
+          mbar_arrive_expect_tx(&full[s], half * (kWBytes / 2 + 512u));
+          load_2d(st, &tmW, &full[s], x, row);
+          if (k > 1) load_2d(st + kWBytes, &tmW, &full[s], x + 128, row);
+          load_bulk(st + 2u * (kWBytes + b_bytes), sf, half * 512u, &full[s]);
+          x += 256;
+          sf += 1024;
+          st += (uint32_t)stage_bytes;
+          if (++s == g.stages) {
+            s = 0;
+            ph ^= 1u;
+            st = ring;
+          }
         }
-        if (fill >= fills) weights(u, k, s);
-        tokens(u, k, s);
       }
-      if (!ok) break;
     }
-    if (abort_flag) {
-      // copies in flight may still land: give them time before the CTA exits
-      const uint64_t t0 = global_timer_ns();
-      while (global_timer_ns() - t0 < 1000000ull) {
+  } else if (warp == 6) {
+    // the tokens' rows: two (hi and lo) a copy in the up product, where tokens lie in
+    // order of the batch; sixteen a copy in the down product, sorted by expert
+    if (lane == 0) tma_prefetch_desc(&tmB);
+    if (!UP) grid_dep_wait();
+    uint32_t st = ring + 2u * kWBytes, ph = 1;
+    int s = 0;
+    bool ok = true;
+    for (int i = blockIdx.x; i < units && ok; i += gridDim.x) {
+      const Unit u = unit_at(g, lists, i);
+      const int copies = UP ? u.n : (u.n + 7) / 8;
+      int row0 = 0, row1 = 0;
+      if (UP) {
+        if (lane < u.n) row0 = lists.slot[u.off + lane] / g.topk * 2;
+        if (lane + 32 < u.n) row1 = lists.slot[u.off + lane + 32] / g.topk * 2;
+      } else {
+        row0 = 2 * u.off + lane * 16;
+      }
+      const uint32_t bytes = UP ? (uint32_t)copies * 256u : (uint32_t)copies * 2048u + 512u;
+      const uint32_t to = (uint32_t)lane * (UP ? 256u : 2048u);
+      const uint8_t* sf = g.h_scales + ((int64_t)u.a * kqs + u.k0) * 512;
+      int x = u.k0 * 128;
+      for (int k = u.nk; k > 0; k -= 2) {
+        ok = __all_sync(0xFFFFFFFFu,
+                        mbar_wait_lazy(&empty[s], ph, &abort_flag, g.status, kDevTimeoutEmpty));
+        if (!ok) break;
+        const uint32_t half = k > 1 ? 2u : 1u;
+        if (lane == 0) mbar_arrive_expect_tx(&full[s], half * bytes);
+        __syncwarp();
+        for (uint32_t h = 0; h < half; ++h) {
+          if (lane < copies) load_2d(st + h * b_bytes + to, &tmB, &full[s], x + 128 * (int)h, row0);
+          if (UP && lane + 32 < copies)
+            load_2d(st + h * b_bytes + to + 32u * 256u, &tmB, &full[s], x + 128 * (int)h, row1);
+        }
+        if (!UP && lane == 0) load_bulk(st + 2u * b_bytes + 1024u, sf, half * 512u, &full[s]);
+        x += 256;
+        sf += 1024;
+        st += (uint32_t)stage_bytes;
+        if (++s == g.stages) {
+          s = 0;
+          ph ^= 1u;
+          st = ring + 2u * kWBytes;
+        }
       }
     }
   } else if (warp == 1) {
     if (lane == 0) {
-      if (UP) mx4::copy_scales(tmem + kConstCol, smem_u32(const_sf));
-      int fill = 0, local = 0;
+      if (UP) mx4::copy_scales(tmem + kConstCol, mx4::scale_desc_lo(smem_u32(const_sf)));
+      const uint32_t b_off = 2u * kWBytes >> 4, f_off = 2u * (kWBytes + b_bytes) >> 4;
+      uint32_t st = ring >> 4, ph = 0, cols = tmem + kSfCol;
+      int s = 0, local = 0;
       bool ok = true;
       for (int i = blockIdx.x; i < units && ok; i += gridDim.x, ++local) {
         const Unit u = unit_at(g, lists, i);
         const int buf = local & 1;
-        if (!mbar_wait_bounded(&acc_empty[buf], ((uint32_t)(local >> 1) & 1u) ^ 1u, &abort_flag,
-                               g.status, kDevTimeoutMma))
+        if (!mbar_wait_lazy(&acc_empty[buf], ((uint32_t)(local >> 1) & 1u) ^ 1u, &abort_flag,
+                            g.status, kDevTimeoutMma))
           break;
         tc_fence_after();
         const uint32_t d = tmem + (uint32_t)buf * 128u;
-        const uint32_t N = (uint32_t)(u.n + 7) / 8 * 16;
-        for (int k = 0; k < u.nk; ++k, ++fill) {
-          const int s = fill % g.stages;
-          if (!mbar_wait_bounded(&full[s], (uint32_t)(fill / g.stages) & 1u, &abort_flag, g.status,
-                                 kDevTimeoutFull)) {
+        const uint32_t idesc = mx4::idesc_mxf4_f8(128, (uint32_t)(u.n + 7) / 8 * 16, 0);
+        uint32_t acc = 0;
+        for (int k = u.nk; k > 0; k -= 2) {
+          if (!mbar_wait_lazy(&full[s], ph, &abort_flag, g.status, kDevTimeoutFull)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t w = smem_u32(smem + s * stage_bytes), b = w + kWBytes;
-          const uint32_t sf = b + (uint32_t)(g.b_rows * kBK);
-          const uint32_t sfa = tmem + kSfCol + (uint32_t)s * 8u;
-          const uint32_t sfb = UP ? tmem + kConstCol : sfa + 4;
-          mx4::copy_scales(sfa, sf);
-          if (!UP) mx4::copy_scales(sfb, sf + 512);
+          const uint32_t w = mx4::code_desc_lo(st << 4), b = w + b_off;
+          const uint32_t f = mx4::scale_desc_lo((st + f_off) << 4);
+          const uint32_t sfb = UP ? tmem + kConstCol : cols + 8u;
+          mx4::copy_scales(cols, f);
+          if (!UP) mx4::copy_scales(sfb, f + 64u);
+          if (k > 1) {
+            mx4::copy_scales(cols + 4u, f + 32u);
+            if (!UP) mx4::copy_scales(sfb + 4u, f + 96u);
+          }
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            mx4::mma_mxf8f6f4(d, smem_desc(w + j * 32, 16, 1024, 2),
-                              smem_desc(b + j * 32, 16, 1024, 2),
-                              mx4::idesc_mxf4_f8(128, N, (uint32_t)j), sfa, sfb,
-                              (k > 0 || j > 0) ? 1u : 0u);
+          for (uint32_t j = 0; j < 4; ++j) {
+            mx4::mma_mxf8f6f4(d, mx4::code_desc(w + 2u * j), mx4::code_desc(b + 2u * j),
+                              idesc | (j << 4) | (j << 29), cols, sfb, acc);
+            acc = 1;
+          }
+          if (k > 1) {
+            const uint32_t w1 = w + (kWBytes >> 4), b1 = b + (b_bytes >> 4);
+#pragma unroll
+            for (uint32_t j = 0; j < 4; ++j)
+              mx4::mma_mxf8f6f4(d, mx4::code_desc(w1 + 2u * j), mx4::code_desc(b1 + 2u * j),
+                                idesc | (j << 4) | (j << 29), cols + 4u, UP ? sfb : sfb + 4u, 1);
+          }
           mma_commit(&empty[s]);
+          st += (uint32_t)stage_bytes >> 4;
+          cols += 16u;
+          if (++s == g.stages) {
+            s = 0;
+            ph ^= 1u;
+            st = ring >> 4;
+            cols = tmem + kSfCol;
+          }
         }
         if (ok) mma_commit(&acc_full[buf]);
       }
@@ -489,8 +523,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = blockIdx.x; i < units; i += gridDim.x, ++local) {
       const Unit u = unit_at(g, lists, i);
       const int buf = local & 1;
-      const bool ok = mbar_wait_bounded(&acc_full[buf], (uint32_t)(local >> 1) & 1u, &abort_flag,
-                                        g.status, kDevTimeoutMma);
+      const bool ok = mbar_wait_lazy(&acc_full[buf], (uint32_t)(local >> 1) & 1u, &abort_flag,
+                                     g.status, kDevTimeoutMma);
       __syncwarp();
       if (bar_red_or(1, 128, !ok)) break;
       tc_fence_after();
@@ -619,6 +653,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         bar_sync(1, 128);   // ready is free again
       }
+    }
+  }
+  __syncwarp();
+  if (abort_flag) {
+    // copies in flight may still land: give them time before the CTA exits
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < 1000000ull) {
     }
   }
   __syncwarp();
@@ -778,7 +819,7 @@ cudaError_t launch_moe(const MoeArgs& a, int sm_count, cudaStream_t st) {
   g.T = a.T;
   g.topk = a.topk;
   g.b_rows = (2 * a.T + 15) / 16 * 16;
-  const int stage_bytes = kWBytes + g.b_rows * kBK + 1024;
+  const int stage_bytes = 2 * (kWBytes + g.b_rows * kBK + 1024);
   g.stages = kRingBytes / stage_bytes < kMaxStages ? kRingBytes / stage_bytes : kMaxStages;
   g.xs = xs;
   g.hq = w + l.hq;

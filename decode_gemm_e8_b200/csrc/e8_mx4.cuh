@@ -98,11 +98,21 @@ __device__ __forceinline__ void mma_mxf8f6f4(uint32_t d_tmem, uint64_t a_desc, u
       : "memory");
 }
 
+// Matrix descriptors from their low word, so that the issuing thread's loop adds
+// to one register.  Codes: K-major rows of 128 bytes with the 128-byte swizzle;
+// scales: 8 rows of 16 bytes after one another.
+__device__ __forceinline__ uint32_t code_desc_lo(uint32_t smem) { return (smem >> 4) | (1u << 16); }
+__device__ __forceinline__ uint64_t code_desc(uint32_t lo) {
+  return (uint64_t)((1024u >> 4) | (1u << 14) | (2u << 29)) << 32 | lo;
+}
+__device__ __forceinline__ uint32_t scale_desc_lo(uint32_t smem) {
+  return (smem >> 4) | ((128u >> 4) << 16);
+}
 // One 512-byte scale tile (32 lanes of 16 bytes) into four columns of tensor
 // memory, repeated in all four lane quarters.
-__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t smem) {
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t desc_lo) {
   asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr),
-               "l"(smem_desc(smem, 128, 128, 0))
+               "l"((uint64_t)((128u >> 4) | (1u << 14)) << 32 | desc_lo)
                : "memory");
 }
 

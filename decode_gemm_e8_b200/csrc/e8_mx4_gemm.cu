@@ -19,13 +19,15 @@ namespace mx4 {
 // than SMs; every CTA leaves its partial tile in its own shared memory and each
 // then adds up, in rank order, the columns it was given (distributed shared
 // memory), so results do not depend on timing.
-//   warp 0     TMA producer: codes of W (128 x 256 K, 16 KB) and of the tokens
-//              (128-byte swizzle), scale tiles by plain bulk copies
+//   warps 0, 6 TMA producers of W (128 x 256 K, 16 KB) and of the tokens: codes
+//              with the 128-byte swizzle, scale tiles by plain bulk copies.  One
+//              thread each: at 16 KB a stage the SM's share of HBM leaves an issuing
+//              thread some 350 cycles a stage
 //   warp 1     tensor-memory allocation; one thread copies the stage's scales to
 //              tensor memory (a slot of its own for each stage, so that no copy
 //              meets an MMA that still reads) and issues the MMAs
 //   warps 2-5  epilogue
-constexpr int kStreamThreads = 192;
+constexpr int kStreamThreads = 224;
 constexpr int kStreamRows = 128;
 constexpr int kBK = 256;               // K of a stage: 128 bytes of codes
 constexpr int kCodeTile = 128 * 128;   // bytes of 128 rows
@@ -67,7 +69,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < a.stages; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], 2);   // both producers
       mbar_init(&empty[s], 1);
     }
     mbar_init(&done, 1);
@@ -84,86 +86,114 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   const uint32_t tmem = tmem_slot;
   if (!a.early) grid_dep_wait();
 
+  const uint32_t ring = smem_u32(smem);
   if (warp == 0) {
     if (lane == 0) {
+      // codes and scales of W
       tma_prefetch_desc(&tmW);
-      tma_prefetch_desc(&tmA);
-      // scale tiles of a stage: both 128-column tiles, or the last one alone
-      auto sf_bytes = [&](int kb) { return (uint32_t)min(2, kqs - 2 * kb) * 512u; };
-      auto tok_tiles = [&]() { return min(nbt, (a.M - m0 + 127) / 128); };
-      auto weights = [&](int i, int s) {
-        const int kb = kb0 + i;
-        uint8_t* st = smem + s * stage_bytes;
-        const uint32_t sf = sf_bytes(kb);
-        mbar_arrive_expect_tx(&full[s], (uint32_t)(kCodeTile + a.bn * 128) +
-                                            sf * (1u + (uint32_t)tok_tiles()));
-        tma_load_2d(st, &tmW, &full[s], kb * 128, n0);
-        bulk_load(st + kCodeTile + a.bn * 128,
-                  a.w_scales + ((int64_t)(n0 >> 7) * kqs + 2 * kb) * 512, sf, &full[s]);
-      };
-      auto tokens = [&](int i, int s) {
-        const int kb = kb0 + i;
-        uint8_t* st = smem + s * stage_bytes;
-        tma_load_2d(st + kCodeTile, &tmA, &full[s], kb * 128, m0);
-        for (int t = 0; t < tok_tiles(); ++t)
-          bulk_load(st + kCodeTile + a.bn * 128 + 1024 + t * 1024,
-                    a.a_scales + ((int64_t)((m0 >> 7) + t) * kqs + 2 * kb) * 512, sf_bytes(kb),
-                    &full[s]);
-      };
-      const int head = min(nkb, a.stages);
-      for (int i = 0; i < head; ++i) weights(i, i);
-      if (a.early) grid_dep_wait();
-      for (int i = 0; i < head; ++i) tokens(i, i);
-      int i = head;
-      for (; i < nkb; ++i) {
-        const int s = i % a.stages;
-        if (!mbar_wait_bounded(&empty[s], (uint32_t)(i / a.stages - 1) & 1u, &abort_flag, a.status,
-                               kDevTimeoutEmpty))
-          break;
-        weights(i, s);
-        tokens(i, s);
+      const uint8_t* sf = a.w_scales + ((int64_t)(n0 >> 7) * kqs + 2 * kb0) * 512;
+      uint32_t st = ring, ph = 1;
+      int s = 0;
+      for (int i = 0; i < nkb; ++i) {
+        if (!mbar_wait_lazy(&empty[s], ph, &abort_flag, a.status, kDevTimeoutEmpty)) break;
+        // both 128-column scale tiles of the stage, or the last one alone
+        const uint32_t sb = 2 * (kb0 + i) + 1 < kqs ? 1024u : 512u;
+        mbar_arrive_expect_tx(&full[s], (uint32_t)kCodeTile + sb);
+        load_2d(st, &tmW, &full[s], (kb0 + i) * 128, n0);
+        load_bulk(st + kCodeTile + (uint32_t)a.bn * 128u, sf, sb, &full[s]);
+        sf += 1024;
+        st += (uint32_t)stage_bytes;
+        if (++s == a.stages) {
+          s = 0;
+          ph ^= 1u;
+          st = ring;
+        }
       }
-      if (abort_flag) {
-        // copies in flight may still land: give them time before the CTA exits
-        const uint64_t t0 = global_timer_ns();
-        while (global_timer_ns() - t0 < 1000000ull) {
+    }
+  } else if (warp == 6) {
+    if (lane == 0) {
+      // codes and scales of the tokens
+      tma_prefetch_desc(&tmA);
+      if (a.early) grid_dep_wait();
+      const int tiles = min(nbt, (a.M - m0 + 127) / 128);
+      const uint8_t* sf = a.a_scales + ((int64_t)(m0 >> 7) * kqs + 2 * kb0) * 512;
+      uint32_t st = ring + kCodeTile, ph = 1;
+      int s = 0;
+      for (int i = 0; i < nkb; ++i) {
+        if (!mbar_wait_lazy(&empty[s], ph, &abort_flag, a.status, kDevTimeoutEmpty)) break;
+        const uint32_t sb = 2 * (kb0 + i) + 1 < kqs ? 1024u : 512u;
+        mbar_arrive_expect_tx(&full[s], (uint32_t)a.bn * 128u + sb * (uint32_t)tiles);
+        load_2d(st, &tmA, &full[s], (kb0 + i) * 128, m0);
+        const uint32_t to = st + (uint32_t)a.bn * 128u + 1024u;
+        load_bulk(to, sf, sb, &full[s]);
+        if (tiles > 1) load_bulk(to + 1024u, sf + (size_t)kqs * 512, sb, &full[s]);
+        sf += 1024;
+        st += (uint32_t)stage_bytes;
+        if (++s == a.stages) {
+          s = 0;
+          ph ^= 1u;
+          st = ring + kCodeTile;
         }
       }
     }
   } else if (warp == 1) {
     if (lane == 0) {
+      const uint32_t idesc0 = idesc_mxf4(128, (uint32_t)a.bn, 0),
+                     idesc1 = idesc_mxf4(128, (uint32_t)a.bn, 2);
+      const uint32_t t_off = kCodeTile >> 4, f_off = t_off + (uint32_t)a.bn * 8u;
+      const uint32_t sf_cols = 8u + 8u * (uint32_t)nbt;
+      uint32_t st = ring >> 4, ph = 0, cols = tmem + kSfCol, acc = 0;
+      int s = 0, left = a.K - kb0 * kBK;   // columns from here on
       for (int i = 0; i < nkb; ++i) {
-        const int s = i % a.stages;
-        if (!mbar_wait_bounded(&full[s], (uint32_t)(i / a.stages) & 1u, &abort_flag, a.status,
-                               kDevTimeoutFull))
-          break;
+        if (!mbar_wait_lazy(&full[s], ph, &abort_flag, a.status, kDevTimeoutFull)) break;
         tc_fence_after();
-        const uint32_t w = smem_u32(smem + s * stage_bytes), t = w + kCodeTile;
-        const uint32_t sf = t + (uint32_t)a.bn * 128u;
-        const uint32_t sfa = tmem + kSfCol + (uint32_t)(s * (8 + 8 * nbt)), sfb = sfa + 8;
-        const int steps = min(4, (a.K - (kb0 + i) * kBK + 63) / 64);   // of 64 columns
-        for (int q = 0; q < (steps + 1) / 2; ++q) {
-          copy_scales(sfa + q * 4, sf + q * 512);
-          for (int b = 0; b < nbt; ++b)
-            copy_scales(sfb + (q * nbt + b) * 4, sf + 1024 + b * 1024 + q * 512);
+        const uint32_t w = code_desc_lo(st << 4), t = w + t_off;
+        const uint32_t f = scale_desc_lo((st + f_off) << 4);
+        const uint32_t sfb = cols + 8u, half = 4u * (uint32_t)nbt;
+        const int steps = min(4, (left + 63) / 64);   // of 64 columns
+        copy_scales(cols, f);
+        copy_scales(sfb, f + 64u);
+        if (nbt > 1) copy_scales(sfb + 4u, f + 128u);
+        if (steps > 2) {
+          copy_scales(cols + 4u, f + 32u);
+          copy_scales(sfb + half, f + 96u);
+          if (nbt > 1) copy_scales(sfb + half + 4u, f + 160u);
         }
-        for (int j = 0; j < steps; ++j)
-          mma_mxf4(tmem, smem_desc(w + j * 32, 16, 1024, 2), smem_desc(t + j * 32, 16, 1024, 2),
-                   idesc_mxf4(128, (uint32_t)a.bn, (uint32_t)(j & 1) * 2u), sfa + (j >> 1) * 4,
-                   sfb + (j >> 1) * 4 * nbt, (i > 0 || j > 0) ? 1u : 0u);
+        mma_mxf4(tmem, code_desc(w), code_desc(t), idesc0, cols, sfb, acc);
+        acc = 1;
+        if (steps > 1) mma_mxf4(tmem, code_desc(w + 2u), code_desc(t + 2u), idesc1, cols, sfb, 1);
+        if (steps > 2)
+          mma_mxf4(tmem, code_desc(w + 4u), code_desc(t + 4u), idesc0, cols + 4u, sfb + half, 1);
+        if (steps > 3)
+          mma_mxf4(tmem, code_desc(w + 6u), code_desc(t + 6u), idesc1, cols + 4u, sfb + half, 1);
         mma_commit(&empty[s]);
+        left -= kBK;
+        st += (uint32_t)stage_bytes >> 4;
+        cols += sf_cols;
+        if (++s == a.stages) {
+          s = 0;
+          ph ^= 1u;
+          st = ring >> 4;
+          cols = tmem + kSfCol;
+        }
       }
       mma_commit(&done);   // also after a wait that gave up: nothing may be in flight at the end
     }
   }
   __syncwarp();
   // every warp: all MMAs of this CTA have finished
-  const bool ok = mbar_wait_bounded(&done, 0, &abort_flag, a.status, kDevTimeoutMma);
+  const bool ok = mbar_wait_lazy(&done, 0, &abort_flag, a.status, kDevTimeoutMma);
   __syncwarp();
   tc_fence_after();
   const int cols = min(a.bn, a.M - m0);
+  if (abort_flag) {
+    // copies in flight may still land: give them time before the CTA exits
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < 1000000ull) {
+    }
+  }
   if (S == 1) {
-    if (warp >= 2 && ok) {
+    if (warp >= 2 && warp < 6 && ok) {
       const int quarter = warp & 3, n = n0 + quarter * 32 + lane;
       for (int c = 0; c < cols; c += 16) {
         uint32_t r[16];
@@ -180,7 +210,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     }
   } else {
     float* part = reinterpret_cast<float*>(smem);   // [column][128], the ring is free
-    if (warp >= 2) {
+    if (warp >= 2 && warp < 6) {
       const int quarter = warp & 3;
       for (int c = 0; c < cols; c += 16) {
         uint32_t r[16];
