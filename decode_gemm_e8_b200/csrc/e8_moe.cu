@@ -3,10 +3,8 @@
 // launches after the first are programmatic, so that a kernel's prologue overlaps
 // its predecessor's end.
 //
-//   k_moe_logits  router logits (products exact in fp32, sums in fp64) and the
-//                 activations as two e4m3 rows a token
-//   k_moe_route   top-k, probabilities, and the slots (token, choice) sorted by
-//                 expert
+//   k_moe_route   router logits (products exact in fp32 and summed in fp64), top-k and
+//                 probabilities, and the activations as two e4m3 rows a token
 //   k_moe_gemm    twice.  The tensor cores take the 4-bit weights as they are
 //                 (tcgen05.mma.kind::mxf8f6f4, e2m1 x e4m3): 128 rows of an expert's
 //                 matrix on the M side, its tokens on the N side.  The activations
@@ -59,24 +57,103 @@ __device__ __forceinline__ uint32_t to_pair(float v) {
 }
 
 // ------------------------------------------------------------------ router ---
-constexpr int kLogitTokens = 4;   // tokens a warp takes with one expert's row
+constexpr int kRouteCtas = 8, kRouteTokens = 4;   // a cluster takes 4 tokens
 
-// Blocks [0, T): one token's e4m3 rows.  Then 8 experts x kLogitTokens tokens a
-// block, one expert a warp.  All blocks clear the counters of the later kernels.
-__global__ void __launch_bounds__(256)
-    k_moe_logits(const uint16_t* __restrict__ X, int T, int H, const uint16_t* __restrict__ R,
-                 int E, double* __restrict__ logits, uint8_t* __restrict__ Xq,
-                 float* __restrict__ xs, int* __restrict__ counters, int n_counters) {
+// Sums 16 values over the warp's lanes; lane l returns the sum of v[l >> 1].
+__device__ __forceinline__ double warp_sum16(double (&v)[16], int lane) {
+#pragma unroll
+  for (int w = 8; w; w >>= 1) {
+    const bool up = (lane & (2 * w)) != 0;
+#pragma unroll
+    for (int i = 0; i < w; ++i) {
+      const double send = up ? v[i] : v[i + w];
+      v[i] = (up ? v[i + w] : v[i]) + __shfl_xor_sync(0xFFFFFFFFu, send, 2 * w);
+    }
+  }
+  return v[0] + __shfl_xor_sync(0xFFFFFFFFu, v[0], 1);
+}
+
+// One cluster of 8 CTAs for 4 tokens: each CTA takes an eighth of the experts, its
+// warps 4 experts x 4 tokens of a part of H each (16 fp64 sums a lane; converting
+// bf16 to fp64 costs four times an fp64 product, so every converted value is used
+// four times).  The logits of token j go to CTA j, which chooses; CTAs 4..7 write
+// the tokens' e4m3 rows meanwhile.  One launch and no counters: the logits cross
+// CTAs in distributed shared memory.
+__global__ void __cluster_dims__(kRouteCtas, 1, 1) __launch_bounds__(256)
+    k_moe_route(const uint16_t* __restrict__ X, int T, int H, const uint16_t* __restrict__ R,
+                int E, int topk, int renorm, int32_t* __restrict__ experts,
+                float* __restrict__ probs, int32_t* __restrict__ experts_out,
+                float* __restrict__ probs_out, uint8_t* __restrict__ Xq, float* __restrict__ xs,
+                int* __restrict__ counters, int n_counters) {
+  __shared__ double part[16][16];   // [experts of four x part of H][expert, token]
+  __shared__ double logit[kMaxExperts];
+  __shared__ uint64_t key[kMaxExperts];
+  __shared__ int chosen[kMaxTopk];
+  __shared__ uint32_t wmax[8];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = (int)cluster_ctarank(), t0 = (int)blockIdx.x / kRouteCtas * kRouteTokens;
+  const int nt = min(kRouteTokens, T - t0);
   grid_dep_launch();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int i = blockIdx.x * 256 + threadIdx.x; i < n_counters; i += gridDim.x * 256)
-    counters[i] = 0;
-  if ((int)blockIdx.x < T) {
-    __shared__ uint32_t wmax[8];
-    const int t = blockIdx.x;
+  cluster_arrive();   // (the wait below: every CTA of the cluster has started)
+  for (int i = blockIdx.x * 256 + tid; i < n_counters; i += gridDim.x * 256) counters[i] = 0;
+
+  const int per = (E + kRouteCtas - 1) / kRouteCtas, e0 = rank * per;
+  const int ne = min(per, E - e0), groups = ne > 0 ? (ne + 3) / 4 : 0;
+  const int parts = groups > 0 && groups < 8 ? 8 / groups : 1, chunks = (H + 255) / 256;
+  for (int item = warp; item < groups * parts; item += 8) {
+    const int e = e0 + item / parts * 4, p = item % parts;
+    double acc[16] = {};
+    for (int c = chunks * p / parts; c < chunks * (p + 1) / parts; ++c) {
+      const int k = c * 256 + lane * 8;
+      uint4 r[4], x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        r[j] = x[j] = make_uint4(0, 0, 0, 0);
+        if (k < H && e + j < e0 + ne)
+          r[j] = *reinterpret_cast<const uint4*>(R + (size_t)(e + j) * H + k);
+        if (k < H && j < nt)
+          x[j] = *reinterpret_cast<const uint4*>(X + (size_t)(t0 + j) * H + k);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        double rd[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t w = i < 2 ? r[j].x : i < 4 ? r[j].y : i < 6 ? r[j].z : r[j].w;
+          rd[j] = (double)((i & 1) ? bf16_hi_to_f32(w) : bf16_lo_to_f32(w));
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (j >= nt) break;
+          const uint32_t w = i < 2 ? x[j].x : i < 4 ? x[j].y : i < 6 ? x[j].z : x[j].w;
+          const double xd = (double)((i & 1) ? bf16_hi_to_f32(w) : bf16_lo_to_f32(w));
+#pragma unroll
+          for (int q = 0; q < 4; ++q) acc[q * 4 + j] = fma(rd[q], xd, acc[q * 4 + j]);
+        }
+      }
+    }
+    const double s = warp_sum16(acc, lane);
+    if (!(lane & 1)) part[item][lane >> 1] = s;
+  }
+  __syncthreads();
+  cluster_wait();
+  if (tid < ne * kRouteTokens) {
+    const int el = tid / kRouteTokens, j = tid % kRouteTokens;
+    double s = 0.0;
+    for (int p = 0; p < parts; ++p) s += part[el / 4 * parts + p][(el & 3) * 4 + j];
+    asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(
+                     mapa_shared(smem_u32(&logit[e0 + el]), (uint32_t)j)),
+                 "d"(s)
+                 : "memory");
+  }
+  __syncwarp();
+  cluster_arrive();
+  if (rank >= kRouteTokens && rank - kRouteTokens < nt) {
+    // hi and lo rows of one token
+    const int t = t0 + rank - kRouteTokens;
     const uint4* x = reinterpret_cast<const uint4*>(X + (size_t)t * H);
     uint32_t m = 0;
-    for (int k = threadIdx.x; k < H / 8; k += 256) {
+    for (int k = tid; k < H / 8; k += 256) {
       const uint4 v = x[k];
       const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -92,7 +169,7 @@ __global__ void __launch_bounds__(256)
     const float inv = byte == 255u ? 0.0f : mx4::inv_scale(byte);
     uint2* hi = reinterpret_cast<uint2*>(Xq + (size_t)(2 * t) * H);
     uint2* lo = reinterpret_cast<uint2*>(Xq + (size_t)(2 * t + 1) * H);
-    for (int k = threadIdx.x; k < H / 8; k += 256) {
+    for (int k = tid; k < H / 8; k += 256) {
       const uint4 v = x[k];
       const uint32_t w[4] = {v.x, v.y, v.z, v.w};
       uint32_t h2[2] = {0, 0}, l2[2] = {0, 0};
@@ -106,157 +183,45 @@ __global__ void __launch_bounds__(256)
       hi[k] = make_uint2(h2[0], h2[1]);
       lo[k] = make_uint2(l2[0], l2[1]);
     }
-    if (threadIdx.x == 0) xs[t] = mx4::scale_value(byte);
-    return;
+    if (tid == 0) xs[t] = mx4::scale_value(byte);
   }
-  const int b = blockIdx.x - T, eb = (E + 7) / 8;
-  const int e = b % eb * 8 + warp, t0 = b / eb * kLogitTokens;
-  if (e >= E) return;
-  double s[kLogitTokens] = {};
-  const uint4* r = reinterpret_cast<const uint4*>(R + (size_t)e * H);
-  for (int k = lane; k < H / 8; k += 32) {
-    const uint4 rv = r[k];
-    const uint32_t rw[4] = {rv.x, rv.y, rv.z, rv.w};
-#pragma unroll
-    for (int j = 0; j < kLogitTokens; ++j) {
-      if (t0 + j >= T) break;
-      const uint4 v = reinterpret_cast<const uint4*>(X + (size_t)(t0 + j) * H)[k];
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        s[j] += (double)(bf16_lo_to_f32(rw[i]) * bf16_lo_to_f32(w[i]));
-        s[j] += (double)(bf16_hi_to_f32(rw[i]) * bf16_hi_to_f32(w[i]));
-      }
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < kLogitTokens; ++j) {
-    for (int o = 16; o; o >>= 1) s[j] += __shfl_xor_sync(0xFFFFFFFFu, s[j], o);
-    if (lane == 0 && t0 + j < T) logits[(size_t)(t0 + j) * E + e] = s[j];
-  }
-}
-
-// Sorted slots: active expert a has the slots slot_of[off[a]] .. slot_of[off[a + 1] - 1].
-struct Lists {
-  int* nact;
-  int* expert;    // [nact]
-  int* off;       // [nact + 1]
-  int* slot_of;   // [T topk], slot = token * topk + choice
-  float* probs;   // [T topk] by slot
-};
-
-// One block.  Warp w chooses for tokens w, w + 32, ..: the largest key (fp64 bits
-// in an order-preserving form, NaN lowest) by two 32-bit warp reductions, then the
-// lowest expert that has it.
-__global__ void __launch_bounds__(1024)
-    k_moe_route(const double* __restrict__ logits, int T, int E, int topk, int renorm, Lists l,
-                int32_t* __restrict__ experts_out, float* __restrict__ probs_out) {
-  __shared__ int16_t chosen[kMaxSlots];
-  __shared__ uint16_t count[32][kMaxExperts];   // slots of an expert in a group of 32 slots
-  __shared__ int first[kMaxExperts];
-  __shared__ uint32_t wsum[32];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int slots = T * topk, groups = (slots + 31) / 32;
-  grid_dep_launch();
-  for (int i = tid; i < groups * kMaxExperts; i += 1024) (&count[0][0])[i] = 0;
-  grid_dep_wait();
-  for (int t = warp; t < T; t += 32) {
-    uint64_t key[kMaxExperts / 32];
-#pragma unroll
-    for (int j = 0; j < kMaxExperts / 32; ++j) {
-      const int e = lane + 32 * j;
-      key[j] = 0;
-      if (e < E) {
-        const double v = logits[(size_t)t * E + e] + 0.0;   // -0 becomes 0
-        const uint64_t u = (uint64_t)__double_as_longlong(v);
-        key[j] = v != v ? 1ull : (u >> 63 ? ~u : u | (1ull << 63));
-      }
-    }
-    double top = 0.0;
-    float sum = 0.0f, mine = 0.0f;
-    int mine_e = 0;
-    for (int i = 0; i < topk; ++i) {
-      uint64_t best = 0;
-      int be = E;
-#pragma unroll
-      for (int j = 0; j < kMaxExperts / 32; ++j)
-        if (key[j] > best) {
-          best = key[j];
-          be = lane + 32 * j;
-        }
-      const uint32_t hi = __reduce_max_sync(0xFFFFFFFFu, (uint32_t)(best >> 32));
-      const bool in_hi = (uint32_t)(best >> 32) == hi && best != 0;
-      const uint32_t lo = __reduce_max_sync(0xFFFFFFFFu, in_hi ? (uint32_t)best : 0u);
-      const bool in = in_hi && (uint32_t)best == lo;
-      const int e = (int)__reduce_min_sync(0xFFFFFFFFu, in ? (uint32_t)be : 0xFFFFFFFFu);
-#pragma unroll
-      for (int j = 0; j < kMaxExperts / 32; ++j)
-        if (lane + 32 * j == e) key[j] = 0;
-      const double v = logits[(size_t)t * E + e];
-      if (i == 0) top = v;
-      const float p = expf((float)(v - top));
-      sum += p;
-      if (lane == i) {
-        mine = p;
-        mine_e = e;
-      }
-    }
-    if (!renorm) {
-      sum = 0.0f;
-      for (int e = lane; e < E; e += 32) sum += expf((float)(logits[(size_t)t * E + e] - top));
-      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    }
-    if (lane < topk) {
-      const int s = t * topk + lane;
-      chosen[s] = (int16_t)mine_e;
-      l.probs[s] = mine / sum;
-      if (experts_out) experts_out[s] = mine_e;
-      if (probs_out) probs_out[s] = mine / sum;
-    }
+  __syncwarp();
+  cluster_wait();
+  if (rank >= nt) return;
+  // this CTA chooses for token t0 + rank: an expert's place is the number of experts
+  // before it (larger logit, or the same and a lower number; NaN comes last)
+  const int t = t0 + rank;
+  for (int e = tid; e < E; e += 256) {
+    const double v = logit[e] + 0.0;   // -0 becomes 0
+    const uint64_t u = (uint64_t)__double_as_longlong(v);
+    key[e] = v != v ? 0ull : (u >> 63 ? ~u : u | (1ull << 63));
   }
   __syncthreads();
-  // this thread's slot: its place among the slots of its expert in its group
-  const int e = tid < slots ? chosen[tid] : -1;
-  const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
-  const int place = __popc(same & ((1u << lane) - 1u));
-  if (e >= 0 && place == 0) count[warp][e] = (uint16_t)__popc(same);
-  __syncthreads();
-  // per expert: running count over the groups; then a scan over experts of
-  // (is active, slots) packed in one word
-  uint32_t v = 0;
-  if (tid < E) {
-    uint32_t run = 0;
-    for (int g = 0; g < groups; ++g) {
-      const uint32_t c = count[g][tid];
-      count[g][tid] = (uint16_t)run;
-      run += c;
-    }
-    v = run ? (1u << 16) | run : 0u;
-  }
-  uint32_t scan = v;
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, scan, o);
-    if (lane >= o) scan += u;
-  }
-  if (lane == 31) wsum[warp] = scan;
-  __syncthreads();
-  uint32_t before = 0;
-  for (int w = 0; w < warp; ++w) before += wsum[w];
-  const uint32_t ex = before + scan - v;   // of the experts before this one
-  if (tid < E) {
-    first[tid] = (int)(ex & 0xFFFFu);
-    if (v) {
-      l.expert[ex >> 16] = tid;
-      l.off[ex >> 16] = (int)(ex & 0xFFFFu);
-    }
-    if (tid == E - 1) {
-      const int n = (int)((ex + v) >> 16);
-      *l.nact = n;
-      l.off[n] = slots;
-    }
+  for (int e = tid; e < E; e += 256) {
+    const uint64_t mine = key[e];
+    int place = 0;
+#pragma unroll 4
+    for (int j = 0; j < E; ++j) place += key[j] > mine || (key[j] == mine && j < e);
+    if (place < topk) chosen[place] = e;
   }
   __syncthreads();
-  if (e >= 0) l.slot_of[first[e] + count[warp][e] + place] = tid;
+  if (warp) return;
+  const double top = logit[chosen[0]];
+  float p = 0.0f, sum = 0.0f;
+  if (lane < topk) p = expf((float)(logit[chosen[lane]] - top));
+  if (renorm) {
+    sum = p;
+  } else {
+    for (int e = lane; e < E; e += 32) sum += expf((float)(logit[e] - top));
+  }
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+  if (lane < topk) {
+    const int s = t * topk + lane;
+    experts[s] = chosen[lane];
+    probs[s] = p / sum;
+    if (experts_out) experts_out[s] = chosen[lane];
+    if (probs_out) probs_out[s] = p / sum;
+  }
 }
 
 // ---------------------------------------------------------------- products ---
@@ -269,10 +234,12 @@ constexpr int kConstCol = 256, kSfCol = 264;   // tensor-memory columns of the s
 constexpr int kRingBytes = 212 * 1024;
 
 struct GemmArgs {
-  Lists l;
+  const int32_t* experts;  // by slot = token * topk + choice
+  const float* probs;
   const uint8_t* w_scales;
   int K, tiles, splits;    // tiles of 128 rows of one expert; K split in `splits`
-  int T, topk, stages, b_rows;
+  int T, E, topk, stages, b_rows;
+  const uint8_t* xq;       // up: the tokens' hi and lo rows
   const float* xs;         // up: scale of each token's pair
   uint8_t* hq;             // up: writes, down: reads through the tensor map
   uint8_t* h_scales;       // [active expert][I / 128][512]
@@ -286,11 +253,91 @@ struct GemmArgs {
 __device__ __forceinline__ void bar_sync(uint32_t id, uint32_t n) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
 }
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// Arrives on the barrier once this thread's copies so far have landed.
+__device__ __forceinline__ void copy_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+// The same value in every lane, known as such to the compiler.
+__device__ __forceinline__ int uniform(int v) {
+  return (int)__reduce_max_sync(0xFFFFFFFFu, (unsigned)v);
+}
 
-// The lists in shared memory.
+// Slots sorted by expert: active expert a (in order of number) has the slots
+// slot[off[a]] .. slot[off[a + 1] - 1], by rising slot.
 struct SharedLists {
   int16_t expert[kMaxExperts], off[kMaxExperts + 1], slot[kMaxSlots];
+  uint32_t wsum[8];
 };
+
+// Builds the lists (all threads; `scratch`: at least 32 * E + 4 * 1024 + 2 * E bytes);
+// returns the number of active experts.
+__device__ __forceinline__ int build_lists(SharedLists& l, uint8_t* scratch,
+                                           const int32_t* __restrict__ experts, int slots, int E) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int groups = (slots + 31) / 32;
+  uint8_t* count = scratch;   // [groups][E]: slots of an expert in a group of 32 slots
+  int16_t* se = reinterpret_cast<int16_t*>(scratch + 32 * kMaxExperts);
+  int16_t* sp = se + kMaxSlots;
+  int16_t* first = sp + kMaxSlots;
+  for (int i = tid; i < groups * E; i += kThreads) count[i] = 0;
+  __syncthreads();
+  for (int g = warp; g < groups; g += kThreads / 32) {
+    const int s = g * 32 + lane, e = s < slots ? experts[s] : -1;
+    const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
+    const int place = __popc(same & ((1u << lane) - 1u));
+    if (e >= 0 && place == 0) count[g * E + e] = (uint8_t)__popc(same);
+    se[s] = (int16_t)e;
+    sp[s] = (int16_t)place;
+  }
+  __syncthreads();
+  // running counts over the groups, then a scan over experts of (is active, slots)
+  const int per = (E + kThreads - 1) / kThreads;
+  uint32_t mine = 0;
+  for (int e = tid * per; e < min(E, (tid + 1) * per); ++e) {
+    uint32_t run = 0;
+    for (int g = 0; g < groups; ++g) {
+      const uint32_t c = count[g * E + e];
+      count[g * E + e] = (uint8_t)run;
+      run += c;
+    }
+    first[e] = (int16_t)run;
+    mine += run ? (1u << 16) | run : 0u;
+  }
+  uint32_t scan = mine;
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, scan, o);
+    if (lane >= o) scan += u;
+  }
+  if (lane == 31) l.wsum[warp] = scan;
+  __syncthreads();
+  uint32_t at = scan - mine, total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) at += l.wsum[w];
+    total += l.wsum[w];
+  }
+  for (int e = tid * per; e < min(E, (tid + 1) * per); ++e) {
+    const uint32_t n = (uint32_t)first[e];
+    first[e] = (int16_t)(at & 0xFFFFu);
+    if (n) {
+      l.expert[at >> 16] = (int16_t)e;
+      l.off[at >> 16] = (int16_t)(at & 0xFFFFu);
+      at += (1u << 16) | n;
+    }
+  }
+  const int nact = (int)(total >> 16);
+  if (tid == 0) l.off[nact] = (int16_t)slots;
+  __syncthreads();
+  for (int s = tid; s < slots; s += kThreads)
+    l.slot[first[se[s]] + count[(s >> 5) * E + se[s]] + sp[s]] = (int16_t)s;
+  fence_proxy_async_smem();   // the scratch space becomes the copies' ring
+  __syncthreads();
+  return nact;
+}
+
 // The units of one block in turn: all row tiles and K parts of an expert, then the next.
 struct Unit {
   int a, tile, part, expert, off, n, k0, nk;
@@ -299,9 +346,9 @@ __device__ __forceinline__ Unit unit_at(const GemmArgs& g, const SharedLists& l,
   Unit r;
   const int per = g.tiles * g.splits;
   r.a = u / per;
-  const int rest = u % per;
+  const int rest = u - r.a * per;
   r.tile = rest / g.splits;
-  r.part = rest % g.splits;
+  r.part = rest - r.tile * g.splits;
   r.expert = l.expert[r.a];
   r.off = l.off[r.a];
   r.n = l.off[r.a + 1] - r.off;
@@ -311,6 +358,14 @@ __device__ __forceinline__ Unit unit_at(const GemmArgs& g, const SharedLists& l,
   return r;
 }
 
+// Waits of a whole warp, which then agrees on the outcome.
+#define WARP_WAIT(bar, parity, code) \
+  __all_sync(0xFFFFFFFFu, mbar_wait_lazy(bar, parity, &abort_flag, g.status, code))
+
+// Warps: 0 weights producer, 6 tokens producer, 1 MMAs, 2..5 epilogue.  At 16 KB of
+// weights a stage the SM's share of HBM leaves each role some 700 cycles a stage, so
+// the issuing warps run their loops as a whole (uniform registers) and only the
+// asynchronous instructions are one lane's.
 template <bool UP>
 __global__ void __launch_bounds__(kThreads, 1)
     k_moe_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmB,
@@ -319,8 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   __shared__ __align__(16) uint8_t const_sf[512];
-  __shared__ __align__(16) uint8_t stage_h[8][2][64];
-  __shared__ uint32_t h_max[4][8];
+  __shared__ __align__(16) float stage_v[8][128 + 4];
   __shared__ int ready[kMaxTokens];
   __shared__ SharedLists lists;
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drain;
@@ -328,11 +382,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ volatile uint32_t abort_flag;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int stage_bytes = 2 * (kWBytes + g.b_rows * kBK + 1024);
+  const uint32_t b_bytes = (uint32_t)(g.b_rows * 128);
+  const uint32_t stage_bytes = 2u * (kWBytes + b_bytes + 1024u);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < g.stages; ++s) {
-      mbar_init(&full[s], 2);   // both producers
+      mbar_init(&full[s], UP ? 33 : 2);   // the weights' producer, and the tokens'
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -342,6 +397,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&drain, 1);
     abort_flag = 0u;
     fence_mbar_init();
+    tma_prefetch_desc(&tmW);
+    if (!UP) tma_prefetch_desc(&tmB);
   }
   if (warp == 1) {
     tmem_alloc(&tmem_slot, 512);
@@ -353,99 +410,97 @@ __global__ void __launch_bounds__(kThreads, 1)
         ((threadIdx.x - 64) / 4) & 1 ? 0x7B7B7B7Bu : 0x7F7F7F7Fu;
     fence_proxy_async_smem();
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = tmem_slot;
   if (UP) {
     grid_dep_wait();
     grid_dep_launch();
   }
-  // (down: the lists were complete before the up kernel let this one start)
-  const int nact = *g.l.nact;
-  for (int i = threadIdx.x; i <= nact; i += kThreads) {
-    lists.off[i] = (int16_t)g.l.off[i];
-    if (i < nact) lists.expert[i] = (int16_t)g.l.expert[i];
-  }
-  for (int i = threadIdx.x; i < g.T * g.topk; i += kThreads)
-    lists.slot[i] = (int16_t)g.l.slot_of[i];
-  __syncthreads();
-  const int units = nact * g.tiles * g.splits;
+  // (down: the choice was complete before the up kernel let this one start)
+  tc_fence_before();
+  const int slots = g.T * g.topk;
+  const int units = build_lists(lists, smem, g.experts, slots, g.E) * g.tiles * g.splits;
+  tc_fence_after();
+  const uint32_t tmem = (uint32_t)uniform((int)tmem_slot);
+  const uint32_t ring = smem_u32(smem);
+  const int kqs = g.K / kBK;
 
-  const uint32_t ring = smem_u32(smem), b_bytes = (uint32_t)(g.b_rows * 128);
-  const int kqs = g.K / 128;
   if (warp == 0) {
-    if (lane == 0) {
-      // codes and scales of the weights; they do not depend on the preceding kernel
-      tma_prefetch_desc(&tmW);
-      uint32_t st = ring, ph = 1;
-      int s = 0;
-      bool ok = true;
-      for (int i = blockIdx.x; i < units && ok; i += gridDim.x) {
-        const Unit u = unit_at(g, lists, i);
-        const int row = (u.expert * g.tiles + u.tile) * kRows;
-        const uint8_t* sf = g.w_scales + ((int64_t)(row >> 7) * kqs + u.k0) * 512;
-        int x = u.k0 * 128;
-        for (int k = u.nk; k > 0; k -= 2) {
-          if (!mbar_wait_lazy(&empty[s], ph, &abort_flag, g.status, kDevTimeoutEmpty)) {
-            ok = false;
-            break;
-          }
-          // the tensor map unpacks: its bytes are counted as they lie in memory
-          const uint32_t half = k > 1 ? 2u : 1u;
-          mbar_arrive_expect_tx(&full[s], half * (kWBytes / 2 + 512u));
-          load_2d(st, &tmW, &full[s], x, row);
-          if (k > 1) load_2d(st + kWBytes, &tmW, &full[s], x + 128, row);
-          load_bulk(st + 2u * (kWBytes + b_bytes), sf, half * 512u, &full[s]);
-          x += 256;
-          sf += 1024;
-          st += (uint32_t)stage_bytes;
-          if (++s == g.stages) {
-            s = 0;
-            ph ^= 1u;
-            st = ring;
-          }
-        }
-      }
-    }
-  } else if (warp == 6) {
-    // the tokens' rows: two (hi and lo) a copy in the up product, where tokens lie in
-    // order of the batch; sixteen a copy in the down product, sorted by expert
-    if (lane == 0) tma_prefetch_desc(&tmB);
-    if (!UP) grid_dep_wait();
-    uint32_t st = ring + 2u * kWBytes, ph = 1;
+    // codes and scales of the weights; they do not depend on the preceding kernel
+    uint32_t st = ring, ph = 1;
     int s = 0;
     bool ok = true;
     for (int i = blockIdx.x; i < units && ok; i += gridDim.x) {
       const Unit u = unit_at(g, lists, i);
-      const int copies = UP ? u.n : (u.n + 7) / 8;
-      int row0 = 0, row1 = 0;
-      if (UP) {
-        if (lane < u.n) row0 = lists.slot[u.off + lane] / g.topk * 2;
-        if (lane + 32 < u.n) row1 = lists.slot[u.off + lane + 32] / g.topk * 2;
-      } else {
-        row0 = 2 * u.off + lane * 16;
-      }
-      const uint32_t bytes = UP ? (uint32_t)copies * 256u : (uint32_t)copies * 2048u + 512u;
-      const uint32_t to = (uint32_t)lane * (UP ? 256u : 2048u);
-      const uint8_t* sf = g.h_scales + ((int64_t)u.a * kqs + u.k0) * 512;
-      int x = u.k0 * 128;
+      const int row = (uniform(u.expert) * g.tiles + u.tile) * kRows;
+      const uint8_t* sf = g.w_scales + ((int64_t)(row >> 7) * kqs + u.k0) * 512;
+      int x = u.k0 * kBK;
       for (int k = u.nk; k > 0; k -= 2) {
-        ok = __all_sync(0xFFFFFFFFu,
-                        mbar_wait_lazy(&empty[s], ph, &abort_flag, g.status, kDevTimeoutEmpty));
+        ok = WARP_WAIT(&empty[s], ph, kDevTimeoutEmpty);
         if (!ok) break;
         const uint32_t half = k > 1 ? 2u : 1u;
-        if (lane == 0) mbar_arrive_expect_tx(&full[s], half * bytes);
-        __syncwarp();
-        for (uint32_t h = 0; h < half; ++h) {
-          if (lane < copies) load_2d(st + h * b_bytes + to, &tmB, &full[s], x + 128 * (int)h, row0);
-          if (UP && lane + 32 < copies)
-            load_2d(st + h * b_bytes + to + 32u * 256u, &tmB, &full[s], x + 128 * (int)h, row1);
+        if (elect_one()) {
+          // the tensor map unpacks: its bytes are counted as they lie in memory
+          mbar_arrive_expect_tx(&full[s], half * (kWBytes / 2 + 512u));
+          load_2d(st, &tmW, &full[s], x, row);
+          if (k > 1) load_2d(st + kWBytes, &tmW, &full[s], x + kBK, row);
+          load_bulk(st + 2u * (kWBytes + b_bytes), sf, half * 512u, &full[s]);
         }
-        if (!UP && lane == 0) load_bulk(st + 2u * b_bytes + 1024u, sf, half * 512u, &full[s]);
-        x += 256;
+        __syncwarp();
+        x += 2 * kBK;
         sf += 1024;
-        st += (uint32_t)stage_bytes;
+        st += stage_bytes;
+        if (++s == g.stages) {
+          s = 0;
+          ph ^= 1u;
+          st = ring;
+        }
+      }
+    }
+  } else if (warp == 6) {
+    uint32_t st = ring + 2u * kWBytes, ph = 1;
+    int s = 0;
+    bool ok = true;
+    if (!UP) grid_dep_wait();
+    for (int i = blockIdx.x; i < units && ok; i += gridDim.x) {
+      const Unit u = unit_at(g, lists, i);
+      const int n = uniform(u.n), off = uniform(u.off);
+      int x = u.k0 * kBK;
+      // up: tokens lie in order of the batch; 16 lanes copy the 256 bytes of each of
+      // a token's two rows, 16 bytes a lane, to where the 128-byte swizzle has them
+      const int r = lane >> 4, c = lane & 15;
+      const uint8_t* src = g.xq + (size_t)r * g.K + c * 16;
+      const uint32_t to = (c >> 3) * b_bytes + (uint32_t)r * 128u;
+      const uint8_t* sf = g.h_scales + ((int64_t)u.a * kqs + u.k0) * 512;
+      for (int k = u.nk; k > 0; k -= 2) {
+        ok = WARP_WAIT(&empty[s], ph, kDevTimeoutEmpty);
+        if (!ok) break;
+        if (UP) {
+          if (k > 1 || c < 8) {
+#pragma unroll 2
+            for (int j = 0; j < n; ++j) {
+              const int t = lists.slot[off + j] / g.topk;
+              copy_async16(st + to + (uint32_t)j * 256u +
+                               (uint32_t)(((c & 7) ^ ((2 * j + r) & 7)) << 4),
+                           src + (size_t)t * 2 * g.K + x);
+            }
+          }
+          copy_async_arrive(&full[s]);
+        } else {
+          // down: sorted by expert, sixteen rows a copy
+          const uint32_t half = k > 1 ? 2u : 1u, copies = (uint32_t)(n + 7) / 8;
+          if (elect_one()) {
+            mbar_arrive_expect_tx(&full[s], half * (copies * 2048u + 512u));
+            for (uint32_t q = 0; q < copies; ++q) {
+              load_2d(st + q * 2048u, &tmB, &full[s], x, 2 * off + (int)q * 16);
+              if (k > 1)
+                load_2d(st + b_bytes + q * 2048u, &tmB, &full[s], x + kBK, 2 * off + (int)q * 16);
+            }
+            load_bulk(st + 2u * b_bytes + 1024u, sf, half * 512u, &full[s]);
+          }
+          __syncwarp();
+        }
+        x += 2 * kBK;
+        sf += 1024;
+        st += stage_bytes;
         if (++s == g.stages) {
           s = 0;
           ph ^= 1u;
@@ -454,71 +509,72 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      if (UP) mx4::copy_scales(tmem + kConstCol, mx4::scale_desc_lo(smem_u32(const_sf)));
-      const uint32_t b_off = 2u * kWBytes >> 4, f_off = 2u * (kWBytes + b_bytes) >> 4;
-      uint32_t st = ring >> 4, ph = 0, cols = tmem + kSfCol;
-      int s = 0, local = 0;
-      bool ok = true;
-      for (int i = blockIdx.x; i < units && ok; i += gridDim.x, ++local) {
-        const Unit u = unit_at(g, lists, i);
-        const int buf = local & 1;
-        if (!mbar_wait_lazy(&acc_empty[buf], ((uint32_t)(local >> 1) & 1u) ^ 1u, &abort_flag,
-                            g.status, kDevTimeoutMma))
-          break;
+    const uint32_t b_off = 2u * kWBytes >> 4, f_off = 2u * (kWBytes + b_bytes) >> 4;
+    uint32_t st = ring >> 4, ph = 0, cols = tmem + kSfCol;
+    int s = 0, local = 0;
+    bool ok = true;
+    if (UP && elect_one())
+      mx4::copy_scales(tmem + kConstCol, mx4::scale_desc_lo(smem_u32(const_sf)));
+    __syncwarp();
+    for (int i = blockIdx.x; i < units && ok; i += gridDim.x, ++local) {
+      const Unit u = unit_at(g, lists, i);
+      const int buf = local & 1;
+      ok = WARP_WAIT(&acc_empty[buf], ((uint32_t)(local >> 1) & 1u) ^ 1u, kDevTimeoutMma);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t d = tmem + (uint32_t)buf * 128u;
+      const uint32_t idesc = mx4::idesc_mxf4_f8(128, (uint32_t)(uniform(u.n) + 7) / 8 * 16, 0);
+      for (int k = u.nk; k > 0; k -= 2) {
+        ok = WARP_WAIT(&full[s], ph, kDevTimeoutFull);
+        if (!ok) break;
         tc_fence_after();
-        const uint32_t d = tmem + (uint32_t)buf * 128u;
-        const uint32_t idesc = mx4::idesc_mxf4_f8(128, (uint32_t)(u.n + 7) / 8 * 16, 0);
-        uint32_t acc = 0;
-        for (int k = u.nk; k > 0; k -= 2) {
-          if (!mbar_wait_lazy(&full[s], ph, &abort_flag, g.status, kDevTimeoutFull)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t w = mx4::code_desc_lo(st << 4), b = w + b_off;
-          const uint32_t f = mx4::scale_desc_lo((st + f_off) << 4);
-          const uint32_t sfb = UP ? tmem + kConstCol : cols + 8u;
+        if (UP) fence_proxy_async_smem();   // the tokens' rows came by ordinary copies
+        uint32_t w = mx4::code_desc_lo(st << 4), b = w + b_off;
+        const uint32_t f = mx4::scale_desc_lo((st + f_off) << 4);
+        uint32_t acc = k < u.nk;
+        if (elect_one()) {
           mx4::copy_scales(cols, f);
-          if (!UP) mx4::copy_scales(sfb, f + 64u);
+          if (!UP) mx4::copy_scales(cols + 8u, f + 64u);
           if (k > 1) {
             mx4::copy_scales(cols + 4u, f + 32u);
-            if (!UP) mx4::copy_scales(sfb + 4u, f + 96u);
+            if (!UP) mx4::copy_scales(cols + 12u, f + 96u);
           }
+#pragma unroll 1
+          for (uint32_t h = 0; h < (k > 1 ? 8u : 4u); h += 4) {
+            const uint32_t sfb = UP ? tmem + kConstCol : cols + 8u + h;
 #pragma unroll
-          for (uint32_t j = 0; j < 4; ++j) {
-            mx4::mma_mxf8f6f4(d, mx4::code_desc(w + 2u * j), mx4::code_desc(b + 2u * j),
-                              idesc | (j << 4) | (j << 29), cols, sfb, acc);
-            acc = 1;
-          }
-          if (k > 1) {
-            const uint32_t w1 = w + (kWBytes >> 4), b1 = b + (b_bytes >> 4);
-#pragma unroll
-            for (uint32_t j = 0; j < 4; ++j)
-              mx4::mma_mxf8f6f4(d, mx4::code_desc(w1 + 2u * j), mx4::code_desc(b1 + 2u * j),
-                                idesc | (j << 4) | (j << 29), cols + 4u, UP ? sfb : sfb + 4u, 1);
+            for (uint32_t j = 0; j < 4; ++j) {
+              mx4::mma_mxf8f6f4(d, mx4::code_desc(w + 2u * j), mx4::code_desc(b + 2u * j),
+                                idesc | (j << 4) | (j << 29), cols + h, sfb, acc);
+              acc = 1;
+            }
+            w += kWBytes >> 4;
+            b += b_bytes >> 4;
           }
           mma_commit(&empty[s]);
-          st += (uint32_t)stage_bytes >> 4;
-          cols += 16u;
-          if (++s == g.stages) {
-            s = 0;
-            ph ^= 1u;
-            st = ring >> 4;
-            cols = tmem + kSfCol;
-          }
         }
-        if (ok) mma_commit(&acc_full[buf]);
+        __syncwarp();
+        st += stage_bytes >> 4;
+        cols += 16u;
+        if (++s == g.stages) {
+          s = 0;
+          ph ^= 1u;
+          st = ring >> 4;
+          cols = tmem + kSfCol;
+        }
       }
-      // every MMA of this thread has finished once `drain` flips
-      mma_commit(&drain);
-      const uint64_t t0 = global_timer_ns();
-      while (!mbar_try_wait(&drain, 0) && global_timer_ns() - t0 < 200000000ull) {
-      }
+      if (ok && elect_one()) mma_commit(&acc_full[buf]);
+      __syncwarp();
+    }
+    // every MMA of this warp has finished once `drain` flips
+    if (elect_one()) mma_commit(&drain);
+    __syncwarp();
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait(&drain, 0) && global_timer_ns() - t0 < 200000000ull) {
     }
   } else {
     const int quarter = warp & 3, row = quarter * 32 + lane, et = (int)threadIdx.x - 64;
-    const int slots = g.T * g.topk, width = g.tiles * kRows;
+    const int width = g.tiles * kRows;
     int local = 0;
     for (int i = blockIdx.x; i < units; i += gridDim.x, ++local) {
       const Unit u = unit_at(g, lists, i);
@@ -546,6 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (UP) {
         bool last = true;
         if (g.splits > 1) {
+#pragma unroll 1
           for (int j0 = 0; j0 < u.n; j0 += 8) {
             float v[8];
             read8(j0, v);
@@ -562,63 +619,77 @@ __global__ void __launch_bounds__(kThreads, 1)
             ready[0] = atomicAdd(&g.counters[u.a * g.tiles + u.tile], 1) == g.splits - 1;
           bar_sync(1, 128);
           last = ready[0] != 0;
-          bar_sync(1, 128);   // ready is free again
           __threadfence();
         }
         if (last) {
+#pragma unroll 1
           for (int j0 = 0; j0 < u.n; j0 += 8) {
-            float v[8];
             if (g.splits == 1) {
+              float v[8];
               read8(j0, v);
-            } else {
 #pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                v[j] = 0.0f;
-                if (j0 + j < u.n)
-                  for (int p = 0; p < g.splits; ++p)
-                    v[j] += __ldcg(&g.part[((size_t)p * slots + u.off + j0 + j) * width +
-                                           u.tile * kRows + row]);
+              for (int j = 0; j < 8; ++j) stage_v[j][row] = v[j];
+              bar_sync(1, 128);
+            }
+            // 16 lanes a token, four values of h (eight rows) a lane
+            const int j = j0 + et / 16, q = et & 15;
+            const bool mine = j < u.n;
+            float4 p0 = make_float4(0, 0, 0, 0), p1 = p0;
+            if (mine) {
+              if (g.splits == 1) {
+                p0 = *reinterpret_cast<const float4*>(&stage_v[et / 16][q * 8]);
+                p1 = *reinterpret_cast<const float4*>(&stage_v[et / 16][q * 8 + 4]);
+              } else {
+                const float* at = g.part + (size_t)(u.off + j) * width + u.tile * kRows + q * 8;
+                for (int p = 0; p < g.splits; ++p) {
+                  const float4 a = __ldcg(reinterpret_cast<const float4*>(at));
+                  const float4 b = __ldcg(reinterpret_cast<const float4*>(at + 4));
+                  p0.x += a.x; p0.y += a.y; p0.z += a.z; p0.w += a.w;
+                  p1.x += b.x; p1.y += b.y; p1.z += b.z; p1.w += b.w;
+                  at += (size_t)slots * width;
+                }
               }
             }
+            const float x = mine ? g.xs[lists.slot[u.off + j] / g.topk] : 0.0f;
+            const float gate[4] = {p0.x * x, p0.z * x, p1.x * x, p1.z * x};
+            const float up[4] = {p0.y * x, p0.w * x, p1.y * x, p1.w * x};
+            float h[4];
+            uint32_t m = 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float x = j0 + j < u.n ? g.xs[lists.slot[u.off + j0 + j] / g.topk] : 0.0f;
-              const float mine = v[j] * x, other = __shfl_xor_sync(0xFFFFFFFFu, mine, 1);
-              const float gate = lane & 1 ? other : mine, up = lane & 1 ? mine : other;
-              v[j] = j0 + j < u.n ? gate / (1.0f + __expf(-gate)) * up : 0.0f;
-              const uint32_t m =
-                  __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-              if (lane == 0) h_max[quarter][j] = m;
+            for (int e = 0; e < 4; ++e) {
+              h[e] = gate[e] / (1.0f + __expf(-gate[e])) * up[e];
+              m = max(m, __float_as_uint(h[e]) & 0x7FFFFFFFu);
             }
-            bar_sync(1, 128);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const uint32_t byte = pair_byte(
-                  max(max(h_max[0][j], h_max[1][j]), max(h_max[2][j], h_max[3][j])));
-              const uint32_t p = byte == 255u ? 0u : to_pair(v[j] * mx4::inv_scale(byte));
-              stage_h[j][lane & 1][quarter * 16 + lane / 2] = (uint8_t)(lane & 1 ? p >> 8 : p);
+            for (int o = 8; o; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+            const uint32_t byte = pair_byte(m);
+            const float inv = byte == 255u ? 0.0f : mx4::inv_scale(byte);
+            uint32_t hi = 0, lo = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t p = byte == 255u ? 0u : to_pair(h[e] * inv);
+              hi |= (p & 0xFFu) << (8 * e);
+              lo |= (p >> 8) << (8 * e);
             }
-            if (et < 16 && j0 + et / 2 < u.n) {
-              // scale bytes of hi and lo rows, both blocks of 32 of this tile
-              const int j = et / 2, r = 2 * (j0 + j) + (et & 1), at = u.tile * 64;
-              uint32_t byte = pair_byte(
-                  max(max(h_max[0][j], h_max[1][j]), max(h_max[2][j], h_max[3][j])));
-              if ((et & 1) && byte != 255u) byte -= 4u;
-              *reinterpret_cast<uint16_t*>(
-                  g.h_scales + ((int64_t)u.a * (g.I / 128) + at / 128) * 512 + (r & 31) * 16 +
-                  (r >> 5) * 4 + (at & 127) / 32) = (uint16_t)(byte | byte << 8);
+            if (mine) {
+              uint8_t* out = g.hq + (size_t)(2 * (u.off + j)) * g.I + u.tile * 64 + q * 4;
+              *reinterpret_cast<uint32_t*>(out) = hi;
+              *reinterpret_cast<uint32_t*>(out + g.I) = lo;
+              if (q < 2) {
+                // scale bytes of the hi and the lo row, both blocks of 32 of this tile
+                const int r = 2 * j + q, at = u.tile * 64;
+                const uint32_t by = q && byte != 255u ? byte - 4u : byte;
+                *reinterpret_cast<uint16_t*>(
+                    g.h_scales + ((int64_t)u.a * (g.I / 128) + at / 128) * 512 + (r & 31) * 16 +
+                    (r >> 5) * 4 + (at & 127) / 32) = (uint16_t)(by | by << 8);
+              }
             }
-            bar_sync(1, 128);
-            if (et < 64 && j0 + et / 8 < u.n) {
-              const int j = et / 8, r = (et >> 2) & 1, q = et & 3;
-              *reinterpret_cast<uint4*>(g.hq + (size_t)(2 * (u.off + j0 + j) + r) * g.I +
-                                        u.tile * 64 + q * 16) =
-                  *reinterpret_cast<const uint4*>(&stage_h[j][r][q * 16]);
-            }
+            if (g.splits == 1) bar_sync(1, 128);   // stage_v is free again
           }
         }
         if (g.splits == 1) release();
       } else {
+#pragma unroll 1
         for (int j0 = 0; j0 < u.n; j0 += 8) {
           float v[8];
           read8(j0, v);
@@ -627,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (j0 + j < u.n) {
               const int slot = lists.slot[u.off + j0 + j];
               g.part[((size_t)u.part * slots + slot) * width + u.tile * kRows + row] =
-                  v[j] * g.l.probs[slot];
+                  v[j] * __ldg(&g.probs[slot]);
             }
         }
         release();
@@ -640,19 +711,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         bar_sync(1, 128);
         __threadfence();
+#pragma unroll 1
         for (int j = 0; j < u.n; ++j) {
           const int t = ready[j];
           if (t < 0) continue;
           float y = 0.0f;
-#pragma unroll 8
-          for (int c = 0; c < g.topk * g.splits; ++c)
-            y += __ldcg(&g.part[((size_t)(c % g.splits) * slots + t * g.topk + c / g.splits) *
-                                    width + u.tile * kRows + row]);
+          const float* at = g.part + (size_t)t * g.topk * width + u.tile * kRows + row;
+          for (int p = 0; p < g.splits; ++p) {
+#pragma unroll 4
+            for (int c = 0; c < g.topk; ++c) y += __ldcg(at + (size_t)c * width);
+            at += (size_t)slots * width;
+          }
           g.Y[(size_t)t * width + u.tile * kRows + row] =
               (uint16_t)(pack_bf16x2(y, 0.0f) & 0xFFFFu);
         }
-        bar_sync(1, 128);   // ready is free again
       }
+      bar_sync(1, 128);   // `ready` is free again
     }
   }
   __syncwarp();
@@ -670,6 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_dealloc(tmem, 512);
   }
 }
+#undef WARP_WAIT
 
 // ------------------------------------------------------------------- host ---
 // K parts of a product of `tiles` row tiles of an expected number of experts: the
@@ -695,7 +770,7 @@ static int choose_splits(int64_t T, int64_t E, int topk, int64_t tiles, int64_t 
 }
 
 struct Layout {
-  size_t logits, xq, xs, lists, hq, h_scales, part_up, part_down, counters, total;
+  size_t xq, xs, experts, probs, hq, h_scales, part_up, part_down, counters, total;
   int splits_up, splits_down, max_act, n_up, n_down;
 };
 static Layout layout(int64_t T, int64_t H, int64_t E, int topk, int64_t I) {
@@ -712,10 +787,10 @@ static Layout layout(int64_t T, int64_t H, int64_t E, int topk, int64_t I) {
   l.splits_down = choose_splits(T, E, topk, H / kRows, I);
   l.n_up = (int)(l.max_act * (2 * I / kRows));
   l.n_down = (int)(T * (H / kRows));
-  l.logits = take((size_t)T * E * 8);
   l.xq = take((size_t)T * 2 * H);
   l.xs = take((size_t)T * 4);
-  l.lists = take((1 + (size_t)E + (size_t)E + 1 + 2 * slots) * 4);
+  l.experts = take(slots * 4);
+  l.probs = take(slots * 4);
   l.hq = take(slots * 2 * I);
   l.h_scales = take((size_t)l.max_act * (I / 128) * 512);
   l.part_up = take(l.splits_up > 1 ? (size_t)l.splits_up * slots * 2 * I * 4 : 0);
@@ -772,21 +847,14 @@ cudaError_t launch_moe(const MoeArgs& a, int sm_count, cudaStream_t st) {
   const Layout l = layout(a.T, a.H, a.E, a.topk, a.I);
   uint8_t* w = static_cast<uint8_t*>(a.workspace);
   const int slots = a.T * a.topk;
-  double* logits = reinterpret_cast<double*>(w + l.logits);
   float* xs = reinterpret_cast<float*>(w + l.xs);
   int* counters = reinterpret_cast<int*>(w + l.counters);
-  Lists ls;
-  ls.nact = reinterpret_cast<int*>(w + l.lists);
-  ls.expert = ls.nact + 1;
-  ls.off = ls.expert + a.E;
-  ls.slot_of = ls.off + a.E + 1;
-  ls.probs = reinterpret_cast<float*>(ls.slot_of + slots);
+  int32_t* experts = reinterpret_cast<int32_t*>(w + l.experts);
+  float* probs = reinterpret_cast<float*>(w + l.probs);
 
-  CUtensorMap tw13, tw2, tx, th;
+  CUtensorMap tw13, tw2, th;
   if (!weights_map(&tw13, a.w13_codes, (uint64_t)a.E * 2 * a.I, (uint64_t)a.H) ||
       !weights_map(&tw2, a.w2_codes, (uint64_t)a.E * a.H, (uint64_t)a.I) ||
-      !make_tmap_2d(&tx, w + l.xq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)a.T * 2,
-                    (uint64_t)a.H, 2, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_tmap_2d(&th, w + l.hq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)slots * 2,
                     (uint64_t)a.I, 16, 128, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
@@ -794,10 +862,9 @@ cudaError_t launch_moe(const MoeArgs& a, int sm_count, cudaStream_t st) {
   if (e == cudaSuccess) e = ensure_smem_limit(k_moe_gemm<false>, kMaxDynSmem);
   if (e != cudaSuccess) return e;
 
-  const int logit_blocks =
-      a.T + (a.E + 7) / 8 * ((a.T + kLogitTokens - 1) / kLogitTokens);
-  k_moe_logits<<<logit_blocks, 256, 0, st>>>(a.X, a.T, a.H, a.router, a.E, logits, w + l.xq, xs,
-                                             counters, l.n_up + l.n_down);
+  k_moe_route<<<(a.T + kRouteTokens - 1) / kRouteTokens * kRouteCtas, 256, 0, st>>>(
+      a.X, a.T, a.H, a.router, a.E, a.topk, a.renorm, experts, probs, a.experts, a.probs, w + l.xq,
+      xs, counters, l.n_up + l.n_down);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
 
@@ -808,14 +875,11 @@ cudaError_t launch_moe(const MoeArgs& a, int sm_count, cudaStream_t st) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.stream = st;
-  cfg.gridDim = dim3(1);
-  cfg.blockDim = dim3(1024);
-  e = cudaLaunchKernelEx(&cfg, k_moe_route, (const double*)logits, a.T, a.E, a.topk, a.renorm, ls,
-                         a.experts, a.probs);
-  if (e != cudaSuccess) return e;
-
   GemmArgs g;
-  g.l = ls;
+  g.experts = experts;
+  g.probs = probs;
+  g.E = a.E;
+  g.xq = w + l.xq;
   g.T = a.T;
   g.topk = a.topk;
   g.b_rows = (2 * a.T + 15) / 16 * 16;
@@ -838,7 +902,7 @@ cudaError_t launch_moe(const MoeArgs& a, int sm_count, cudaStream_t st) {
   g.counters = counters;
   int64_t units = (int64_t)l.max_act * g.tiles * g.splits;
   cfg.gridDim = dim3((unsigned)(units < sm_count ? units : sm_count));
-  e = cudaLaunchKernelEx(&cfg, k_moe_gemm<true>, tw13, tx, g);
+  e = cudaLaunchKernelEx(&cfg, k_moe_gemm<true>, tw13, th, g);
   if (e != cudaSuccess) return e;
 
   g.w_scales = a.w2_scales;
