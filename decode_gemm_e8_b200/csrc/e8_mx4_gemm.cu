@@ -48,6 +48,10 @@ __host__ __device__ __forceinline__ int stream_stage_bytes(int bn) {
   return kCodeTile + bn * 128 + 1024 + 1024 * ((bn + 127) / 128);
 }
 
+// A wait of a whole warp, which then agrees on the outcome.
+#define WARP_WAIT(bar, parity, code) \
+  __all_sync(0xFFFFFFFFu, mbar_wait_lazy(bar, parity, &abort_flag, a.status, code))
+
 __global__ void __launch_bounds__(kStreamThreads, 1)
     k_mx4_stream(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA,
                  const __grid_constant__ StreamArgs a) {
@@ -75,6 +79,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     mbar_init(&done, 1);
     abort_flag = 0u;
     fence_mbar_init();
+    tma_prefetch_desc(&tmW);
+    tma_prefetch_desc(&tmA);
   }
   if (warp == 1) {
     tmem_alloc(&tmem_slot, 512);
@@ -83,102 +89,105 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_slot;
+  const uint32_t tmem = __reduce_max_sync(0xFFFFFFFFu, tmem_slot);   // uniform
   if (!a.early) grid_dep_wait();
 
   const uint32_t ring = smem_u32(smem);
+  // the issuing warps run their loops as a whole (uniform registers), one lane issues
   if (warp == 0) {
-    if (lane == 0) {
-      // codes and scales of W
-      tma_prefetch_desc(&tmW);
-      const uint8_t* sf = a.w_scales + ((int64_t)(n0 >> 7) * kqs + 2 * kb0) * 512;
-      uint32_t st = ring, ph = 1;
-      int s = 0;
-      for (int i = 0; i < nkb; ++i) {
-        if (!mbar_wait_lazy(&empty[s], ph, &abort_flag, a.status, kDevTimeoutEmpty)) break;
-        // both 128-column scale tiles of the stage, or the last one alone
-        const uint32_t sb = 2 * (kb0 + i) + 1 < kqs ? 1024u : 512u;
+    // codes and scales of W
+    const uint8_t* sf = a.w_scales + ((int64_t)(n0 >> 7) * kqs + 2 * kb0) * 512;
+    uint32_t st = ring, ph = 1;
+    int s = 0;
+    for (int i = 0; i < nkb; ++i) {
+      if (!WARP_WAIT(&empty[s], ph, kDevTimeoutEmpty)) break;
+      // both 128-column scale tiles of the stage, or the last one alone
+      const uint32_t sb = 2 * (kb0 + i) + 1 < kqs ? 1024u : 512u;
+      if (elect_one()) {
         mbar_arrive_expect_tx(&full[s], (uint32_t)kCodeTile + sb);
         load_2d(st, &tmW, &full[s], (kb0 + i) * 128, n0);
         load_bulk(st + kCodeTile + (uint32_t)a.bn * 128u, sf, sb, &full[s]);
-        sf += 1024;
-        st += (uint32_t)stage_bytes;
-        if (++s == a.stages) {
-          s = 0;
-          ph ^= 1u;
-          st = ring;
-        }
+      }
+      __syncwarp();
+      sf += 1024;
+      st += (uint32_t)stage_bytes;
+      if (++s == a.stages) {
+        s = 0;
+        ph ^= 1u;
+        st = ring;
       }
     }
   } else if (warp == 6) {
-    if (lane == 0) {
-      // codes and scales of the tokens
-      tma_prefetch_desc(&tmA);
-      if (a.early) grid_dep_wait();
-      const int tiles = min(nbt, (a.M - m0 + 127) / 128);
-      const uint8_t* sf = a.a_scales + ((int64_t)(m0 >> 7) * kqs + 2 * kb0) * 512;
-      uint32_t st = ring + kCodeTile, ph = 1;
-      int s = 0;
-      for (int i = 0; i < nkb; ++i) {
-        if (!mbar_wait_lazy(&empty[s], ph, &abort_flag, a.status, kDevTimeoutEmpty)) break;
-        const uint32_t sb = 2 * (kb0 + i) + 1 < kqs ? 1024u : 512u;
+    // codes and scales of the tokens
+    if (a.early) grid_dep_wait();
+    const int tiles = min(nbt, (a.M - m0 + 127) / 128);
+    const uint8_t* sf = a.a_scales + ((int64_t)(m0 >> 7) * kqs + 2 * kb0) * 512;
+    uint32_t st = ring + kCodeTile, ph = 1;
+    int s = 0;
+    for (int i = 0; i < nkb; ++i) {
+      if (!WARP_WAIT(&empty[s], ph, kDevTimeoutEmpty)) break;
+      const uint32_t sb = 2 * (kb0 + i) + 1 < kqs ? 1024u : 512u;
+      if (elect_one()) {
         mbar_arrive_expect_tx(&full[s], (uint32_t)a.bn * 128u + sb * (uint32_t)tiles);
         load_2d(st, &tmA, &full[s], (kb0 + i) * 128, m0);
         const uint32_t to = st + (uint32_t)a.bn * 128u + 1024u;
         load_bulk(to, sf, sb, &full[s]);
         if (tiles > 1) load_bulk(to + 1024u, sf + (size_t)kqs * 512, sb, &full[s]);
-        sf += 1024;
-        st += (uint32_t)stage_bytes;
-        if (++s == a.stages) {
-          s = 0;
-          ph ^= 1u;
-          st = ring + kCodeTile;
-        }
+      }
+      __syncwarp();
+      sf += 1024;
+      st += (uint32_t)stage_bytes;
+      if (++s == a.stages) {
+        s = 0;
+        ph ^= 1u;
+        st = ring + kCodeTile;
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t idesc0 = idesc_mxf4(128, (uint32_t)a.bn, 0),
-                     idesc1 = idesc_mxf4(128, (uint32_t)a.bn, 2);
-      const uint32_t t_off = kCodeTile >> 4, f_off = t_off + (uint32_t)a.bn * 8u;
-      const uint32_t sf_cols = 8u + 8u * (uint32_t)nbt;
-      uint32_t st = ring >> 4, ph = 0, cols = tmem + kSfCol, acc = 0;
-      int s = 0, left = a.K - kb0 * kBK;   // columns from here on
-      for (int i = 0; i < nkb; ++i) {
-        if (!mbar_wait_lazy(&full[s], ph, &abort_flag, a.status, kDevTimeoutFull)) break;
-        tc_fence_after();
-        const uint32_t w = code_desc_lo(st << 4), t = w + t_off;
-        const uint32_t f = scale_desc_lo((st + f_off) << 4);
-        const uint32_t sfb = cols + 8u, half = 4u * (uint32_t)nbt;
-        const int steps = min(4, (left + 63) / 64);   // of 64 columns
-        copy_scales(cols, f);
-        copy_scales(sfb, f + 64u);
-        if (nbt > 1) copy_scales(sfb + 4u, f + 128u);
-        if (steps > 2) {
-          copy_scales(cols + 4u, f + 32u);
-          copy_scales(sfb + half, f + 96u);
-          if (nbt > 1) copy_scales(sfb + half + 4u, f + 160u);
+    const uint32_t idesc0 = idesc_mxf4(128, (uint32_t)a.bn, 0),
+                   idesc1 = idesc_mxf4(128, (uint32_t)a.bn, 2);
+    const uint32_t t_off = kCodeTile >> 4, f_off = t_off + (uint32_t)a.bn * 8u;
+    const uint32_t sf_cols = 8u + 8u * (uint32_t)nbt;
+    uint32_t st = ring >> 4, ph = 0, cols = tmem + kSfCol;
+    int s = 0, left = a.K - kb0 * kBK;   // columns from here on
+    for (int i = 0; i < nkb; ++i) {
+      if (!WARP_WAIT(&full[s], ph, kDevTimeoutFull)) break;
+      tc_fence_after();
+      const int steps = min(4, (left + 63) / 64);   // of 64 columns
+      uint32_t w = code_desc_lo(st << 4), t = w + t_off;
+      uint32_t f = scale_desc_lo((st + f_off) << 4), sfa = cols, acc = i > 0;
+      if (elect_one()) {
+        // 128 columns at a time: their scales, then two MMAs
+#pragma unroll 1
+        for (int q = 0; q < steps; q += 2) {
+          const uint32_t sfb = cols + 8u + (uint32_t)(q * 2 * nbt);
+          copy_scales(sfa, f);
+          copy_scales(sfb, f + 64u);
+          if (nbt > 1) copy_scales(sfb + 4u, f + 128u);
+          mma_mxf4(tmem, code_desc(w), code_desc(t), idesc0, sfa, sfb, acc);
+          if (q + 1 < steps) mma_mxf4(tmem, code_desc(w + 2u), code_desc(t + 2u), idesc1, sfa, sfb, 1);
+          acc = 1;
+          w += 4u;
+          t += 4u;
+          f += 32u;
+          sfa += 4u;
         }
-        mma_mxf4(tmem, code_desc(w), code_desc(t), idesc0, cols, sfb, acc);
-        acc = 1;
-        if (steps > 1) mma_mxf4(tmem, code_desc(w + 2u), code_desc(t + 2u), idesc1, cols, sfb, 1);
-        if (steps > 2)
-          mma_mxf4(tmem, code_desc(w + 4u), code_desc(t + 4u), idesc0, cols + 4u, sfb + half, 1);
-        if (steps > 3)
-          mma_mxf4(tmem, code_desc(w + 6u), code_desc(t + 6u), idesc1, cols + 4u, sfb + half, 1);
         mma_commit(&empty[s]);
-        left -= kBK;
-        st += (uint32_t)stage_bytes >> 4;
-        cols += sf_cols;
-        if (++s == a.stages) {
-          s = 0;
-          ph ^= 1u;
-          st = ring >> 4;
-          cols = tmem + kSfCol;
-        }
       }
-      mma_commit(&done);   // also after a wait that gave up: nothing may be in flight at the end
+      __syncwarp();
+      left -= kBK;
+      st += (uint32_t)stage_bytes >> 4;
+      cols += sf_cols;
+      if (++s == a.stages) {
+        s = 0;
+        ph ^= 1u;
+        st = ring >> 4;
+        cols = tmem + kSfCol;
+      }
     }
+    // also after a wait that gave up: nothing may be in flight at the end
+    if (elect_one()) mma_commit(&done);
+    __syncwarp();
   }
   __syncwarp();
   // every warp: all MMAs of this CTA have finished
