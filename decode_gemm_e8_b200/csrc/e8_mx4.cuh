@@ -116,5 +116,23 @@ __device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t desc_lo) {
                : "memory");
 }
 
+// The same two for a pair of CTAs (cta_group::2): M = 256, each CTA holds 128 rows of
+// A, half the rows of B and all scales its tensor memory needs.
+__device__ __forceinline__ void mma_mxf4_2sm(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                             uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;"
+      "\n\t}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void copy_scales_2sm(uint32_t taddr, uint32_t desc_lo) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr),
+               "l"((uint64_t)((128u >> 4) | (1u << 14)) << 32 | desc_lo)
+               : "memory");
+}
+
 }  // namespace mx4
 }  // namespace e8

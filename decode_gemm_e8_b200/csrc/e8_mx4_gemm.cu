@@ -306,6 +306,290 @@ static cudaError_t launch_stream(const uint8_t* a_codes, const uint8_t* a_scales
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+// ----------------------------------------------------------- many tokens ---
+// A cluster of two CTAs computes 256 x 256 tiles (cta_group::2): each CTA holds 128
+// rows of both operands and loads 35 KB for the 256 columns of a stage, 64 bytes a
+// cycle at the tensor cores' full 4-bit rate, which is about what an SM gets from L2;
+// a one-CTA tile of 128 x 256 would need half as much again.  Persistent; the fp32
+// accumulator takes 256 of the 512 tensor-memory columns and the stages' scales 144,
+// so there is one accumulator: eight epilogue warps take it into registers as bf16
+// (64 a thread), hand it back and store while the next tile's MMAs run.
+//   warp 0      TMA producer of both CTAs; all bytes are counted by the leader
+//   warp 1      tensor memory; in the leader scale copies, MMAs, commits to both CTAs
+//   warps 2-9   epilogue
+namespace pair {
+constexpr int kThreads = 320;
+constexpr int kMaxStages2 = 6;
+constexpr uint32_t kScaleOff = 2 * kCodeTile;
+constexpr uint32_t kStageBytes = 2 * kCodeTile + 1024 + 2048;
+constexpr int kSfCols = 24;
+constexpr int kPitch = 130;                        // elements of a staged row
+constexpr int kStaged = 8 * 32 * kPitch * 2;       // bytes, eight warps
+constexpr uint32_t kPeerBitMask = 0xFEFFFFFFu;     // shared::cluster address -> the even CTA
+}  // namespace pair
+
+struct PairArgs {
+  uint16_t* Y;
+  int M, N, K, stages;
+  uint32_t* status;
+};
+
+__global__ void __launch_bounds__(pair::kThreads, 1)
+    k_mx4_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW,
+               const __grid_constant__ CUtensorMap tmAs, const __grid_constant__ CUtensorMap tmWs,
+               const __grid_constant__ PairArgs a) {
+  using namespace pair;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  __shared__ uint64_t full[kMaxStages2], empty[kMaxStages2], acc_full, acc_empty, drain;
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile uint32_t abort_flag;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)blockIdx.x & 1;
+  const int first = (int)blockIdx.x >> 1, step = (int)gridDim.x >> 1;
+  const int tiles_m = (a.M + 255) / 256, tiles = tiles_m * ((a.N + 255) / 256);
+  const int kblocks = (a.K + kBK - 1) / kBK, kqs = (int)scale_tiles(a.K);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < a.stages; ++s) {
+      mbar_init(&full[s], 1);    // the leader's producer; both CTAs' copies add bytes
+      mbar_init(&empty[s], 1);   // the leader's commit, to both CTAs
+    }
+    mbar_init(&acc_full, 1);
+    mbar_init(&acc_empty, 16);   // eight epilogue warps of each CTA (the leader's is used)
+    mbar_init(&drain, 1);
+    abort_flag = 0u;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmW);
+    tma_prefetch_desc(&tmAs);
+    tma_prefetch_desc(&tmWs);
+  }
+  if (warp == 1) {
+    tmem_alloc_2sm(&tmem_slot, 512);
+    tmem_relinquish_2sm();
+  }
+  // both CTAs' barriers are initialised before any copy or commit reaches them
+  __syncwarp();
+  tc_fence_before();
+  cluster_arrive();
+  cluster_wait();
+  tc_fence_after();
+  grid_dep_wait();
+  const uint32_t tmem = __reduce_max_sync(0xFFFFFFFFu, tmem_slot);   // uniform
+  const uint32_t ring = smem_u32(smem);
+
+  if (warp == 0) {
+    uint32_t st = ring, ph = 1;
+    int s = 0;
+    bool ok = true;
+    for (int tile = first; tile < tiles && ok; tile += step) {
+      const int tn = tile / tiles_m, tm = tile - tn * tiles_m;
+      for (int kb = 0; kb < kblocks; ++kb) {
+        ok = WARP_WAIT(&empty[s], ph, kDevTimeoutEmpty);
+        if (!ok) break;
+        if (elect_one()) {
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2u * kStageBytes);
+          const uint32_t bar = smem_u32(&full[s]) & kPeerBitMask;
+          load_2d_2sm(st, &tmA, bar, kb * 128, tm * 256 + rank * 128);
+          load_2d_2sm(st + kCodeTile, &tmW, bar, kb * 128, tn * 256 + rank * 128);
+          // scale tiles of 128 rows: two 512-byte rows of the map, the stage's columns
+          load_2d_2sm(st + kScaleOff, &tmAs, bar, 0, (tm * 2 + rank) * kqs + 2 * kb);
+          load_2d_2sm(st + kScaleOff + 1024u, &tmWs, bar, 0, tn * 2 * kqs + 2 * kb);
+          load_2d_2sm(st + kScaleOff + 2048u, &tmWs, bar, 0, (tn * 2 + 1) * kqs + 2 * kb);
+        }
+        __syncwarp();
+        st += kStageBytes;
+        if (++s == a.stages) {
+          s = 0;
+          ph ^= 1u;
+          st = ring;
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (rank == 0) {
+      const uint32_t idesc0 = idesc_mxf4(256, 256, 0), idesc1 = idesc_mxf4(256, 256, 2);
+      uint32_t st = ring >> 4, ph = 0, cols = tmem + kSfCol;
+      int s = 0, local = 0;
+      bool ok = true;
+      for (int tile = first; tile < tiles && ok; tile += step, ++local) {
+        ok = WARP_WAIT(&acc_empty, ((uint32_t)local & 1u) ^ 1u, kDevTimeoutMma);
+        if (!ok) break;
+        tc_fence_after();
+        int left = a.K;   // columns from here on
+        for (int kb = 0; kb < kblocks; ++kb) {
+          ok = WARP_WAIT(&full[s], ph, kDevTimeoutFull);
+          if (!ok) break;
+          tc_fence_after();
+          const int steps = min(4, (left + 63) / 64);   // of 64 columns
+          uint32_t x = code_desc_lo(st << 4), w = x + (kCodeTile >> 4);
+          uint32_t f = scale_desc_lo((st << 4) + kScaleOff), sfa = cols, sfb = cols + 8u;
+          uint32_t acc = kb > 0;
+          if (elect_one()) {
+#pragma unroll 1
+            for (int q = 0; q < steps; q += 2) {
+              copy_scales_2sm(sfa, f);
+              copy_scales_2sm(sfb, f + 64u);
+              copy_scales_2sm(sfb + 4u, f + 128u);
+              mma_mxf4_2sm(tmem, code_desc(x), code_desc(w), idesc0, sfa, sfb, acc);
+              if (q + 1 < steps)
+                mma_mxf4_2sm(tmem, code_desc(x + 2u), code_desc(w + 2u), idesc1, sfa, sfb, 1);
+              acc = 1;
+              x += 4u;
+              w += 4u;
+              f += 32u;
+              sfa += 4u;
+              sfb += 8u;
+            }
+            mma_commit_2sm_mc(&empty[s], 0x3);
+          }
+          __syncwarp();
+          left -= kBK;
+          st += kStageBytes >> 4;
+          cols += kSfCols;
+          if (++s == a.stages) {
+            s = 0;
+            ph ^= 1u;
+            st = ring >> 4;
+            cols = tmem + kSfCol;
+          }
+        }
+        if (ok && elect_one()) mma_commit_2sm_mc(&acc_full, 0x3);
+        __syncwarp();
+      }
+      // every MMA of this warp has finished once `drain` flips
+      if (elect_one()) mma_commit_2sm(&drain);
+      __syncwarp();
+      const uint64_t t0 = global_timer_ns();
+      while (!mbar_try_wait(&drain, 0) && global_timer_ns() - t0 < 200000000ull) {
+      }
+    }
+  } else {
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t release = mapa_shared(smem_u32(&acc_empty), 0);
+    const bool vec = (a.N & 7) == 0;
+    uint16_t* staged = reinterpret_cast<uint16_t*>(smem + (size_t)a.stages * kStageBytes) +
+                       (warp - 2) * 32 * kPitch;
+    int local = 0;
+    for (int tile = first; tile < tiles; tile += step, ++local) {
+      if (!WARP_WAIT(&acc_full, (uint32_t)local & 1u, kDevTimeoutMma)) break;
+      tc_fence_after();
+      const int tn = tile / tiles_m, tm = tile - tn * tiles_m;
+      uint32_t v[64];
+#pragma unroll
+      for (int c = 0; c < 128; c += 64) {
+        uint32_t r[64];
+        const uint32_t at = tmem + (uint32_t)(half * 128 + c) + ((uint32_t)(quarter * 32) << 16);
+        tmem_ld32(at, r);
+        tmem_ld32(at + 32u, r + 32);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          v[c / 2 + j] = pack_bf16x2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(release);
+      const int row0 = tm * 256 + rank * 128 + quarter * 32, col0 = tn * 256 + half * 128;
+      if (vec) {
+        uint16_t* y = a.Y + (size_t)(row0 + lane) * a.N + col0;
+        if (row0 + lane < a.M) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (col0 + 8 * j < a.N)
+              *reinterpret_cast<uint4*>(y + 8 * j) =
+                  make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        }
+      } else {
+        // rows of Y start anywhere: through shared memory, so that a warp stores 32
+        // neighbouring values of a row at a time
+#pragma unroll
+        for (int j = 0; j < 64; ++j)
+          reinterpret_cast<uint32_t*>(staged)[lane * (kPitch / 2) + j] = v[j];
+        __syncwarp();
+        const int rows = min(32, a.M - row0);
+        for (int r = 0; r < rows; ++r) {
+          uint16_t* y = a.Y + (size_t)(row0 + r) * a.N + col0;
+#pragma unroll
+          for (int j = 0; j < 128; j += 32)
+            if (col0 + j + lane < a.N) y[j + lane] = staged[r * kPitch + j + lane];
+        }
+        __syncwarp();
+      }
+    }
+  }
+  __syncwarp();
+  if (abort_flag) {
+    // copies in flight may still land: give them time before the CTA exits
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < 1000000ull) {
+    }
+  }
+  // neither CTA frees its tensor memory while the pair's MMAs or the other CTA's
+  // epilogue may still use it
+  __syncwarp();
+  tc_fence_before();
+  cluster_arrive();
+  cluster_wait();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_2sm(tmem, 512);
+  }
+}
+
+// A map of [rows][row_bytes] bytes as 32-bit words: the scale tiles, 512 bytes each.
+static bool scale_map(CUtensorMap* map, const uint8_t* scales, int64_t rows, int64_t K) {
+  return make_tmap_2d(map, scales, CU_TENSOR_MAP_DATA_TYPE_INT32, 4,
+                      (uint64_t)((rows + 127) / 128 * scale_tiles(K)), 128, 2, 128,
+                      CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+static cudaError_t launch_pair(const uint8_t* a_codes, const uint8_t* a_scales, int64_t M,
+                               const uint8_t* w_codes, const uint8_t* w_scales, int64_t N,
+                               int64_t K, uint16_t* Y, uint32_t* status, int sm_count, int early,
+                               cudaStream_t st) {
+  PairArgs a;
+  a.Y = Y;
+  a.M = (int)M;
+  a.N = (int)N;
+  a.K = (int)K;
+  a.status = status;
+  const bool vec = (N & 7) == 0;
+  a.stages = vec ? pair::kMaxStages2 : pair::kMaxStages2 - 2;   // room for staged rows
+  const int64_t cs = code_stride(K);
+  CUtensorMap ta, tw, tas, tws;
+  if (!make_tmap_2d(&ta, a_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)M, (uint64_t)cs, 128,
+                    128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_tmap_2d(&tw, w_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)N, (uint64_t)cs, 128,
+                    128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !scale_map(&tas, a_scales, M, K) || !scale_map(&tws, w_scales, N, K))
+    return cudaErrorInvalidValue;
+  cudaError_t e = ensure_smem_limit(k_mx4_pair, kMaxDynSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = ((M + 255) / 256) * ((N + 255) / 256);
+  const int pairs = (int)(tiles < sm_count / 2 ? tiles : sm_count / 2);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(2 * pairs));
+  cfg.blockDim = dim3(pair::kThreads);
+  cfg.dynamicSmemBytes =
+      1024 + (size_t)a.stages * pair::kStageBytes + (vec ? 0 : (size_t)pair::kStaged);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = early ? 2 : 1;
+  e = cudaLaunchKernelEx(&cfg, k_mx4_pair, ta, tw, tas, tws, a);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 }  // namespace mx4
 
 cudaError_t launch_mx4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int64_t M,
@@ -313,6 +597,12 @@ cudaError_t launch_mx4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int
                             uint16_t* Y, void* ws, uint32_t* status, int sm_count, int early,
                             cudaStream_t st) {
   (void)ws;
+  // The pair kernel where its 256 x 256 tiles occupy at least half the SM pairs.
+  const int64_t tiles = ((M + 255) / 256) * ((N + 255) / 256);
+  const int64_t scale_rows = ((M > N ? M : N) + 127) / 128 * mx4::scale_tiles(K);
+  if (M > 256 && tiles * 4 >= sm_count && scale_rows <= INT32_MAX)
+    return mx4::launch_pair(a_codes, a_scales, M, w_codes, w_scales, N, K, Y, status, sm_count,
+                            early, st);
   return mx4::launch_stream(a_codes, a_scales, M, w_codes, w_scales, N, K, Y, status, sm_count,
                             early, st);
 }
