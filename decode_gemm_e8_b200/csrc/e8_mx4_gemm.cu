@@ -307,24 +307,29 @@ static cudaError_t launch_stream(const uint8_t* a_codes, const uint8_t* a_scales
 }
 
 // ----------------------------------------------------------- many tokens ---
-// A cluster of two CTAs computes 256 x 256 tiles (cta_group::2): each CTA holds 128
-// rows of both operands and loads 35 KB for the 256 columns of a stage, 64 bytes a
-// cycle at the tensor cores' full 4-bit rate, which is about what an SM gets from L2;
-// a one-CTA tile of 128 x 256 would need half as much again.  Persistent; the fp32
+// Two CTAs compute a 256 x 256 tile (cta_group::2): each holds 128 rows of both
+// operands, 35 KB for the 256 columns of a stage, which the tensor cores finish in 512
+// cycles at their full 4-bit rate.  An SM gets about 43 bytes a cycle from L2
+// (measured: 12 TB/s over all SMs), so those bytes alone would take 830 cycles.  With
+// two pairs in a cluster, one below the other, the pairs share the rows of W: every
+// CTA reads half of its 128 rows and multicasts them to its counterpart, 26 KB a stage
+// and CTA from L2.  Persistent; the fp32
 // accumulator takes 256 of the 512 tensor-memory columns and the stages' scales 144,
 // so there is one accumulator: eight epilogue warps take it into registers as bf16
 // (64 a thread), hand it back and store while the next tile's MMAs run.
-//   warp 0      TMA producer of both CTAs; all bytes are counted by the leader
-//   warp 1      tensor memory; in the leader scale copies, MMAs, commits to both CTAs
+//   warp 0      TMA producer of each CTA; a pair's bytes are counted by its leader
+//   warp 1      tensor memory; in the leader scale copies, MMAs, commits: a stage is
+//               free when every pair of the cluster has finished with it
 //   warps 2-9   epilogue
 namespace pair {
 constexpr int kThreads = 320;
-constexpr int kMaxStages2 = 6;
+constexpr int kMaxStages2 = 5;
 constexpr uint32_t kScaleOff = 2 * kCodeTile;
 constexpr uint32_t kStageBytes = 2 * kCodeTile + 1024 + 2048;
 constexpr int kSfCols = 24;
 constexpr int kPitch = 130;                        // elements of a staged row
 constexpr int kStaged = 8 * 32 * kPitch * 2;       // bytes, eight warps
+constexpr int kPieces = 8 * 4096;                  // 32 rows of 128 bytes a warp
 constexpr uint32_t kPeerBitMask = 0xFEFFFFFFu;     // shared::cluster address -> the even CTA
 }  // namespace pair
 
@@ -334,10 +339,11 @@ struct PairArgs {
   uint32_t* status;
 };
 
+template <int PAIRS>
 __global__ void __launch_bounds__(pair::kThreads, 1)
     k_mx4_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW,
                const __grid_constant__ CUtensorMap tmAs, const __grid_constant__ CUtensorMap tmWs,
-               const __grid_constant__ PairArgs a) {
+               const __grid_constant__ CUtensorMap tmY, const __grid_constant__ PairArgs a) {
   using namespace pair;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -347,15 +353,17 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
   __shared__ volatile uint32_t abort_flag;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = (int)blockIdx.x & 1;
-  const int first = (int)blockIdx.x >> 1, step = (int)gridDim.x >> 1;
-  const int tiles_m = (a.M + 255) / 256, tiles = tiles_m * ((a.N + 255) / 256);
+  const int crank = (int)cluster_ctarank(), rank = crank & 1, pr = crank >> 1;
+  const int first = (int)blockIdx.x / (2 * PAIRS), step = (int)gridDim.x / (2 * PAIRS);
+  // tiles of a cluster: PAIRS x 256 rows by 256 columns
+  const int tiles_m = (a.M + 256 * PAIRS - 1) / (256 * PAIRS);
+  const int tiles = tiles_m * ((a.N + 255) / 256);
   const int kblocks = (a.K + kBK - 1) / kBK, kqs = (int)scale_tiles(a.K);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < a.stages; ++s) {
-      mbar_init(&full[s], 1);    // the leader's producer; both CTAs' copies add bytes
-      mbar_init(&empty[s], 1);   // the leader's commit, to both CTAs
+      mbar_init(&full[s], 1);        // the leader's producer; the copies add bytes
+      mbar_init(&empty[s], PAIRS);   // every leader's commit, to all CTAs
     }
     mbar_init(&acc_full, 1);
     mbar_init(&acc_empty, 16);   // eight epilogue warps of each CTA (the leader's is used)
@@ -393,12 +401,23 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
         if (elect_one()) {
           if (rank == 0) mbar_arrive_expect_tx(&full[s], 2u * kStageBytes);
           const uint32_t bar = smem_u32(&full[s]) & kPeerBitMask;
-          load_2d_2sm(st, &tmA, bar, kb * 128, tm * 256 + rank * 128);
-          load_2d_2sm(st + kCodeTile, &tmW, bar, kb * 128, tn * 256 + rank * 128);
+          const int tr = (tm * PAIRS + pr) * 2 + rank;   // this CTA's 128 rows
+          load_2d_2sm(st, &tmA, bar, kb * 128, tr * 128);
           // scale tiles of 128 rows: two 512-byte rows of the map, the stage's columns
-          load_2d_2sm(st + kScaleOff, &tmAs, bar, 0, (tm * 2 + rank) * kqs + 2 * kb);
-          load_2d_2sm(st + kScaleOff + 1024u, &tmWs, bar, 0, tn * 2 * kqs + 2 * kb);
-          load_2d_2sm(st + kScaleOff + 2048u, &tmWs, bar, 0, (tn * 2 + 1) * kqs + 2 * kb);
+          load_2d_2sm(st + kScaleOff, &tmAs, bar, 0, tr * kqs + 2 * kb);
+          if constexpr (PAIRS == 1) {
+            load_2d_2sm(st + kCodeTile, &tmW, bar, kb * 128, tn * 256 + rank * 128);
+            load_2d_2sm(st + kScaleOff + 1024u, &tmWs, bar, 0, tn * 2 * kqs + 2 * kb);
+            load_2d_2sm(st + kScaleOff + 2048u, &tmWs, bar, 0, (tn * 2 + 1) * kqs + 2 * kb);
+          } else {
+            // 64 rows of W for this CTA and its counterpart; W's scales for all four
+            // from the first pair
+            load_2d_2sm_mc(st + kCodeTile + (uint32_t)pr * 8192u, &tmW, bar, kb * 128,
+                           tn * 256 + rank * 128 + pr * 64, (uint16_t)(0x5 << rank));
+            if (pr == 0)
+              load_2d_2sm_mc(st + kScaleOff + 1024u + (uint32_t)rank * 1024u, &tmWs, bar, 0,
+                             (tn * 2 + rank) * kqs + 2 * kb, (uint16_t)0xF);
+          }
         }
         __syncwarp();
         st += kStageBytes;
@@ -444,7 +463,7 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
               sfa += 4u;
               sfb += 8u;
             }
-            mma_commit_2sm_mc(&empty[s], 0x3);
+            mma_commit_2sm_mc(&empty[s], (uint16_t)((1 << (2 * PAIRS)) - 1));
           }
           __syncwarp();
           left -= kBK;
@@ -457,7 +476,7 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
             cols = tmem + kSfCol;
           }
         }
-        if (ok && elect_one()) mma_commit_2sm_mc(&acc_full, 0x3);
+        if (ok && elect_one()) mma_commit_2sm_mc(&acc_full, (uint16_t)(0x3 << (2 * pr)));
         __syncwarp();
       }
       // every MMA of this warp has finished once `drain` flips
@@ -469,8 +488,9 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
     }
   } else {
     const int quarter = warp & 3, half = (warp - 2) >> 2;
-    const uint32_t release = mapa_shared(smem_u32(&acc_empty), 0);
+    const uint32_t release = mapa_shared(smem_u32(&acc_empty), (uint32_t)(2 * pr));
     const bool vec = (a.N & 7) == 0;
+    uint8_t* piece = smem + (size_t)a.stages * kStageBytes + (warp - 2) * 4096;
     uint16_t* staged = reinterpret_cast<uint16_t*>(smem + (size_t)a.stages * kStageBytes) +
                        (warp - 2) * 32 * kPitch;
     int local = 0;
@@ -478,30 +498,36 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
       if (!WARP_WAIT(&acc_full, (uint32_t)local & 1u, kDevTimeoutMma)) break;
       tc_fence_after();
       const int tn = tile / tiles_m, tm = tile - tn * tiles_m;
-      uint32_t v[64];
+      // everything into registers before the first conversion: the accumulator is back
+      // with the MMAs as soon as it is read
+      uint32_t r[128], v[64];
+      const uint32_t at = tmem + (uint32_t)(half * 128) + ((uint32_t)(quarter * 32) << 16);
 #pragma unroll
-      for (int c = 0; c < 128; c += 64) {
-        uint32_t r[64];
-        const uint32_t at = tmem + (uint32_t)(half * 128 + c) + ((uint32_t)(quarter * 32) << 16);
-        tmem_ld32(at, r);
-        tmem_ld32(at + 32u, r + 32);
-        tmem_ld_wait();
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-          v[c / 2 + j] = pack_bf16x2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
-      }
+      for (int c = 0; c < 128; c += 32) tmem_ld32(at + (uint32_t)c, r + c);
+      tmem_ld_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(release);
-      const int row0 = tm * 256 + rank * 128 + quarter * 32, col0 = tn * 256 + half * 128;
-      if (vec) {
-        uint16_t* y = a.Y + (size_t)(row0 + lane) * a.N + col0;
-        if (row0 + lane < a.M) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (col0 + 8 * j < a.N)
-              *reinterpret_cast<uint4*>(y + 8 * j) =
-                  make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+      for (int j = 0; j < 64; ++j)
+        v[j] = pack_bf16x2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+      const int row0 = ((tm * PAIRS + pr) * 2 + rank) * 128 + quarter * 32, col0 = tn * 256 + half * 128;
+      if (vec) {
+        // 64 columns at a time through shared memory (128-byte swizzle) and the TMA unit:
+        // stores of each lane's own row would fill the queue that the barriers and the
+        // MMAs' issue go through
+#pragma unroll
+        for (int c = 0; c < 64; c += 32) {
+          if (lane == 0) bulk_wait_read_all();   // the copy before has left the buffer
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<uint4*>(piece + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+                make_uint4(v[c + 4 * j], v[c + 4 * j + 1], v[c + 4 * j + 2], v[c + 4 * j + 3]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && row0 < a.M && col0 + 2 * c < a.N)
+            tma_store_2d(&tmY, smem_u32(piece), col0 + 2 * c, row0);
         }
       } else {
         // rows of Y start anywhere: through shared memory, so that a warp stores 32
@@ -520,6 +546,7 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
         __syncwarp();
       }
     }
+    if (lane == 0) bulk_wait_all();   // stores read this CTA's shared memory
   }
   __syncwarp();
   if (abort_flag) {
@@ -547,6 +574,26 @@ static bool scale_map(CUtensorMap* map, const uint8_t* scales, int64_t rows, int
                       CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
+// Clusters of this kernel that can be resident at once (kept per device; 0 if the
+// runtime does not say).
+template <int PAIRS>
+static int resident_clusters(cudaLaunchConfig_t cfg, int sm_count) {
+  constexpr int kMaxDev = 64;
+  static int kept[kMaxDev];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return 0;
+  if (kept[dev] > 0) return kept[dev];
+  cfg.gridDim = dim3((unsigned)(sm_count / (2 * PAIRS) * 2 * PAIRS));
+  cfg.dynamicSmemBytes = 1024 + (size_t)pair::kMaxStages2 * pair::kStageBytes + pair::kPieces;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, k_mx4_pair<PAIRS>, &cfg) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return 0;
+  }
+  return kept[dev] = n;
+}
+
+template <int PAIRS>
 static cudaError_t launch_pair(const uint8_t* a_codes, const uint8_t* a_scales, int64_t M,
                                const uint8_t* w_codes, const uint8_t* w_scales, int64_t N,
                                int64_t K, uint16_t* Y, uint32_t* status, int sm_count, int early,
@@ -558,35 +605,39 @@ static cudaError_t launch_pair(const uint8_t* a_codes, const uint8_t* a_scales, 
   a.K = (int)K;
   a.status = status;
   const bool vec = (N & 7) == 0;
-  a.stages = vec ? pair::kMaxStages2 : pair::kMaxStages2 - 2;   // room for staged rows
+  a.stages = vec ? pair::kMaxStages2 : pair::kMaxStages2 - 1;   // room for staged rows
   const int64_t cs = code_stride(K);
-  CUtensorMap ta, tw, tas, tws;
+  CUtensorMap ta, tw, tas, tws, ty = {};
   if (!make_tmap_2d(&ta, a_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)M, (uint64_t)cs, 128,
                     128, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !make_tmap_2d(&tw, w_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)N, (uint64_t)cs, 128,
-                    128, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !scale_map(&tas, a_scales, M, K) || !scale_map(&tws, w_scales, N, K))
+      !make_tmap_2d(&tw, w_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)N, (uint64_t)cs,
+                    128 / PAIRS, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !scale_map(&tas, a_scales, M, K) || !scale_map(&tws, w_scales, N, K) ||
+      (vec && !make_tmap_2d(&ty, Y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, (uint64_t)M, (uint64_t)N,
+                            32, 64, CU_TENSOR_MAP_SWIZZLE_128B)))
     return cudaErrorInvalidValue;
-  cudaError_t e = ensure_smem_limit(k_mx4_pair, kMaxDynSmem);
+  cudaError_t e = ensure_smem_limit(k_mx4_pair<PAIRS>, kMaxDynSmem);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = ((M + 255) / 256) * ((N + 255) / 256);
-  const int pairs = (int)(tiles < sm_count / 2 ? tiles : sm_count / 2);
+  const int64_t tiles = ((M + 256 * PAIRS - 1) / (256 * PAIRS)) * ((N + 255) / 256);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(2 * pairs));
   cfg.blockDim = dim3(pair::kThreads);
   cfg.dynamicSmemBytes =
-      1024 + (size_t)a.stages * pair::kStageBytes + (vec ? 0 : (size_t)pair::kStaged);
+      1024 + (size_t)a.stages * pair::kStageBytes + (size_t)(vec ? pair::kPieces : pair::kStaged);
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.x = 2 * PAIRS;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
+  int clusters = resident_clusters<PAIRS>(cfg, sm_count);
+  if (clusters < 1) clusters = sm_count / (2 * PAIRS);
+  if (tiles < clusters) clusters = (int)tiles;
+  cfg.gridDim = dim3((unsigned)(2 * PAIRS * clusters));
   cfg.numAttrs = early ? 2 : 1;
-  e = cudaLaunchKernelEx(&cfg, k_mx4_pair, ta, tw, tas, tws, a);
+  e = cudaLaunchKernelEx(&cfg, k_mx4_pair<PAIRS>, ta, tw, tas, tws, ty, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -597,12 +648,12 @@ cudaError_t launch_mx4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int
                             uint16_t* Y, void* ws, uint32_t* status, int sm_count, int early,
                             cudaStream_t st) {
   (void)ws;
-  // The pair kernel where its 256 x 256 tiles occupy at least half the SM pairs.
+  // The pair kernel where its 256 x 256 tiles occupy at least a quarter of the SM pairs.
   const int64_t tiles = ((M + 255) / 256) * ((N + 255) / 256);
   const int64_t scale_rows = ((M > N ? M : N) + 127) / 128 * mx4::scale_tiles(K);
-  if (M > 256 && tiles * 4 >= sm_count && scale_rows <= INT32_MAX)
-    return mx4::launch_pair(a_codes, a_scales, M, w_codes, w_scales, N, K, Y, status, sm_count,
-                            early, st);
+  if (M > 256 && tiles * 8 >= sm_count && scale_rows <= INT32_MAX)
+    return mx4::launch_pair<2>(a_codes, a_scales, M, w_codes, w_scales, N, K, Y, status, sm_count,
+                               early, st);
   return mx4::launch_stream(a_codes, a_scales, M, w_codes, w_scales, N, K, Y, status, sm_count,
                             early, st);
 }
