@@ -261,11 +261,6 @@ __device__ __forceinline__ void copy_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
                : "memory");
 }
-// The same value in every lane, known as such to the compiler.
-__device__ __forceinline__ int uniform(int v) {
-  return (int)__reduce_max_sync(0xFFFFFFFFu, (unsigned)v);
-}
-
 // Slots sorted by expert: active expert a (in order of number) has the slots
 // slot[off[a]] .. slot[off[a + 1] - 1], by rising slot.
 struct SharedLists {
@@ -358,14 +353,9 @@ __device__ __forceinline__ Unit unit_at(const GemmArgs& g, const SharedLists& l,
   return r;
 }
 
-// Waits of a whole warp, which then agrees on the outcome.
-#define WARP_WAIT(bar, parity, code) \
-  __all_sync(0xFFFFFFFFu, mbar_wait_lazy(bar, parity, &abort_flag, g.status, code))
-
 // Warps: 0 weights producer, 6 tokens producer, 1 MMAs, 2..5 epilogue.  At 16 KB of
-// weights a stage the SM's share of HBM leaves each role some 700 cycles a stage, so
-// the issuing warps run their loops as a whole (uniform registers) and only the
-// asynchronous instructions are one lane's.
+// weights a stage the SM's share of HBM leaves each role some 700 cycles a stage: one
+// elected thread runs a role's whole loop with its addresses in registers.
 template <bool UP>
 __global__ void __launch_bounds__(kThreads, 1)
     k_moe_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmB,
@@ -419,158 +409,171 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int slots = g.T * g.topk;
   const int units = build_lists(lists, smem, g.experts, slots, g.E) * g.tiles * g.splits;
   tc_fence_after();
-  const uint32_t tmem = (uint32_t)uniform((int)tmem_slot);
+  const uint32_t tmem = tmem_slot;
   const uint32_t ring = smem_u32(smem);
   const int kqs = g.K / kBK;
 
   if (warp == 0) {
-    // codes and scales of the weights; they do not depend on the preceding kernel
-    uint32_t st = ring, ph = 1;
-    int s = 0;
-    bool ok = true;
-    for (int i = blockIdx.x; i < units && ok; i += gridDim.x) {
-      const Unit u = unit_at(g, lists, i);
-      const int row = (uniform(u.expert) * g.tiles + u.tile) * kRows;
-      const uint8_t* sf = g.w_scales + ((int64_t)(row >> 7) * kqs + u.k0) * 512;
-      int x = u.k0 * kBK;
-      for (int k = u.nk; k > 0; k -= 2) {
-        ok = WARP_WAIT(&empty[s], ph, kDevTimeoutEmpty);
-        if (!ok) break;
-        const uint32_t half = k > 1 ? 2u : 1u;
-        if (elect_one()) {
+    if (elect_one()) {
+      // codes and scales of the weights; they do not depend on the preceding kernel
+      uint32_t st = ring, ph = 1;
+      int s = 0;
+      bool ok = true;
+      for (int i = blockIdx.x; i < units && ok; i += gridDim.x) {
+        const Unit u = unit_at(g, lists, i);
+        const int row = (u.expert * g.tiles + u.tile) * kRows;
+        const uint8_t* sf = g.w_scales + ((int64_t)(row >> 7) * kqs + u.k0) * 512;
+        int x = u.k0 * kBK;
+        for (int k = u.nk; k > 0; k -= 2) {
+          ok = mbar_wait_lazy(&empty[s], ph, &abort_flag, g.status, kDevTimeoutEmpty);
+          if (!ok) break;
           // the tensor map unpacks: its bytes are counted as they lie in memory
+          const uint32_t half = k > 1 ? 2u : 1u;
           mbar_arrive_expect_tx(&full[s], half * (kWBytes / 2 + 512u));
           load_2d(st, &tmW, &full[s], x, row);
           if (k > 1) load_2d(st + kWBytes, &tmW, &full[s], x + kBK, row);
           load_bulk(st + 2u * (kWBytes + b_bytes), sf, half * 512u, &full[s]);
-        }
-        __syncwarp();
-        x += 2 * kBK;
-        sf += 1024;
-        st += stage_bytes;
-        if (++s == g.stages) {
-          s = 0;
-          ph ^= 1u;
-          st = ring;
+          x += 2 * kBK;
+          sf += 1024;
+          st += stage_bytes;
+          if (++s == g.stages) {
+            s = 0;
+            ph ^= 1u;
+            st = ring;
+          }
         }
       }
     }
   } else if (warp == 6) {
-    uint32_t st = ring + 2u * kWBytes, ph = 1;
-    int s = 0;
-    bool ok = true;
-    if (!UP) grid_dep_wait();
-    for (int i = blockIdx.x; i < units && ok; i += gridDim.x) {
-      const Unit u = unit_at(g, lists, i);
-      const int n = uniform(u.n), off = uniform(u.off);
-      int x = u.k0 * kBK;
-      // up: tokens lie in order of the batch; 16 lanes copy the 256 bytes of each of
-      // a token's two rows, 16 bytes a lane, to where the 128-byte swizzle has them
+    if (!UP) {
+      // sorted by expert: sixteen rows a copy
+      grid_dep_wait();
+      if (elect_one()) {
+        uint32_t st = ring + 2u * kWBytes, ph = 1;
+        int s = 0;
+        bool ok = true;
+        for (int i = blockIdx.x; i < units && ok; i += gridDim.x) {
+          const Unit u = unit_at(g, lists, i);
+          const uint8_t* sf = g.h_scales + ((int64_t)u.a * kqs + u.k0) * 512;
+          const uint32_t copies = (uint32_t)(u.n + 7) / 8;
+          int x = u.k0 * kBK;
+          for (int k = u.nk; k > 0; k -= 2) {
+            ok = mbar_wait_lazy(&empty[s], ph, &abort_flag, g.status, kDevTimeoutEmpty);
+            if (!ok) break;
+            const uint32_t half = k > 1 ? 2u : 1u;
+            mbar_arrive_expect_tx(&full[s], half * (copies * 2048u + 512u));
+            for (uint32_t q = 0; q < copies; ++q) {
+              load_2d(st + q * 2048u, &tmB, &full[s], x, 2 * u.off + (int)q * 16);
+              if (k > 1)
+                load_2d(st + b_bytes + q * 2048u, &tmB, &full[s], x + kBK, 2 * u.off + (int)q * 16);
+            }
+            load_bulk(st + 2u * b_bytes + 1024u, sf, half * 512u, &full[s]);
+            x += 2 * kBK;
+            sf += 1024;
+            st += stage_bytes;
+            if (++s == g.stages) {
+              s = 0;
+              ph ^= 1u;
+              st = ring + 2u * kWBytes;
+            }
+          }
+        }
+      }
+    } else {
+      // tokens lie in order of the batch; 16 lanes copy the 256 bytes of each of a
+      // token's two rows, 16 bytes a lane, to where the 128-byte swizzle has them
       const int r = lane >> 4, c = lane & 15;
       const uint8_t* src = g.xq + (size_t)r * g.K + c * 16;
       const uint32_t to = (c >> 3) * b_bytes + (uint32_t)r * 128u;
-      const uint8_t* sf = g.h_scales + ((int64_t)u.a * kqs + u.k0) * 512;
-      for (int k = u.nk; k > 0; k -= 2) {
-        ok = WARP_WAIT(&empty[s], ph, kDevTimeoutEmpty);
-        if (!ok) break;
-        if (UP) {
+      uint32_t st = ring + 2u * kWBytes, ph = 1;
+      int s = 0;
+      bool ok = true;
+      for (int i = blockIdx.x; i < units && ok; i += gridDim.x) {
+        const Unit u = unit_at(g, lists, i);
+        int x = u.k0 * kBK;
+        for (int k = u.nk; k > 0; k -= 2) {
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait_lazy(&empty[s], ph, &abort_flag, g.status,
+                                                      kDevTimeoutEmpty));
+          if (!ok) break;
           if (k > 1 || c < 8) {
 #pragma unroll 2
-            for (int j = 0; j < n; ++j) {
-              const int t = lists.slot[off + j] / g.topk;
+            for (int j = 0; j < u.n; ++j) {
+              const int t = lists.slot[u.off + j] / g.topk;
               copy_async16(st + to + (uint32_t)j * 256u +
                                (uint32_t)(((c & 7) ^ ((2 * j + r) & 7)) << 4),
                            src + (size_t)t * 2 * g.K + x);
             }
           }
           copy_async_arrive(&full[s]);
-        } else {
-          // down: sorted by expert, sixteen rows a copy
-          const uint32_t half = k > 1 ? 2u : 1u, copies = (uint32_t)(n + 7) / 8;
-          if (elect_one()) {
-            mbar_arrive_expect_tx(&full[s], half * (copies * 2048u + 512u));
-            for (uint32_t q = 0; q < copies; ++q) {
-              load_2d(st + q * 2048u, &tmB, &full[s], x, 2 * off + (int)q * 16);
-              if (k > 1)
-                load_2d(st + b_bytes + q * 2048u, &tmB, &full[s], x + kBK, 2 * off + (int)q * 16);
-            }
-            load_bulk(st + 2u * b_bytes + 1024u, sf, half * 512u, &full[s]);
+          x += 2 * kBK;
+          st += stage_bytes;
+          if (++s == g.stages) {
+            s = 0;
+            ph ^= 1u;
+            st = ring + 2u * kWBytes;
           }
-          __syncwarp();
-        }
-        x += 2 * kBK;
-        sf += 1024;
-        st += stage_bytes;
-        if (++s == g.stages) {
-          s = 0;
-          ph ^= 1u;
-          st = ring + 2u * kWBytes;
         }
       }
     }
   } else if (warp == 1) {
-    const uint32_t b_off = 2u * kWBytes >> 4, f_off = 2u * (kWBytes + b_bytes) >> 4;
-    uint32_t st = ring >> 4, ph = 0, cols = tmem + kSfCol;
-    int s = 0, local = 0;
-    bool ok = true;
-    if (UP && elect_one())
-      mx4::copy_scales(tmem + kConstCol, mx4::scale_desc_lo(smem_u32(const_sf)));
-    __syncwarp();
-    for (int i = blockIdx.x; i < units && ok; i += gridDim.x, ++local) {
-      const Unit u = unit_at(g, lists, i);
-      const int buf = local & 1;
-      ok = WARP_WAIT(&acc_empty[buf], ((uint32_t)(local >> 1) & 1u) ^ 1u, kDevTimeoutMma);
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t d = tmem + (uint32_t)buf * 128u;
-      const uint32_t idesc = mx4::idesc_mxf4_f8(128, (uint32_t)(uniform(u.n) + 7) / 8 * 16, 0);
-      for (int k = u.nk; k > 0; k -= 2) {
-        ok = WARP_WAIT(&full[s], ph, kDevTimeoutFull);
-        if (!ok) break;
+    if (elect_one()) {
+      const uint32_t b_off = 2u * kWBytes >> 4, f_off = 2u * (kWBytes + b_bytes) >> 4;
+      uint32_t st = ring >> 4, ph = 0, cols = tmem + kSfCol;
+      int s = 0, local = 0;
+      bool ok = true;
+      if (UP) mx4::copy_scales(tmem + kConstCol, mx4::scale_desc_lo(smem_u32(const_sf)));
+      for (int i = blockIdx.x; i < units && ok; i += gridDim.x, ++local) {
+        const Unit u = unit_at(g, lists, i);
+        const int buf = local & 1;
+        if (!mbar_wait_lazy(&acc_empty[buf], ((uint32_t)(local >> 1) & 1u) ^ 1u, &abort_flag,
+                            g.status, kDevTimeoutMma))
+          break;
         tc_fence_after();
-        if (UP) fence_proxy_async_smem();   // the tokens' rows came by ordinary copies
-        uint32_t w = mx4::code_desc_lo(st << 4), b = w + b_off;
-        const uint32_t f = mx4::scale_desc_lo((st + f_off) << 4);
-        uint32_t acc = k < u.nk;
-        if (elect_one()) {
+        const uint32_t d = tmem + (uint32_t)buf * 128u;
+        const uint32_t idesc = mx4::idesc_mxf4_f8(128, (uint32_t)(u.n + 7) / 8 * 16, 0);
+        for (int k = u.nk; k > 0; k -= 2) {
+          ok = mbar_wait_lazy(&full[s], ph, &abort_flag, g.status, kDevTimeoutFull);
+          if (!ok) break;
+          tc_fence_after();
+          if (UP) fence_proxy_async_smem();   // the tokens' rows came by ordinary copies
+          const uint32_t w = mx4::code_desc_lo(st << 4), b = w + b_off;
+          const uint32_t w1 = w + (kWBytes >> 4), b1 = b + (b_bytes >> 4);
+          const uint32_t f = mx4::scale_desc_lo((st + f_off) << 4);
+          const uint32_t sfb = UP ? tmem + kConstCol : cols + 8u, sfb1 = UP ? sfb : sfb + 4u;
           mx4::copy_scales(cols, f);
-          if (!UP) mx4::copy_scales(cols + 8u, f + 64u);
+          if (!UP) mx4::copy_scales(sfb, f + 64u);
           if (k > 1) {
             mx4::copy_scales(cols + 4u, f + 32u);
-            if (!UP) mx4::copy_scales(cols + 12u, f + 96u);
+            if (!UP) mx4::copy_scales(sfb1, f + 96u);
           }
-#pragma unroll 1
-          for (uint32_t h = 0; h < (k > 1 ? 8u : 4u); h += 4) {
-            const uint32_t sfb = UP ? tmem + kConstCol : cols + 8u + h;
 #pragma unroll
-            for (uint32_t j = 0; j < 4; ++j) {
-              mx4::mma_mxf8f6f4(d, mx4::code_desc(w + 2u * j), mx4::code_desc(b + 2u * j),
-                                idesc | (j << 4) | (j << 29), cols + h, sfb, acc);
-              acc = 1;
-            }
-            w += kWBytes >> 4;
-            b += b_bytes >> 4;
+          for (uint32_t j = 0; j < 4; ++j)
+            mx4::mma_mxf8f6f4(d, mx4::code_desc(w + 2u * j), mx4::code_desc(b + 2u * j),
+                              idesc | (j << 4) | (j << 29), cols, sfb,
+                              (k < u.nk || j > 0) ? 1u : 0u);
+          if (k > 1) {
+#pragma unroll
+            for (uint32_t j = 0; j < 4; ++j)
+              mx4::mma_mxf8f6f4(d, mx4::code_desc(w1 + 2u * j), mx4::code_desc(b1 + 2u * j),
+                                idesc | (j << 4) | (j << 29), cols + 4u, sfb1, 1);
           }
           mma_commit(&empty[s]);
+          st += stage_bytes >> 4;
+          cols += 16u;
+          if (++s == g.stages) {
+            s = 0;
+            ph ^= 1u;
+            st = ring >> 4;
+            cols = tmem + kSfCol;
+          }
         }
-        __syncwarp();
-        st += stage_bytes >> 4;
-        cols += 16u;
-        if (++s == g.stages) {
-          s = 0;
-          ph ^= 1u;
-          st = ring >> 4;
-          cols = tmem + kSfCol;
-        }
+        if (ok) mma_commit(&acc_full[buf]);
       }
-      if (ok && elect_one()) mma_commit(&acc_full[buf]);
-      __syncwarp();
-    }
-    // every MMA of this warp has finished once `drain` flips
-    if (elect_one()) mma_commit(&drain);
-    __syncwarp();
-    const uint64_t t0 = global_timer_ns();
-    while (!mbar_try_wait(&drain, 0) && global_timer_ns() - t0 < 200000000ull) {
+      // every MMA of this thread has finished once `drain` flips
+      mma_commit(&drain);
+      const uint64_t t0 = global_timer_ns();
+      while (!mbar_try_wait(&drain, 0) && global_timer_ns() - t0 < 200000000ull) {
+      }
     }
   } else {
     const int quarter = warp & 3, row = quarter * 32 + lane, et = (int)threadIdx.x - 64;
@@ -744,8 +747,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_dealloc(tmem, 512);
   }
 }
-#undef WARP_WAIT
-
 // ------------------------------------------------------------------- host ---
 // K parts of a product of `tiles` row tiles of an expected number of experts: the
 // rounds of units over the SMs, each as long as its share of K and about four

@@ -60,6 +60,9 @@ __device__ __forceinline__ float code_value(uint32_t c) {
 }
 
 // ------------------------------------------------------- tensor cores ---
+// Their callers run in a branch that elect.sync chose the thread of: under any other
+// condition the compiler has to serve several threads, at some 40 cycles an
+// instruction (measured; 9 a scale copy and the tensor cores' own time an MMA here).
 // Instruction descriptor of tcgen05.mma.kind::mxf4: e2m1 A and B (both K-major),
 // ue8m0 scales, fp32 accumulator, K = 64.  sf: which pair of the four scale
 // bytes of a 32-bit tensor-memory column this step takes (0 or 2), for A and B.
@@ -111,7 +114,8 @@ __device__ __forceinline__ uint32_t scale_desc_lo(uint32_t smem) {
 // One 512-byte scale tile (32 lanes of 16 bytes) into four columns of tensor
 // memory, repeated in all four lane quarters.
 __device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t desc_lo) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr),
+  asm volatile(
+      "tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr),
                "l"((uint64_t)((128u >> 4) | (1u << 14)) << 32 | desc_lo)
                : "memory");
 }
@@ -129,7 +133,8 @@ __device__ __forceinline__ void mma_mxf4_2sm(uint32_t d_tmem, uint64_t a_desc, u
       : "memory");
 }
 __device__ __forceinline__ void copy_scales_2sm(uint32_t taddr, uint32_t desc_lo) {
-  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr),
+  asm volatile(
+      "tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr),
                "l"((uint64_t)((128u >> 4) | (1u << 14)) << 32 | desc_lo)
                : "memory");
 }

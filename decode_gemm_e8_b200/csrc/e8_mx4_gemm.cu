@@ -48,10 +48,6 @@ __host__ __device__ __forceinline__ int stream_stage_bytes(int bn) {
   return kCodeTile + bn * 128 + 1024 + 1024 * ((bn + 127) / 128);
 }
 
-// A wait of a whole warp, which then agrees on the outcome.
-#define WARP_WAIT(bar, parity, code) \
-  __all_sync(0xFFFFFFFFu, mbar_wait_lazy(bar, parity, &abort_flag, a.status, code))
-
 __global__ void __launch_bounds__(kStreamThreads, 1)
     k_mx4_stream(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA,
                  const __grid_constant__ StreamArgs a) {
@@ -89,105 +85,98 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = __reduce_max_sync(0xFFFFFFFFu, tmem_slot);   // uniform
+  const uint32_t tmem = tmem_slot;
   if (!a.early) grid_dep_wait();
 
   const uint32_t ring = smem_u32(smem);
-  // the issuing warps run their loops as a whole (uniform registers), one lane issues
   if (warp == 0) {
-    // codes and scales of W
-    const uint8_t* sf = a.w_scales + ((int64_t)(n0 >> 7) * kqs + 2 * kb0) * 512;
-    uint32_t st = ring, ph = 1;
-    int s = 0;
-    for (int i = 0; i < nkb; ++i) {
-      if (!WARP_WAIT(&empty[s], ph, kDevTimeoutEmpty)) break;
-      // both 128-column scale tiles of the stage, or the last one alone
-      const uint32_t sb = 2 * (kb0 + i) + 1 < kqs ? 1024u : 512u;
-      if (elect_one()) {
+    if (elect_one()) {
+      // codes and scales of W
+      const uint8_t* sf = a.w_scales + ((int64_t)(n0 >> 7) * kqs + 2 * kb0) * 512;
+      uint32_t st = ring, ph = 1;
+      int s = 0;
+      for (int i = 0; i < nkb; ++i) {
+        if (!mbar_wait_lazy(&empty[s], ph, &abort_flag, a.status, kDevTimeoutEmpty)) break;
+        // both 128-column scale tiles of the stage, or the last one alone
+        const uint32_t sb = 2 * (kb0 + i) + 1 < kqs ? 1024u : 512u;
         mbar_arrive_expect_tx(&full[s], (uint32_t)kCodeTile + sb);
         load_2d(st, &tmW, &full[s], (kb0 + i) * 128, n0);
         load_bulk(st + kCodeTile + (uint32_t)a.bn * 128u, sf, sb, &full[s]);
-      }
-      __syncwarp();
-      sf += 1024;
-      st += (uint32_t)stage_bytes;
-      if (++s == a.stages) {
-        s = 0;
-        ph ^= 1u;
-        st = ring;
+        sf += 1024;
+        st += (uint32_t)stage_bytes;
+        if (++s == a.stages) {
+          s = 0;
+          ph ^= 1u;
+          st = ring;
+        }
       }
     }
   } else if (warp == 6) {
-    // codes and scales of the tokens
     if (a.early) grid_dep_wait();
-    const int tiles = min(nbt, (a.M - m0 + 127) / 128);
-    const uint8_t* sf = a.a_scales + ((int64_t)(m0 >> 7) * kqs + 2 * kb0) * 512;
-    uint32_t st = ring + kCodeTile, ph = 1;
-    int s = 0;
-    for (int i = 0; i < nkb; ++i) {
-      if (!WARP_WAIT(&empty[s], ph, kDevTimeoutEmpty)) break;
-      const uint32_t sb = 2 * (kb0 + i) + 1 < kqs ? 1024u : 512u;
-      if (elect_one()) {
+    if (elect_one()) {
+      // codes and scales of the tokens
+      const int tiles = min(nbt, (a.M - m0 + 127) / 128);
+      const uint8_t* sf = a.a_scales + ((int64_t)(m0 >> 7) * kqs + 2 * kb0) * 512;
+      uint32_t st = ring + kCodeTile, ph = 1;
+      int s = 0;
+      for (int i = 0; i < nkb; ++i) {
+        if (!mbar_wait_lazy(&empty[s], ph, &abort_flag, a.status, kDevTimeoutEmpty)) break;
+        const uint32_t sb = 2 * (kb0 + i) + 1 < kqs ? 1024u : 512u;
         mbar_arrive_expect_tx(&full[s], (uint32_t)a.bn * 128u + sb * (uint32_t)tiles);
         load_2d(st, &tmA, &full[s], (kb0 + i) * 128, m0);
         const uint32_t to = st + (uint32_t)a.bn * 128u + 1024u;
         load_bulk(to, sf, sb, &full[s]);
         if (tiles > 1) load_bulk(to + 1024u, sf + (size_t)kqs * 512, sb, &full[s]);
-      }
-      __syncwarp();
-      sf += 1024;
-      st += (uint32_t)stage_bytes;
-      if (++s == a.stages) {
-        s = 0;
-        ph ^= 1u;
-        st = ring + kCodeTile;
+        sf += 1024;
+        st += (uint32_t)stage_bytes;
+        if (++s == a.stages) {
+          s = 0;
+          ph ^= 1u;
+          st = ring + kCodeTile;
+        }
       }
     }
   } else if (warp == 1) {
-    const uint32_t idesc0 = idesc_mxf4(128, (uint32_t)a.bn, 0),
-                   idesc1 = idesc_mxf4(128, (uint32_t)a.bn, 2);
-    const uint32_t t_off = kCodeTile >> 4, f_off = t_off + (uint32_t)a.bn * 8u;
-    const uint32_t sf_cols = 8u + 8u * (uint32_t)nbt;
-    uint32_t st = ring >> 4, ph = 0, cols = tmem + kSfCol;
-    int s = 0, left = a.K - kb0 * kBK;   // columns from here on
-    for (int i = 0; i < nkb; ++i) {
-      if (!WARP_WAIT(&full[s], ph, kDevTimeoutFull)) break;
-      tc_fence_after();
-      const int steps = min(4, (left + 63) / 64);   // of 64 columns
-      uint32_t w = code_desc_lo(st << 4), t = w + t_off;
-      uint32_t f = scale_desc_lo((st + f_off) << 4), sfa = cols, acc = i > 0;
-      if (elect_one()) {
-        // 128 columns at a time: their scales, then two MMAs
-#pragma unroll 1
-        for (int q = 0; q < steps; q += 2) {
-          const uint32_t sfb = cols + 8u + (uint32_t)(q * 2 * nbt);
-          copy_scales(sfa, f);
-          copy_scales(sfb, f + 64u);
-          if (nbt > 1) copy_scales(sfb + 4u, f + 128u);
-          mma_mxf4(tmem, code_desc(w), code_desc(t), idesc0, sfa, sfb, acc);
-          if (q + 1 < steps) mma_mxf4(tmem, code_desc(w + 2u), code_desc(t + 2u), idesc1, sfa, sfb, 1);
-          acc = 1;
-          w += 4u;
-          t += 4u;
-          f += 32u;
-          sfa += 4u;
+    if (elect_one()) {
+      const uint32_t idesc0 = idesc_mxf4(128, (uint32_t)a.bn, 0),
+                     idesc1 = idesc_mxf4(128, (uint32_t)a.bn, 2);
+      const uint32_t t_off = kCodeTile >> 4, f_off = t_off + (uint32_t)a.bn * 8u;
+      const uint32_t sf_cols = 8u + 8u * (uint32_t)nbt, half = 4u * (uint32_t)nbt;
+      uint32_t st = ring >> 4, ph = 0, cols = tmem + kSfCol;
+      int s = 0, left = a.K - kb0 * kBK;   // columns from here on
+      for (int i = 0; i < nkb; ++i) {
+        if (!mbar_wait_lazy(&full[s], ph, &abort_flag, a.status, kDevTimeoutFull)) break;
+        tc_fence_after();
+        const uint32_t w = code_desc_lo(st << 4), t = w + t_off;
+        const uint32_t f = scale_desc_lo((st + f_off) << 4), sfb = cols + 8u;
+        // 64 columns an MMA; a scale tile serves two
+        copy_scales(cols, f);
+        copy_scales(sfb, f + 64u);
+        if (nbt > 1) copy_scales(sfb + 4u, f + 128u);
+        if (left > 128) {
+          copy_scales(cols + 4u, f + 32u);
+          copy_scales(sfb + half, f + 96u);
+          if (nbt > 1) copy_scales(sfb + half + 4u, f + 160u);
         }
+        mma_mxf4(tmem, code_desc(w), code_desc(t), idesc0, cols, sfb, i > 0);
+        if (left > 64) mma_mxf4(tmem, code_desc(w + 2u), code_desc(t + 2u), idesc1, cols, sfb, 1);
+        if (left > 128)
+          mma_mxf4(tmem, code_desc(w + 4u), code_desc(t + 4u), idesc0, cols + 4u, sfb + half, 1);
+        if (left > 192)
+          mma_mxf4(tmem, code_desc(w + 6u), code_desc(t + 6u), idesc1, cols + 4u, sfb + half, 1);
         mma_commit(&empty[s]);
+        left -= kBK;
+        st += (uint32_t)stage_bytes >> 4;
+        cols += sf_cols;
+        if (++s == a.stages) {
+          s = 0;
+          ph ^= 1u;
+          st = ring >> 4;
+          cols = tmem + kSfCol;
+        }
       }
-      __syncwarp();
-      left -= kBK;
-      st += (uint32_t)stage_bytes >> 4;
-      cols += sf_cols;
-      if (++s == a.stages) {
-        s = 0;
-        ph ^= 1u;
-        st = ring >> 4;
-        cols = tmem + kSfCol;
-      }
+      mma_commit(&done);   // also after a wait that gave up: nothing may be in flight at the end
     }
-    // also after a wait that gave up: nothing may be in flight at the end
-    if (elect_one()) mma_commit(&done);
-    __syncwarp();
   }
   __syncwarp();
   // every warp: all MMAs of this CTA have finished
@@ -307,39 +296,44 @@ static cudaError_t launch_stream(const uint8_t* a_codes, const uint8_t* a_scales
 }
 
 // ----------------------------------------------------------- many tokens ---
-// Two CTAs compute a 256 x 256 tile (cta_group::2): each holds 128 rows of both
-// operands, 35 KB for the 256 columns of a stage, which the tensor cores finish in 512
-// cycles at their full 4-bit rate.  An SM gets about 43 bytes a cycle from L2
-// (measured: 12 TB/s over all SMs), so those bytes alone would take 830 cycles.  With
-// two pairs in a cluster, one below the other, the pairs share the rows of W: every
-// CTA reads half of its 128 rows and multicasts them to its counterpart, 26 KB a stage
-// and CTA from L2.  Persistent; the fp32
-// accumulator takes 256 of the 512 tensor-memory columns and the stages' scales 144,
-// so there is one accumulator: eight epilogue warps take it into registers as bf16
-// (64 a thread), hand it back and store while the next tile's MMAs run.
+// Two CTAs compute a 256 x 192 tile (cta_group::2), each holding 128 rows of A and 96
+// of W; a cluster of two such pairs side by side a tile of 256 x 384.
+//   Why 192 columns: reading an fp32 accumulator of 128 x 256 out of tensor memory
+//   takes an SM about 2000 cycles, a fifth of the 16 stages of K = 4096, so it has to
+//   overlap the next tile's MMAs; two accumulators of 192 columns (384) and the scales
+//   of five stages (120) fit the 512 columns, two of 256 do not.
+//   Why two pairs: an SM gets about 43 bytes a cycle from L2 (measured: 12 TB/s over
+//   all SMs); a stage's MMAs take about 480 cycles (four of 256 x 192 x 64 at the 160
+//   cycles for N = 256 that they were measured to take), and its 30 KB would take 700.
+//   The pairs share the rows of A: every CTA reads half of its 128 rows and multicasts
+//   them to its counterpart, 22 KB a stage and CTA from L2.
+// Persistent.
 //   warp 0      TMA producer of each CTA; a pair's bytes are counted by its leader
 //   warp 1      tensor memory; in the leader scale copies, MMAs, commits: a stage is
-//               free when every pair of the cluster has finished with it
-//   warps 2-9   epilogue
+//               free when both pairs of the cluster have finished with it
+//   warps 2-9   epilogue: 64 columns at a time to bf16, shared memory and TMA stores
 namespace pair {
 constexpr int kThreads = 320;
-constexpr int kMaxStages2 = 5;
-constexpr uint32_t kScaleOff = 2 * kCodeTile;
-constexpr uint32_t kStageBytes = 2 * kCodeTile + 1024 + 2048;
-constexpr int kSfCols = 24;
-constexpr int kPitch = 130;                        // elements of a staged row
-constexpr int kStaged = 8 * 32 * kPitch * 2;       // bytes, eight warps
-constexpr int kPieces = 8 * 4096;                  // 32 rows of 128 bytes a warp
+constexpr int kPairs = 2, kCtas = 2 * kPairs;
+constexpr int kN = 192;                            // columns of a pair's tile
+constexpr int kStages = 5;
+constexpr uint32_t kWTile = kN / 2 * 128;
+constexpr uint32_t kScaleOff = kCodeTile + kWTile;
+constexpr uint32_t kStageBytes = kScaleOff + 1024 + 2048;
+constexpr int kSfCol0 = 2 * kN, kSfCols = 24;
+constexpr int kPitch = 66;                         // elements of a staged row
+constexpr int kStaged = 8 * 4352;                  // bytes, a piece of each epilogue warp
 constexpr uint32_t kPeerBitMask = 0xFEFFFFFFu;     // shared::cluster address -> the even CTA
+static_assert(kSfCol0 + kStages * kSfCols <= 512, "tensor memory");
+static_assert(32 * kPitch * 2 <= 4352, "staging");
 }  // namespace pair
 
 struct PairArgs {
   uint16_t* Y;
-  int M, N, K, stages;
+  int M, N, K;
   uint32_t* status;
 };
 
-template <int PAIRS>
 __global__ void __launch_bounds__(pair::kThreads, 1)
     k_mx4_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW,
                const __grid_constant__ CUtensorMap tmAs, const __grid_constant__ CUtensorMap tmWs,
@@ -348,25 +342,26 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  __shared__ uint64_t full[kMaxStages2], empty[kMaxStages2], acc_full, acc_empty, drain;
+  __shared__ uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drain;
   __shared__ uint32_t tmem_slot;
   __shared__ volatile uint32_t abort_flag;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int crank = (int)cluster_ctarank(), rank = crank & 1, pr = crank >> 1;
-  const int first = (int)blockIdx.x / (2 * PAIRS), step = (int)gridDim.x / (2 * PAIRS);
-  // tiles of a cluster: PAIRS x 256 rows by 256 columns
-  const int tiles_m = (a.M + 256 * PAIRS - 1) / (256 * PAIRS);
-  const int tiles = tiles_m * ((a.N + 255) / 256);
+  const int first = (int)blockIdx.x / kCtas, step = (int)gridDim.x / kCtas;
+  const int tiles_m = (a.M + 255) / 256;
+  const int tiles = tiles_m * ((a.N + kPairs * kN - 1) / (kPairs * kN));
   const int kblocks = (a.K + kBK - 1) / kBK, kqs = (int)scale_tiles(a.K);
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < a.stages; ++s) {
-      mbar_init(&full[s], 1);        // the leader's producer; the copies add bytes
-      mbar_init(&empty[s], PAIRS);   // every leader's commit, to all CTAs
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);         // the leader's producer; the copies add bytes
+      mbar_init(&empty[s], kPairs);   // every leader's commit, to all CTAs
     }
-    mbar_init(&acc_full, 1);
-    mbar_init(&acc_empty, 16);   // eight epilogue warps of each CTA (the leader's is used)
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 16);   // eight epilogue warps of each CTA (the leader's is used)
+    }
     mbar_init(&drain, 1);
     abort_flag = 0u;
     fence_mbar_init();
@@ -379,171 +374,169 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
     tmem_alloc_2sm(&tmem_slot, 512);
     tmem_relinquish_2sm();
   }
-  // both CTAs' barriers are initialised before any copy or commit reaches them
+  // all CTAs' barriers are initialised before any copy or commit reaches them
   __syncwarp();
   tc_fence_before();
   cluster_arrive();
   cluster_wait();
   tc_fence_after();
   grid_dep_wait();
-  const uint32_t tmem = __reduce_max_sync(0xFFFFFFFFu, tmem_slot);   // uniform
+  const uint32_t tmem = tmem_slot;
   const uint32_t ring = smem_u32(smem);
 
   if (warp == 0) {
-    uint32_t st = ring, ph = 1;
-    int s = 0;
-    bool ok = true;
-    for (int tile = first; tile < tiles && ok; tile += step) {
-      const int tn = tile / tiles_m, tm = tile - tn * tiles_m;
-      for (int kb = 0; kb < kblocks; ++kb) {
-        ok = WARP_WAIT(&empty[s], ph, kDevTimeoutEmpty);
-        if (!ok) break;
-        if (elect_one()) {
+    if (elect_one()) {
+      uint32_t st = ring, ph = 1;
+      int s = 0;
+      bool ok = true;
+      for (int tile = first; tile < tiles && ok; tile += step) {
+        const int tn = tile / tiles_m, tm = tile - tn * tiles_m;
+        const int n0 = (tn * kPairs + pr) * kN;   // first column of the pair's tile
+        const int tr = tm * 2 + rank;             // this CTA's 128 rows of A
+        const int fa = tr * kqs, fw = ((n0 >> 7) + rank) * kqs;
+        for (int kb = 0; kb < kblocks; ++kb) {
+          ok = mbar_wait_lazy(&empty[s], ph, &abort_flag, a.status, kDevTimeoutEmpty);
+          if (!ok) break;
           if (rank == 0) mbar_arrive_expect_tx(&full[s], 2u * kStageBytes);
           const uint32_t bar = smem_u32(&full[s]) & kPeerBitMask;
-          const int tr = (tm * PAIRS + pr) * 2 + rank;   // this CTA's 128 rows
-          load_2d_2sm(st, &tmA, bar, kb * 128, tr * 128);
-          // scale tiles of 128 rows: two 512-byte rows of the map, the stage's columns
-          load_2d_2sm(st + kScaleOff, &tmAs, bar, 0, tr * kqs + 2 * kb);
-          if constexpr (PAIRS == 1) {
-            load_2d_2sm(st + kCodeTile, &tmW, bar, kb * 128, tn * 256 + rank * 128);
-            load_2d_2sm(st + kScaleOff + 1024u, &tmWs, bar, 0, tn * 2 * kqs + 2 * kb);
-            load_2d_2sm(st + kScaleOff + 2048u, &tmWs, bar, 0, (tn * 2 + 1) * kqs + 2 * kb);
-          } else {
-            // 64 rows of W for this CTA and its counterpart; W's scales for all four
-            // from the first pair
-            load_2d_2sm_mc(st + kCodeTile + (uint32_t)pr * 8192u, &tmW, bar, kb * 128,
-                           tn * 256 + rank * 128 + pr * 64, (uint16_t)(0x5 << rank));
-            if (pr == 0)
-              load_2d_2sm_mc(st + kScaleOff + 1024u + (uint32_t)rank * 1024u, &tmWs, bar, 0,
-                             (tn * 2 + rank) * kqs + 2 * kb, (uint16_t)0xF);
+          load_2d_2sm_mc(st + (uint32_t)pr * 8192u, &tmA, bar, kb * 128, tr * 128 + pr * 64,
+                         (uint16_t)(0x5 << rank));
+          load_2d_2sm(st + kCodeTile, &tmW, bar, kb * 128, n0 + rank * (kN / 2));
+          // scale tiles of 128 rows: two 512-byte rows of the map, the stage's columns;
+          // A's for both pairs, W's two tiles for both CTAs of the pair
+          if (pr == 0)
+            load_2d_2sm_mc(st + kScaleOff, &tmAs, bar, 0, fa + 2 * kb, (uint16_t)(0x5 << rank));
+          load_2d_2sm_mc(st + kScaleOff + 1024u + (uint32_t)rank * 1024u, &tmWs, bar, 0,
+                         fw + 2 * kb, (uint16_t)(0x3 << (2 * pr)));
+          st += kStageBytes;
+          if (++s == kStages) {
+            s = 0;
+            ph ^= 1u;
+            st = ring;
           }
-        }
-        __syncwarp();
-        st += kStageBytes;
-        if (++s == a.stages) {
-          s = 0;
-          ph ^= 1u;
-          st = ring;
         }
       }
     }
   } else if (warp == 1) {
-    if (rank == 0) {
-      const uint32_t idesc0 = idesc_mxf4(256, 256, 0), idesc1 = idesc_mxf4(256, 256, 2);
-      uint32_t st = ring >> 4, ph = 0, cols = tmem + kSfCol;
+    if (rank == 0 && elect_one()) {
+      const uint32_t idesc0 = idesc_mxf4(256, kN, 0), idesc1 = idesc_mxf4(256, kN, 2);
+      uint32_t st = ring >> 4, ph = 0, cols = tmem + kSfCol0;
       int s = 0, local = 0;
       bool ok = true;
       for (int tile = first; tile < tiles && ok; tile += step, ++local) {
-        ok = WARP_WAIT(&acc_empty, ((uint32_t)local & 1u) ^ 1u, kDevTimeoutMma);
-        if (!ok) break;
+        const int buf = local & 1;
+        if (!mbar_wait_lazy(&acc_empty[buf], ((uint32_t)(local >> 1) & 1u) ^ 1u, &abort_flag,
+                            a.status, kDevTimeoutMma))
+          break;
         tc_fence_after();
+        const uint32_t d = tmem + (uint32_t)(buf * kN);
+        // a tile of 192 rows of W starts at row 0 or 64 of a scale tile; a tensor-memory
+        // column holds the scales of 32 rows
+        const uint32_t skip = (uint32_t)((tile / tiles_m * kPairs + pr) & 1) * 2u;
         int left = a.K;   // columns from here on
         for (int kb = 0; kb < kblocks; ++kb) {
-          ok = WARP_WAIT(&full[s], ph, kDevTimeoutFull);
+          ok = mbar_wait_lazy(&full[s], ph, &abort_flag, a.status, kDevTimeoutFull);
           if (!ok) break;
           tc_fence_after();
-          const int steps = min(4, (left + 63) / 64);   // of 64 columns
-          uint32_t x = code_desc_lo(st << 4), w = x + (kCodeTile >> 4);
-          uint32_t f = scale_desc_lo((st << 4) + kScaleOff), sfa = cols, sfb = cols + 8u;
-          uint32_t acc = kb > 0;
-          if (elect_one()) {
-#pragma unroll 1
-            for (int q = 0; q < steps; q += 2) {
-              copy_scales_2sm(sfa, f);
-              copy_scales_2sm(sfb, f + 64u);
-              copy_scales_2sm(sfb + 4u, f + 128u);
-              mma_mxf4_2sm(tmem, code_desc(x), code_desc(w), idesc0, sfa, sfb, acc);
-              if (q + 1 < steps)
-                mma_mxf4_2sm(tmem, code_desc(x + 2u), code_desc(w + 2u), idesc1, sfa, sfb, 1);
-              acc = 1;
-              x += 4u;
-              w += 4u;
-              f += 32u;
-              sfa += 4u;
-              sfb += 8u;
-            }
-            mma_commit_2sm_mc(&empty[s], (uint16_t)((1 << (2 * PAIRS)) - 1));
+          const uint32_t x = code_desc_lo(st << 4), w = x + (kCodeTile >> 4);
+          const uint32_t f = scale_desc_lo((st << 4) + kScaleOff);
+          const uint32_t sfb = cols + 8u, sfb_at = sfb + skip;
+          // 64 columns an MMA; a scale tile serves two
+          copy_scales_2sm(cols, f);
+          copy_scales_2sm(sfb, f + 64u);
+          copy_scales_2sm(sfb + 4u, f + 128u);
+          if (left > 128) {
+            copy_scales_2sm(cols + 4u, f + 32u);
+            copy_scales_2sm(sfb + 8u, f + 96u);
+            copy_scales_2sm(sfb + 12u, f + 160u);
           }
-          __syncwarp();
+          mma_mxf4_2sm(d, code_desc(x), code_desc(w), idesc0, cols, sfb_at, kb > 0);
+          if (left > 64)
+            mma_mxf4_2sm(d, code_desc(x + 2u), code_desc(w + 2u), idesc1, cols, sfb_at, 1);
+          if (left > 128)
+            mma_mxf4_2sm(d, code_desc(x + 4u), code_desc(w + 4u), idesc0, cols + 4u, sfb_at + 8u, 1);
+          if (left > 192)
+            mma_mxf4_2sm(d, code_desc(x + 6u), code_desc(w + 6u), idesc1, cols + 4u, sfb_at + 8u, 1);
+          mma_commit_2sm_mc(&empty[s], (uint16_t)((1 << kCtas) - 1));
           left -= kBK;
           st += kStageBytes >> 4;
           cols += kSfCols;
-          if (++s == a.stages) {
+          if (++s == kStages) {
             s = 0;
             ph ^= 1u;
             st = ring >> 4;
-            cols = tmem + kSfCol;
+            cols = tmem + kSfCol0;
           }
         }
-        if (ok && elect_one()) mma_commit_2sm_mc(&acc_full, (uint16_t)(0x3 << (2 * pr)));
-        __syncwarp();
+        if (ok) mma_commit_2sm_mc(&acc_full[buf], (uint16_t)(0x3 << (2 * pr)));
       }
-      // every MMA of this warp has finished once `drain` flips
-      if (elect_one()) mma_commit_2sm(&drain);
-      __syncwarp();
+      // every MMA of this thread has finished once `drain` flips
+      mma_commit_2sm(&drain);
       const uint64_t t0 = global_timer_ns();
       while (!mbar_try_wait(&drain, 0) && global_timer_ns() - t0 < 200000000ull) {
       }
     }
   } else {
     const int quarter = warp & 3, half = (warp - 2) >> 2;
-    const uint32_t release = mapa_shared(smem_u32(&acc_empty), (uint32_t)(2 * pr));
+    const uint32_t release = mapa_shared(smem_u32(&acc_empty[0]), (uint32_t)(2 * pr));
     const bool vec = (a.N & 7) == 0;
-    uint8_t* piece = smem + (size_t)a.stages * kStageBytes + (warp - 2) * 4096;
-    uint16_t* staged = reinterpret_cast<uint16_t*>(smem + (size_t)a.stages * kStageBytes) +
-                       (warp - 2) * 32 * kPitch;
+    uint8_t* piece = smem + kStages * kStageBytes + (warp - 2) * 4096;
+    uint16_t* staged =
+        reinterpret_cast<uint16_t*>(smem + kStages * kStageBytes + (warp - 2) * 4352);
     int local = 0;
     for (int tile = first; tile < tiles; tile += step, ++local) {
-      if (!WARP_WAIT(&acc_full, (uint32_t)local & 1u, kDevTimeoutMma)) break;
+      const int buf = local & 1;
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait_lazy(&acc_full[buf], (uint32_t)(local >> 1) & 1u,
+                                                  &abort_flag, a.status, kDevTimeoutMma)))
+        break;
       tc_fence_after();
       const int tn = tile / tiles_m, tm = tile - tn * tiles_m;
-      // everything into registers before the first conversion: the accumulator is back
-      // with the MMAs as soon as it is read
-      uint32_t r[128], v[64];
-      const uint32_t at = tmem + (uint32_t)(half * 128) + ((uint32_t)(quarter * 32) << 16);
+      const int row0 = (tm * 2 + rank) * 128 + quarter * 32;
+      // pieces of 64 columns: the first and the last, or the middle one
+#pragma unroll 1
+      for (int c = half * 64; c < kN; c += 128) {
+        uint32_t r[64], v[32];
+        const uint32_t at = tmem + (uint32_t)(buf * kN + c) + ((uint32_t)(quarter * 32) << 16);
+        tmem_ld32(at, r);
+        tmem_ld32(at + 32u, r + 32);
+        tmem_ld_wait();
+        if (c + 128 >= kN) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(release + (uint32_t)buf * 8u);
+        }
 #pragma unroll
-      for (int c = 0; c < 128; c += 32) tmem_ld32(at + (uint32_t)c, r + c);
-      tmem_ld_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(release);
-#pragma unroll
-      for (int j = 0; j < 64; ++j)
-        v[j] = pack_bf16x2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
-      const int row0 = ((tm * PAIRS + pr) * 2 + rank) * 128 + quarter * 32, col0 = tn * 256 + half * 128;
-      if (vec) {
-        // 64 columns at a time through shared memory (128-byte swizzle) and the TMA unit:
-        // stores of each lane's own row would fill the queue that the barriers and the
-        // MMAs' issue go through
-#pragma unroll
-        for (int c = 0; c < 64; c += 32) {
+        for (int j = 0; j < 32; ++j)
+          v[j] = pack_bf16x2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+        const int col = (tn * kPairs + pr) * kN + c;
+        if (vec) {
+          // 128-byte swizzle and a TMA store: stores of each lane's own row would fill
+          // the queue that the barriers and the MMAs' issue go through
           if (lane == 0) bulk_wait_read_all();   // the copy before has left the buffer
           __syncwarp();
 #pragma unroll
           for (int j = 0; j < 8; ++j)
             *reinterpret_cast<uint4*>(piece + lane * 128 + ((j ^ (lane & 7)) << 4)) =
-                make_uint4(v[c + 4 * j], v[c + 4 * j + 1], v[c + 4 * j + 2], v[c + 4 * j + 3]);
+                make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0 && row0 < a.M && col0 + 2 * c < a.N)
-            tma_store_2d(&tmY, smem_u32(piece), col0 + 2 * c, row0);
-        }
-      } else {
-        // rows of Y start anywhere: through shared memory, so that a warp stores 32
-        // neighbouring values of a row at a time
+          if (lane == 0 && row0 < a.M && col < a.N)
+            tma_store_2d(&tmY, smem_u32(piece), col, row0);
+        } else {
+          // rows of Y start anywhere: a warp stores 32 neighbouring values of a row
 #pragma unroll
-        for (int j = 0; j < 64; ++j)
-          reinterpret_cast<uint32_t*>(staged)[lane * (kPitch / 2) + j] = v[j];
-        __syncwarp();
-        const int rows = min(32, a.M - row0);
-        for (int r = 0; r < rows; ++r) {
-          uint16_t* y = a.Y + (size_t)(row0 + r) * a.N + col0;
+          for (int j = 0; j < 32; ++j)
+            reinterpret_cast<uint32_t*>(staged)[lane * (kPitch / 2) + j] = v[j];
+          __syncwarp();
+          const int rows = min(32, a.M - row0);
+          for (int i = 0; i < rows; ++i) {
+            uint16_t* y = a.Y + (size_t)(row0 + i) * a.N + col;
 #pragma unroll
-          for (int j = 0; j < 128; j += 32)
-            if (col0 + j + lane < a.N) y[j + lane] = staged[r * kPitch + j + lane];
+            for (int j = 0; j < 64; j += 32)
+              if (col + j + lane < a.N) y[j + lane] = staged[i * kPitch + j + lane];
+          }
+          __syncwarp();
         }
-        __syncwarp();
       }
     }
     if (lane == 0) bulk_wait_all();   // stores read this CTA's shared memory
@@ -555,8 +548,8 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
     while (global_timer_ns() - t0 < 1000000ull) {
     }
   }
-  // neither CTA frees its tensor memory while the pair's MMAs or the other CTA's
-  // epilogue may still use it
+  // no CTA frees its tensor memory or leaves while the pair's MMAs, another CTA's
+  // epilogue or a copy into it may still be under way
   __syncwarp();
   tc_fence_before();
   cluster_arrive();
@@ -576,68 +569,63 @@ static bool scale_map(CUtensorMap* map, const uint8_t* scales, int64_t rows, int
 
 // Clusters of this kernel that can be resident at once (kept per device; 0 if the
 // runtime does not say).
-template <int PAIRS>
 static int resident_clusters(cudaLaunchConfig_t cfg, int sm_count) {
   constexpr int kMaxDev = 64;
   static int kept[kMaxDev];
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return 0;
   if (kept[dev] > 0) return kept[dev];
-  cfg.gridDim = dim3((unsigned)(sm_count / (2 * PAIRS) * 2 * PAIRS));
-  cfg.dynamicSmemBytes = 1024 + (size_t)pair::kMaxStages2 * pair::kStageBytes + pair::kPieces;
+  cfg.gridDim = dim3((unsigned)(sm_count / pair::kCtas * pair::kCtas));
   cfg.numAttrs = 1;
-  if (cudaOccupancyMaxActiveClusters(&n, k_mx4_pair<PAIRS>, &cfg) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveClusters(&n, k_mx4_pair, &cfg) != cudaSuccess) {
     (void)cudaGetLastError();
     return 0;
   }
   return kept[dev] = n;
 }
 
-template <int PAIRS>
 static cudaError_t launch_pair(const uint8_t* a_codes, const uint8_t* a_scales, int64_t M,
                                const uint8_t* w_codes, const uint8_t* w_scales, int64_t N,
                                int64_t K, uint16_t* Y, uint32_t* status, int sm_count, int early,
                                cudaStream_t st) {
+  using namespace pair;
   PairArgs a;
   a.Y = Y;
   a.M = (int)M;
   a.N = (int)N;
   a.K = (int)K;
   a.status = status;
-  const bool vec = (N & 7) == 0;
-  a.stages = vec ? pair::kMaxStages2 : pair::kMaxStages2 - 1;   // room for staged rows
-  const int64_t cs = code_stride(K);
+  const uint64_t cs = (uint64_t)code_stride(K);
   CUtensorMap ta, tw, tas, tws, ty = {};
-  if (!make_tmap_2d(&ta, a_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)M, (uint64_t)cs, 128,
-                    128, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !make_tmap_2d(&tw, w_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)N, (uint64_t)cs,
-                    128 / PAIRS, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+  if (!make_tmap_2d(&ta, a_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)M, cs, 64, 128,
+                    CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_tmap_2d(&tw, w_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)N, cs, kN / 2, 128,
+                    CU_TENSOR_MAP_SWIZZLE_128B) ||
       !scale_map(&tas, a_scales, M, K) || !scale_map(&tws, w_scales, N, K) ||
-      (vec && !make_tmap_2d(&ty, Y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, (uint64_t)M, (uint64_t)N,
-                            32, 64, CU_TENSOR_MAP_SWIZZLE_128B)))
+      ((N & 7) == 0 && !make_tmap_2d(&ty, Y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, (uint64_t)M,
+                                     (uint64_t)N, 32, 64, CU_TENSOR_MAP_SWIZZLE_128B)))
     return cudaErrorInvalidValue;
-  cudaError_t e = ensure_smem_limit(k_mx4_pair<PAIRS>, kMaxDynSmem);
+  cudaError_t e = ensure_smem_limit(k_mx4_pair, kMaxDynSmem);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = ((M + 256 * PAIRS - 1) / (256 * PAIRS)) * ((N + 255) / 256);
+  const int64_t tiles = ((M + 255) / 256) * ((N + kPairs * kN - 1) / (kPairs * kN));
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(pair::kThreads);
-  cfg.dynamicSmemBytes =
-      1024 + (size_t)a.stages * pair::kStageBytes + (size_t)(vec ? pair::kPieces : pair::kStaged);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = 1024 + (size_t)kStages * kStageBytes + kStaged;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2 * PAIRS;
+  attr[0].val.clusterDim.x = kCtas;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  int clusters = resident_clusters<PAIRS>(cfg, sm_count);
-  if (clusters < 1) clusters = sm_count / (2 * PAIRS);
+  int clusters = resident_clusters(cfg, sm_count);
+  if (clusters < 1) clusters = sm_count / kCtas;
   if (tiles < clusters) clusters = (int)tiles;
-  cfg.gridDim = dim3((unsigned)(2 * PAIRS * clusters));
+  cfg.gridDim = dim3((unsigned)(kCtas * clusters));
   cfg.numAttrs = early ? 2 : 1;
-  e = cudaLaunchKernelEx(&cfg, k_mx4_pair<PAIRS>, ta, tw, tas, tws, ty, a);
+  e = cudaLaunchKernelEx(&cfg, k_mx4_pair, ta, tw, tas, tws, ty, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -648,12 +636,12 @@ cudaError_t launch_mx4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int
                             uint16_t* Y, void* ws, uint32_t* status, int sm_count, int early,
                             cudaStream_t st) {
   (void)ws;
-  // The pair kernel where its 256 x 256 tiles occupy at least a quarter of the SM pairs.
-  const int64_t tiles = ((M + 255) / 256) * ((N + 255) / 256);
+  // The pair kernel where its 256 x 192 tiles occupy at least a quarter of the SM pairs.
+  const int64_t tiles = ((M + 255) / 256) * ((N + 191) / 192);
   const int64_t scale_rows = ((M > N ? M : N) + 127) / 128 * mx4::scale_tiles(K);
   if (M > 256 && tiles * 8 >= sm_count && scale_rows <= INT32_MAX)
-    return mx4::launch_pair<2>(a_codes, a_scales, M, w_codes, w_scales, N, K, Y, status, sm_count,
-                               early, st);
+    return mx4::launch_pair(a_codes, a_scales, M, w_codes, w_scales, N, K, Y, status, sm_count,
+                            early, st);
   return mx4::launch_stream(a_codes, a_scales, M, w_codes, w_scales, N, K, Y, status, sm_count,
                             early, st);
 }
