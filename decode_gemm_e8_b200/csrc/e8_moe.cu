@@ -17,11 +17,12 @@
 //     up          gate and up rows alternate, so a tile holds both factors of 64
 //                 values of h = silu(g) u; the epilogue writes h as two e4m3 rows
 //                 again, with a power-of-two scale for the tile's 64 values
-//     down        every slot's product times its probability goes to a buffer; the
-//                 unit that brings a token's last contribution adds them in the
-//                 order of the choices, so the sums do not depend on timing
-// With few units the K range is split; partial sums are added in order by the unit
-// that arrives last.
+//     down        every slot's product times its probability goes to a buffer
+//   k_moe_combine adds a token's slots in the order of its choices: no sum depends on
+//                 timing (a count of arrivals at the end of each down unit cost three
+//                 times the unit's own work at 64 tokens)
+// With few units the K range is split; the up product's partial sums are added in order
+// by the unit that arrives last, the down product's by k_moe_combine.
 #include "e8_internal.h"
 #include "e8_mx4.cuh"
 #include "e8_tmap.h"
@@ -236,7 +237,7 @@ constexpr int kRingBytes = 212 * 1024;
 struct GemmArgs {
   const int32_t* experts;  // by slot = token * topk + choice
   const float* probs;
-  const uint8_t* w_scales;
+  const uint8_t *w_codes, *w_scales;
   int K, tiles, splits;    // tiles of 128 rows of one expert; K split in `splits`
   int T, E, topk, stages, b_rows;
   const uint8_t* xq;       // up: the tokens' hi and lo rows
@@ -246,12 +247,20 @@ struct GemmArgs {
   int I;
   float* part;             // partial sums / slot products, fp32
   int* counters;
-  uint16_t* Y;
   uint32_t* status;
 };
 
 __device__ __forceinline__ void bar_sync(uint32_t id, uint32_t n) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+// Counts this block's arrival after its other threads' writes (a barrier came before).
+__device__ __forceinline__ int arrive_gpu(int* counter) {
+  int old;
+  asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(old) : "l"(counter) : "memory");
+  return old;
 }
 __device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -365,7 +374,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                              ~uintptr_t(1023));
   __shared__ __align__(16) uint8_t const_sf[512];
   __shared__ __align__(16) float stage_v[8][128 + 4];
-  __shared__ int ready[kMaxTokens];
+  __shared__ int ready;
+  __shared__ float token_scale[kMaxTokens];
   __shared__ SharedLists lists;
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drain;
   __shared__ uint32_t tmem_slot;
@@ -405,8 +415,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     grid_dep_launch();
   }
   // (down: the choice was complete before the up kernel let this one start)
+  if (!UP) grid_dep_launch();
   tc_fence_before();
   const int slots = g.T * g.topk;
+  if (UP && threadIdx.x < g.T) token_scale[threadIdx.x] = g.xs[threadIdx.x];
   const int units = build_lists(lists, smem, g.experts, slots, g.E) * g.tiles * g.splits;
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
@@ -424,6 +436,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int row = (u.expert * g.tiles + u.tile) * kRows;
         const uint8_t* sf = g.w_scales + ((int64_t)(row >> 7) * kqs + u.k0) * 512;
         int x = u.k0 * kBK;
+        if (i + (int)gridDim.x < units) {
+          // the next unit lies in other pages: a first access there costs microseconds
+          // (address translation) and the ring holds less than two
+          const Unit v = unit_at(g, lists, i + (int)gridDim.x);
+          const int64_t next = (int64_t)(v.expert * g.tiles + v.tile);
+          prefetch_l2(g.w_codes + next * kRows * (g.K / 2) + v.k0 * 64);
+          prefetch_l2(g.w_scales + (next * kqs + v.k0) * 512);
+        }
         for (int k = u.nk; k > 0; k -= 2) {
           ok = mbar_wait_lazy(&empty[s], ph, &abort_flag, g.status, kDevTimeoutEmpty);
           if (!ok) break;
@@ -446,6 +466,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 6) {
     if (!UP) {
+      // until the up product has ended HBM would idle: the first unit's weights beyond
+      // the ring go to L2
+      if ((int)blockIdx.x < units) {
+        const Unit u = unit_at(g, lists, blockIdx.x);
+        const uint8_t* at = g.w_codes + (int64_t)(u.expert * g.tiles + u.tile) * kRows * (g.K / 2) +
+                            u.k0 * 64;
+        for (int r = lane; r < kRows; r += 32)
+          bulk_prefetch_l2(at + (int64_t)r * (g.K / 2), (uint32_t)u.nk * 64u);
+      }
       // sorted by expert: sixteen rows a copy
       grid_dep_wait();
       if (elect_one()) {
@@ -490,19 +519,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int i = blockIdx.x; i < units && ok; i += gridDim.x) {
         const Unit u = unit_at(g, lists, i);
+        const int row0 = lane < u.n ? lists.slot[u.off + lane] / g.topk * 2 * g.K : 0;
+        const int row1 = lane + 32 < u.n ? lists.slot[u.off + lane + 32] / g.topk * 2 * g.K : 0;
         int x = u.k0 * kBK;
         for (int k = u.nk; k > 0; k -= 2) {
           ok = __all_sync(0xFFFFFFFFu, mbar_wait_lazy(&empty[s], ph, &abort_flag, g.status,
                                                       kDevTimeoutEmpty));
           if (!ok) break;
-          if (k > 1 || c < 8) {
-#pragma unroll 2
-            for (int j = 0; j < u.n; ++j) {
-              const int t = lists.slot[u.off + j] / g.topk;
-              copy_async16(st + to + (uint32_t)j * 256u +
-                               (uint32_t)(((c & 7) ^ ((2 * j + r) & 7)) << 4),
-                           src + (size_t)t * 2 * g.K + x);
-            }
+          uint32_t dst = st + to;
+#pragma unroll 4
+          for (int j = 0; j < u.n; ++j) {
+            const int row = __shfl_sync(0xFFFFFFFFu, j < 32 ? row0 : row1, j & 31);
+            if (k > 1 || c < 8)
+              copy_async16(dst + (uint32_t)(((c & 7) ^ ((2 * j + r) & 7)) << 4), src + row + x);
+            dst += 256u;
           }
           copy_async_arrive(&full[s]);
           x += 2 * kBK;
@@ -616,13 +646,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     v[j];
           }
           release();
-          __threadfence();
           bar_sync(1, 128);
           if (et == 0)
-            ready[0] = atomicAdd(&g.counters[u.a * g.tiles + u.tile], 1) == g.splits - 1;
+            ready = arrive_gpu(&g.counters[u.a * g.tiles + u.tile]) == g.splits - 1;
           bar_sync(1, 128);
-          last = ready[0] != 0;
-          __threadfence();
+          last = ready != 0;
         }
         if (last) {
 #pragma unroll 1
@@ -653,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
               }
             }
-            const float x = mine ? g.xs[lists.slot[u.off + j] / g.topk] : 0.0f;
+            const float x = mine ? token_scale[lists.slot[u.off + j] / g.topk] : 0.0f;
             const float gate[4] = {p0.x * x, p0.z * x, p1.x * x, p1.z * x};
             const float up[4] = {p0.y * x, p0.w * x, p1.y * x, p1.w * x};
             float h[4];
@@ -705,31 +733,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         release();
-        __threadfence();
-        bar_sync(1, 128);
-        if (et < u.n) {
-          const int t = lists.slot[u.off + et] / g.topk;
-          ready[et] =
-              atomicAdd(&g.counters[u.tile * g.T + t], 1) == g.topk * g.splits - 1 ? t : -1;
-        }
-        bar_sync(1, 128);
-        __threadfence();
-#pragma unroll 1
-        for (int j = 0; j < u.n; ++j) {
-          const int t = ready[j];
-          if (t < 0) continue;
-          float y = 0.0f;
-          const float* at = g.part + (size_t)t * g.topk * width + u.tile * kRows + row;
-          for (int p = 0; p < g.splits; ++p) {
-#pragma unroll 4
-            for (int c = 0; c < g.topk; ++c) y += __ldcg(at + (size_t)c * width);
-            at += (size_t)slots * width;
-          }
-          g.Y[(size_t)t * width + u.tile * kRows + row] =
-              (uint16_t)(pack_bf16x2(y, 0.0f) & 0xFFFFu);
-        }
       }
-      bar_sync(1, 128);   // `ready` is free again
+      if (UP && g.splits > 1) bar_sync(1, 128);   // `ready` is free again
     }
   }
   __syncwarp();
@@ -747,11 +752,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_dealloc(tmem, 512);
   }
 }
+// Y[t] = sum of the slots' shares, by K part and then by choice; four columns a thread.
+__global__ void __launch_bounds__(128)
+    k_moe_combine(const float* __restrict__ part, int topk, int splits, int slots, int H,
+                  uint16_t* __restrict__ Y) {
+  const int col = ((int)blockIdx.x * 128 + (int)threadIdx.x) * 4, t = blockIdx.y;
+  grid_dep_wait();
+  if (col >= H) return;
+  float4 y = make_float4(0, 0, 0, 0);
+  const float* at = part + (size_t)t * topk * H + col;
+  for (int p = 0; p < splits; ++p) {
+#pragma unroll 8
+    for (int c = 0; c < topk; ++c) {
+      const float4 v = __ldcs(reinterpret_cast<const float4*>(at + (size_t)c * H));
+      y.x += v.x; y.y += v.y; y.z += v.z; y.w += v.w;
+    }
+    at += (size_t)slots * H;
+  }
+  *reinterpret_cast<uint2*>(Y + (size_t)t * H + col) =
+      make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+}
+
 // ------------------------------------------------------------------- host ---
 // K parts of a product of `tiles` row tiles of an expected number of experts: the
-// rounds of units over the SMs, each as long as its share of K and about four
-// stages of fixed cost.
-static int choose_splits(int64_t T, int64_t E, int topk, int64_t tiles, int64_t K) {
+// rounds of units over the SMs, each as long as its share of K plus about six of the
+// 128-column steps; `join` is the further cost of a split in such steps.
+static int choose_splits(int64_t T, int64_t E, int topk, int64_t tiles, int64_t K, double join) {
   double miss = 1.0;
   for (int64_t t = 0; t < T; ++t) miss *= 1.0 - (double)topk / (double)E;
   const double n = (double)E * (1.0 - miss);
@@ -761,7 +787,7 @@ static int choose_splits(int64_t T, int64_t E, int topk, int64_t tiles, int64_t 
   double cost = 1e30;
   for (int s = 1; s <= 8 && s <= kq; ++s) {
     const double rounds = (double)((units * s + 147) / 148);
-    const double c = rounds * ((double)kq / s + 4.0) + (s > 1 ? 2.0 : 0.0);
+    const double c = rounds * ((double)kq / s + 6.0) + (s > 1 ? join : 0.0);
     if (c < cost - 1e-9) {
       cost = c;
       best = s;
@@ -772,7 +798,7 @@ static int choose_splits(int64_t T, int64_t E, int topk, int64_t tiles, int64_t 
 
 struct Layout {
   size_t xq, xs, experts, probs, hq, h_scales, part_up, part_down, counters, total;
-  int splits_up, splits_down, max_act, n_up, n_down;
+  int splits_up, splits_down, max_act, n_up;
 };
 static Layout layout(int64_t T, int64_t H, int64_t E, int topk, int64_t I) {
   Layout l;
@@ -784,10 +810,11 @@ static Layout layout(int64_t T, int64_t H, int64_t E, int topk, int64_t I) {
   };
   const size_t slots = (size_t)T * topk;
   l.max_act = (int)(slots < (size_t)E ? slots : (size_t)E);
-  l.splits_up = choose_splits(T, E, topk, 2 * I / kRows, H);
-  l.splits_down = choose_splits(T, E, topk, H / kRows, I);
-  l.n_up = (int)(l.max_act * (2 * I / kRows));
-  l.n_down = (int)(T * (H / kRows));
+  // joining the up product's parts takes five round trips to memory at the end of a unit;
+  // the down product's parts are added where the choices are
+  l.splits_up = choose_splits(T, E, topk, 2 * I / kRows, H, 20.0);
+  l.splits_down = choose_splits(T, E, topk, H / kRows, I, 1.0);
+  l.n_up = l.splits_up > 1 ? (int)(l.max_act * (2 * I / kRows)) : 0;
   l.xq = take((size_t)T * 2 * H);
   l.xs = take((size_t)T * 4);
   l.experts = take(slots * 4);
@@ -796,7 +823,7 @@ static Layout layout(int64_t T, int64_t H, int64_t E, int topk, int64_t I) {
   l.h_scales = take((size_t)l.max_act * (I / 128) * 512);
   l.part_up = take(l.splits_up > 1 ? (size_t)l.splits_up * slots * 2 * I * 4 : 0);
   l.part_down = take((size_t)l.splits_down * slots * H * 4);
-  l.counters = take((size_t)(l.n_up + l.n_down) * 4);
+  l.counters = take((size_t)l.n_up * 4);
   l.total = at;
   return l;
 }
@@ -865,7 +892,7 @@ cudaError_t launch_moe(const MoeArgs& a, int sm_count, cudaStream_t st) {
 
   k_moe_route<<<(a.T + kRouteTokens - 1) / kRouteTokens * kRouteCtas, 256, 0, st>>>(
       a.X, a.T, a.H, a.router, a.E, a.topk, a.renorm, experts, probs, a.experts, a.probs, w + l.xq,
-      xs, counters, l.n_up + l.n_down);
+      xs, counters, l.n_up);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
 
@@ -890,11 +917,11 @@ cudaError_t launch_moe(const MoeArgs& a, int sm_count, cudaStream_t st) {
   g.hq = w + l.hq;
   g.h_scales = w + l.h_scales;
   g.I = a.I;
-  g.Y = a.Y;
   g.status = a.status;
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = 1024 + (size_t)g.stages * stage_bytes;
 
+  g.w_codes = a.w13_codes;
   g.w_scales = a.w13_scales;
   g.K = a.H;
   g.tiles = 2 * a.I / kRows;
@@ -906,15 +933,22 @@ cudaError_t launch_moe(const MoeArgs& a, int sm_count, cudaStream_t st) {
   e = cudaLaunchKernelEx(&cfg, k_moe_gemm<true>, tw13, th, g);
   if (e != cudaSuccess) return e;
 
+  g.w_codes = a.w2_codes;
   g.w_scales = a.w2_scales;
   g.K = a.I;
   g.tiles = a.H / kRows;
   g.splits = l.splits_down;
   g.part = reinterpret_cast<float*>(w + l.part_down);
-  g.counters = counters + l.n_up;
   units = (int64_t)l.max_act * g.tiles * g.splits;
   cfg.gridDim = dim3((unsigned)(units < sm_count ? units : sm_count));
   e = cudaLaunchKernelEx(&cfg, k_moe_gemm<false>, tw2, th, g);
+  if (e != cudaSuccess) return e;
+
+  cfg.gridDim = dim3((unsigned)((a.H + 511) / 512), (unsigned)a.T);
+  cfg.blockDim = dim3(128);
+  cfg.dynamicSmemBytes = 0;
+  e = cudaLaunchKernelEx(&cfg, k_moe_combine, (const float*)g.part, a.topk, g.splits, slots, a.H,
+                         a.Y);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
