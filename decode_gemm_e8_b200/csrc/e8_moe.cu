@@ -239,6 +239,10 @@ struct GemmArgs {
   const float* probs;
   const uint8_t *w_codes, *w_scales;
   int K, tiles, splits;    // tiles of 128 rows of one expert; K split in `splits`
+  // Divisions without a divide: `per` = tiles * splits units an expert, the block's first
+  // expert and rest, the grid's step in the same terms, and ceil(2^16 / d) for the
+  // divisors splits and topk (exact: dividend < 8192, divisor <= 16, product < 2^16 off)
+  int per, step_a, step_rest, by_splits, by_topk, by_per;
   int T, E, topk, stages, b_rows;
   const uint8_t* xq;       // up: the tokens' hi and lo rows
   const float* xs;         // up: scale of each token's pair
@@ -274,20 +278,55 @@ __device__ __forceinline__ void copy_async_arrive(uint64_t* bar) {
 // slot[off[a]] .. slot[off[a + 1] - 1], by rising slot.
 struct SharedLists {
   int16_t expert[kMaxExperts], off[kMaxExperts + 1], slot[kMaxSlots];
+  uint8_t token[kMaxSlots];
+  int16_t k_at[9];   // first 128-column step of each K part
+  int nact;
   uint32_t wsum[8];
 };
 
-// Builds the lists (all threads; `scratch`: at least 32 * E + 4 * 1024 + 2 * E bytes);
-// returns the number of active experts.
-__device__ __forceinline__ int build_lists(SharedLists& l, uint8_t* scratch,
-                                           const int32_t* __restrict__ experts, int slots, int E) {
+// Up to 32 slots: one warp, a lane a slot.
+__device__ __forceinline__ void build_small(SharedLists& l, const int32_t* __restrict__ experts,
+                                            int slots, int by_topk) {
+  const int lane = threadIdx.x & 31;
+  const int e = lane < slots ? experts[lane] : INT32_MAX;
+  const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
+  const bool head = (same & ((1u << lane) - 1u)) == 0 && lane < slots;
+  // slots and active experts before this one's
+  int pos = __popc(same & ((1u << lane) - 1u)), act = 0;
+#pragma unroll 4
+  for (int j = 0; j < slots; ++j) {
+    const int other = __shfl_sync(0xFFFFFFFFu, e, j);
+    const bool other_head = __shfl_sync(0xFFFFFFFFu, (int)head, j) != 0;
+    pos += other < e;
+    act += other < e && other_head;
+  }
+  if (lane < slots) {
+    l.slot[pos] = (int16_t)lane;
+    l.token[pos] = (uint8_t)(lane * by_topk >> 16);
+    if (head) {
+      l.expert[act] = (int16_t)e;
+      l.off[act] = (int16_t)pos;
+    }
+  }
+  const int nact = __popc(__ballot_sync(0xFFFFFFFFu, head));
+  if (lane == 0) {
+    l.off[nact] = (int16_t)slots;
+    l.nact = nact;
+  }
+}
+
+// Any number (all threads; `scratch`: 32 E + 4 kMaxSlots + 2 E bytes).
+__device__ __forceinline__ void build_lists(SharedLists& l, uint8_t* scratch,
+                                            const int32_t* __restrict__ experts, int slots, int E,
+                                            int by_topk) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int groups = (slots + 31) / 32;
   uint8_t* count = scratch;   // [groups][E]: slots of an expert in a group of 32 slots
   int16_t* se = reinterpret_cast<int16_t*>(scratch + 32 * kMaxExperts);
   int16_t* sp = se + kMaxSlots;
   int16_t* first = sp + kMaxSlots;
-  for (int i = tid; i < groups * E; i += kThreads) count[i] = 0;
+  for (int i = tid; i < (groups * E + 3) / 4; i += kThreads)
+    reinterpret_cast<uint32_t*>(count)[i] = 0;
   __syncthreads();
   for (int g = warp; g < groups; g += kThreads / 32) {
     const int s = g * 32 + lane, e = s < slots ? experts[s] : -1;
@@ -303,6 +342,7 @@ __device__ __forceinline__ int build_lists(SharedLists& l, uint8_t* scratch,
   uint32_t mine = 0;
   for (int e = tid * per; e < min(E, (tid + 1) * per); ++e) {
     uint32_t run = 0;
+#pragma unroll 4
     for (int g = 0; g < groups; ++g) {
       const uint32_t c = count[g * E + e];
       count[g * E + e] = (uint8_t)run;
@@ -332,35 +372,48 @@ __device__ __forceinline__ int build_lists(SharedLists& l, uint8_t* scratch,
       at += (1u << 16) | n;
     }
   }
-  const int nact = (int)(total >> 16);
-  if (tid == 0) l.off[nact] = (int16_t)slots;
+  if (tid == 0) {
+    l.nact = (int)(total >> 16);
+    l.off[total >> 16] = (int16_t)slots;
+  }
   __syncthreads();
-  for (int s = tid; s < slots; s += kThreads)
-    l.slot[first[se[s]] + count[(s >> 5) * E + se[s]] + sp[s]] = (int16_t)s;
+  for (int s = tid; s < slots; s += kThreads) {
+    const int pos = first[se[s]] + count[(s >> 5) * E + se[s]] + sp[s];
+    l.slot[pos] = (int16_t)s;
+    l.token[pos] = (uint8_t)(s * by_topk >> 16);
+  }
   fence_proxy_async_smem();   // the scratch space becomes the copies' ring
-  __syncthreads();
-  return nact;
 }
 
 // The units of one block in turn: all row tiles and K parts of an expert, then the next.
 struct Unit {
-  int a, tile, part, expert, off, n, k0, nk;
+  int a, rest;                                    // active expert; tile * splits + part
+  int tile, part, expert, off, n, k0, nk;
+  __device__ __forceinline__ void begin(const GemmArgs& g) {
+    a = g.per > (int)blockIdx.x ? 0 : (int)blockIdx.x * g.by_per >> 16;
+    rest = (int)blockIdx.x - a * g.per;
+  }
+  __device__ __forceinline__ void next(const GemmArgs& g) {
+    a += g.step_a;
+    rest += g.step_rest;
+    if (rest >= g.per) {
+      rest -= g.per;
+      ++a;
+    }
+  }
+  // false after the last unit
+  __device__ __forceinline__ bool load(const GemmArgs& g, const SharedLists& l) {
+    if (a >= l.nact) return false;
+    tile = rest * g.by_splits >> 16;
+    part = rest - tile * g.splits;
+    expert = l.expert[a];
+    off = l.off[a];
+    n = l.off[a + 1] - off;
+    k0 = l.k_at[part];
+    nk = l.k_at[part + 1] - k0;
+    return true;
+  }
 };
-__device__ __forceinline__ Unit unit_at(const GemmArgs& g, const SharedLists& l, int u) {
-  Unit r;
-  const int per = g.tiles * g.splits;
-  r.a = u / per;
-  const int rest = u - r.a * per;
-  r.tile = rest / g.splits;
-  r.part = rest - r.tile * g.splits;
-  r.expert = l.expert[r.a];
-  r.off = l.off[r.a];
-  r.n = l.off[r.a + 1] - r.off;
-  const int kq = g.K / kBK;
-  r.k0 = kq * r.part / g.splits;
-  r.nk = kq * (r.part + 1) / g.splits - r.k0;
-  return r;
-}
 
 // Warps: 0 weights producer, 6 tokens producer, 1 MMAs, 2..5 epilogue.  At 16 KB of
 // weights a stage the SM's share of HBM leaves each role some 700 cycles a stage: one
@@ -419,7 +472,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   const int slots = g.T * g.topk;
   if (UP && threadIdx.x < g.T) token_scale[threadIdx.x] = g.xs[threadIdx.x];
-  const int units = build_lists(lists, smem, g.experts, slots, g.E) * g.tiles * g.splits;
+  if (threadIdx.x >= 128 && threadIdx.x <= 128 + g.splits)
+    lists.k_at[threadIdx.x - 128] =
+        (int16_t)((g.K / kBK) * ((int)threadIdx.x - 128) * g.by_splits >> 16);
+  if (slots > 32) build_lists(lists, smem, g.experts, slots, g.E, g.by_topk);
+  else if (warp == 2) build_small(lists, g.experts, slots, g.by_topk);
+  __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
   const uint32_t ring = smem_u32(smem);
@@ -431,19 +489,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t st = ring, ph = 1;
       int s = 0;
       bool ok = true;
-      for (int i = blockIdx.x; i < units && ok; i += gridDim.x) {
-        const Unit u = unit_at(g, lists, i);
+      Unit u;
+      for (u.begin(g); ok && u.load(g, lists); u.next(g)) {
         const int row = (u.expert * g.tiles + u.tile) * kRows;
         const uint8_t* sf = g.w_scales + ((int64_t)(row >> 7) * kqs + u.k0) * 512;
         int x = u.k0 * kBK;
-        if (i + (int)gridDim.x < units) {
-          // the next unit lies in other pages: a first access there costs microseconds
-          // (address translation) and the ring holds less than two
-          const Unit v = unit_at(g, lists, i + (int)gridDim.x);
-          const int64_t next = (int64_t)(v.expert * g.tiles + v.tile);
-          prefetch_l2(g.w_codes + next * kRows * (g.K / 2) + v.k0 * 64);
-          prefetch_l2(g.w_scales + (next * kqs + v.k0) * 512);
-        }
+        bool ahead = true;
         for (int k = u.nk; k > 0; k -= 2) {
           ok = mbar_wait_lazy(&empty[s], ph, &abort_flag, g.status, kDevTimeoutEmpty);
           if (!ok) break;
@@ -453,6 +504,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           load_2d(st, &tmW, &full[s], x, row);
           if (k > 1) load_2d(st + kWBytes, &tmW, &full[s], x + kBK, row);
           load_bulk(st + 2u * (kWBytes + b_bytes), sf, half * 512u, &full[s]);
+          if (ahead) {
+            // the next unit lies in other pages: a first access there costs microseconds
+            // (address translation) and the ring holds less than two
+            Unit v = u;
+            v.next(g);
+            if (v.load(g, lists)) {
+              const int64_t next = (int64_t)(v.expert * g.tiles + v.tile);
+              prefetch_l2(g.w_codes + next * kRows * (g.K / 2) + v.k0 * 64);
+              prefetch_l2(g.w_scales + (next * kqs + v.k0) * 512);
+            }
+            ahead = false;
+          }
           x += 2 * kBK;
           sf += 1024;
           st += stage_bytes;
@@ -468,8 +531,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!UP) {
       // until the up product has ended HBM would idle: the first unit's weights beyond
       // the ring go to L2
-      if ((int)blockIdx.x < units) {
-        const Unit u = unit_at(g, lists, blockIdx.x);
+      Unit u;
+      u.begin(g);
+      if (u.load(g, lists)) {
         const uint8_t* at = g.w_codes + (int64_t)(u.expert * g.tiles + u.tile) * kRows * (g.K / 2) +
                             u.k0 * 64;
         for (int r = lane; r < kRows; r += 32)
@@ -481,8 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t st = ring + 2u * kWBytes, ph = 1;
         int s = 0;
         bool ok = true;
-        for (int i = blockIdx.x; i < units && ok; i += gridDim.x) {
-          const Unit u = unit_at(g, lists, i);
+        for (; ok && u.load(g, lists); u.next(g)) {
           const uint8_t* sf = g.h_scales + ((int64_t)u.a * kqs + u.k0) * 512;
           const uint32_t copies = (uint32_t)(u.n + 7) / 8;
           int x = u.k0 * kBK;
@@ -517,10 +580,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t st = ring + 2u * kWBytes, ph = 1;
       int s = 0;
       bool ok = true;
-      for (int i = blockIdx.x; i < units && ok; i += gridDim.x) {
-        const Unit u = unit_at(g, lists, i);
-        const int row0 = lane < u.n ? lists.slot[u.off + lane] / g.topk * 2 * g.K : 0;
-        const int row1 = lane + 32 < u.n ? lists.slot[u.off + lane + 32] / g.topk * 2 * g.K : 0;
+      Unit u;
+      for (u.begin(g); ok && u.load(g, lists); u.next(g)) {
+        const int row0 = lane < u.n ? lists.token[u.off + lane] * 2 * g.K : 0;
+        const int row1 = lane + 32 < u.n ? lists.token[u.off + lane + 32] * 2 * g.K : 0;
         int x = u.k0 * kBK;
         for (int k = u.nk; k > 0; k -= 2) {
           ok = __all_sync(0xFFFFFFFFu, mbar_wait_lazy(&empty[s], ph, &abort_flag, g.status,
@@ -552,8 +615,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       int s = 0, local = 0;
       bool ok = true;
       if (UP) mx4::copy_scales(tmem + kConstCol, mx4::scale_desc_lo(smem_u32(const_sf)));
-      for (int i = blockIdx.x; i < units && ok; i += gridDim.x, ++local) {
-        const Unit u = unit_at(g, lists, i);
+      Unit u;
+      for (u.begin(g); ok && u.load(g, lists); u.next(g), ++local) {
         const int buf = local & 1;
         if (!mbar_wait_lazy(&acc_empty[buf], ((uint32_t)(local >> 1) & 1u) ^ 1u, &abort_flag,
                             g.status, kDevTimeoutMma))
@@ -609,8 +672,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int quarter = warp & 3, row = quarter * 32 + lane, et = (int)threadIdx.x - 64;
     const int width = g.tiles * kRows;
     int local = 0;
-    for (int i = blockIdx.x; i < units; i += gridDim.x, ++local) {
-      const Unit u = unit_at(g, lists, i);
+    Unit u;
+    for (u.begin(g); u.load(g, lists); u.next(g), ++local) {
       const int buf = local & 1;
       const bool ok = mbar_wait_lazy(&acc_full[buf], (uint32_t)(local >> 1) & 1u, &abort_flag,
                                      g.status, kDevTimeoutMma);
@@ -681,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
               }
             }
-            const float x = mine ? token_scale[lists.slot[u.off + j] / g.topk] : 0.0f;
+            const float x = mine ? token_scale[lists.token[u.off + j]] : 0.0f;
             const float gate[4] = {p0.x * x, p0.z * x, p1.x * x, p1.z * x};
             const float up[4] = {p0.y * x, p0.w * x, p1.y * x, p1.w * x};
             float h[4];
@@ -828,6 +891,16 @@ static Layout layout(int64_t T, int64_t H, int64_t E, int topk, int64_t I) {
   return l;
 }
 
+// The unit walk's constants for a grid of `grid` blocks.
+static void set_units(GemmArgs* g, int grid) {
+  g->per = g->tiles * g->splits;
+  g->step_a = grid / g->per;
+  g->step_rest = grid % g->per;
+  g->by_splits = (65536 + g->splits - 1) / g->splits;
+  g->by_topk = (65536 + g->topk - 1) / g->topk;
+  g->by_per = (65536 + g->per - 1) / g->per;
+}
+
 // 4-bit rows unpacked to 16 bytes for each 16 values on the way to shared memory
 // (row length and start a multiple of 128 values).
 static bool weights_map(CUtensorMap* map, const uint8_t* base, uint64_t rows, uint64_t K) {
@@ -930,6 +1003,7 @@ cudaError_t launch_moe(const MoeArgs& a, int sm_count, cudaStream_t st) {
   g.counters = counters;
   int64_t units = (int64_t)l.max_act * g.tiles * g.splits;
   cfg.gridDim = dim3((unsigned)(units < sm_count ? units : sm_count));
+  set_units(&g, (int)cfg.gridDim.x);
   e = cudaLaunchKernelEx(&cfg, k_moe_gemm<true>, tw13, th, g);
   if (e != cudaSuccess) return e;
 
@@ -941,6 +1015,7 @@ cudaError_t launch_moe(const MoeArgs& a, int sm_count, cudaStream_t st) {
   g.part = reinterpret_cast<float*>(w + l.part_down);
   units = (int64_t)l.max_act * g.tiles * g.splits;
   cfg.gridDim = dim3((unsigned)(units < sm_count ? units : sm_count));
+  set_units(&g, (int)cfg.gridDim.x);
   e = cudaLaunchKernelEx(&cfg, k_moe_gemm<false>, tw2, th, g);
   if (e != cudaSuccess) return e;
 
