@@ -1,28 +1,30 @@
 // Mixture-of-experts layer for a few tokens, experts in the microscaled 4-bit
-// form.  Bound by the bytes of the chosen experts' weights (17/32 a value); all
-// launches after the first are programmatic, so that a kernel's prologue overlaps
-// its predecessor's end.
+// form.  Bound by the bytes of the chosen experts' weights (17/32 a value), and with
+// one token by the latency of the steps between them; two launches.
 //
 //   k_moe_route   router logits (products exact in fp32 and summed in fp64), top-k and
 //                 probabilities, and the activations as two e4m3 rows a token
-//   k_moe_gemm    twice.  The tensor cores take the 4-bit weights as they are
-//                 (tcgen05.mma.kind::mxf8f6f4, e2m1 x e4m3): 128 rows of an expert's
-//                 matrix on the M side, its tokens on the N side.  The activations
-//                 enter as hi + lo, hi = e4m3(x / s), lo = e4m3(16 (x / s - hi)):
-//                 four significant bits each, so a bf16 value is held exactly
-//                 unless it is 2^14 times smaller than the largest of its row, and
-//                 then within 2^-21 of that.  A dequantised operand would cost
-//                 about one instruction a weight, which alone exceeds the time HBM
-//                 needs to deliver it.
-//     up          gate and up rows alternate, so a tile holds both factors of 64
-//                 values of h = silu(g) u; the epilogue writes h as two e4m3 rows
-//                 again, with a power-of-two scale for the tile's 64 values
+//   k_moe_experts everything else, one block an SM, launched cooperatively because its
+//                 blocks wait for one another's results: first the up products' units,
+//                 then the down products', then the weighted sums.  The ring of weight
+//                 tiles runs through all of it, so HBM is busy while a block waits for
+//                 the activations of its next product (as three kernels, the starts and
+//                 ends of each cost 15 us together).
+//     The tensor cores take the 4-bit weights as they are (tcgen05.mma.kind::mxf8f6f4,
+//     e2m1 x e4m3): 128 rows of an expert's matrix on the M side, its tokens on the N
+//     side.  The activations enter as hi + lo, hi = e4m3(x / s), lo = e4m3(16 (x / s -
+//     hi)): four significant bits each, so a bf16 value is held exactly unless it is
+//     2^14 times smaller than the largest of its row, and then within 2^-21 of that.  A
+//     dequantised operand would cost about one instruction a weight, which alone
+//     exceeds the time HBM needs to deliver it.
+//     up          gate and up rows alternate, so a tile holds both factors of 64 values
+//                 of h = silu(g) u; the epilogue writes h as two e4m3 rows again, with
+//                 a power-of-two scale for the tile's 64 values
 //     down        every slot's product times its probability goes to a buffer
-//   k_moe_combine adds a token's slots in the order of its choices: no sum depends on
-//                 timing (a count of arrivals at the end of each down unit cost three
-//                 times the unit's own work at 64 tokens)
-// With few units the K range is split; the up product's partial sums are added in order
-// by the unit that arrives last, the down product's by k_moe_combine.
+//     sums        a token's slots are added in the order of its choices
+// Few up units are split over K, their partial sums added in order by the unit that
+// arrives last; the down units' parts are added with the slots.  No result depends on
+// timing.
 #include "e8_internal.h"
 #include "e8_mx4.cuh"
 #include "e8_tmap.h"
@@ -225,32 +227,33 @@ __global__ void __cluster_dims__(kRouteCtas, 1, 1) __launch_bounds__(256)
   }
 }
 
-// ---------------------------------------------------------------- products ---
+// ----------------------------------------------------------------- experts ---
 constexpr int kThreads = 224;
 constexpr int kRows = 128;                 // rows of a unit
-constexpr int kBK = 128;                   // K of a stage
+constexpr int kBK = 128;                   // columns of a step: a tile of scales
 constexpr int kWBytes = kRows * kBK;       // 16 values in 16 bytes, 8 of them used
-constexpr int kMaxStages = 5;                // of 2 kBK columns: one barrier round for 16 KB of weights
+constexpr int kMaxStages = 5;              // of two steps: one barrier round for 16 KB of weights
 constexpr int kConstCol = 256, kSfCol = 264;   // tensor-memory columns of the scales
 constexpr int kRingBytes = 212 * 1024;
+constexpr int kMaxGrid = 160;              // blocks
+constexpr int kMaxUpParts = 8, kMaxDownParts = 16;   // K parts of a unit
 
-struct GemmArgs {
+struct ExpertArgs {
   const int32_t* experts;  // by slot = token * topk + choice
   const float* probs;
-  const uint8_t *w_codes, *w_scales;
-  int K, tiles, splits;    // tiles of 128 rows of one expert; K split in `splits`
-  // Divisions without a divide: `per` = tiles * splits units an expert, the block's first
-  // expert and rest, the grid's step in the same terms, and ceil(2^16 / d) for the
-  // divisors splits and topk (exact: dividend < 8192, divisor <= 16, product < 2^16 off)
-  int per, step_a, step_rest, by_splits, by_topk, by_per;
-  int T, E, topk, stages, b_rows;
-  const uint8_t* xq;       // up: the tokens' hi and lo rows
-  const float* xs;         // up: scale of each token's pair
-  uint8_t* hq;             // up: writes, down: reads through the tensor map
+  const uint8_t *w13_codes, *w13_scales, *w2_codes, *w2_scales;
+  int T, E, topk, by_topk, H, I;   // by_topk = ceil(2^16 / topk): a slot's token without a divide
+  int down_parts, stages, b_rows;
+  const uint8_t* xq;       // the tokens' hi and lo rows
+  const float* xs;         // scale of each token's pair
+  uint8_t* hq;             // the slots' hi and lo rows of h, sorted by expert
   uint8_t* h_scales;       // [active expert][I / 128][512]
-  int I;
-  float* part;             // partial sums / slot products, fp32
-  int* counters;
+  float* part_up;          // [up unit * parts + part][T][128]
+  float* part_down;        // [part][slot][H]
+  int* up_done;            // [active expert]: finished tiles
+  int* up_joined;          // [up unit]: arrived parts
+  int* down_done;          // [tile]: finished units
+  uint16_t* Y;
   uint32_t* status;
 };
 
@@ -260,11 +263,35 @@ __device__ __forceinline__ void bar_sync(uint32_t id, uint32_t n) {
 __device__ __forceinline__ void prefetch_l2(const void* p) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
-// Counts this block's arrival after its other threads' writes (a barrier came before).
+// One thread tells (or counts) for its block after a barrier that the others' writes
+// came before.
+__device__ __forceinline__ void signal_gpu(int* counter) {
+  asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(counter) : "memory");
+}
 __device__ __forceinline__ int arrive_gpu(int* counter) {
   int old;
   asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(old) : "l"(counter) : "memory");
   return old;
+}
+// Waits until *counter has reached `want`; bounded as mbar_wait_lazy is.
+__device__ __forceinline__ bool wait_gpu(const int* counter, int want,
+                                         volatile uint32_t* abort_flag, uint32_t* status) {
+  uint64_t t0 = 0;
+  for (uint32_t it = 1;; ++it) {
+    int v;
+    asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(counter) : "memory");
+    if (v >= want) return true;
+    if ((it & 31u) == 0) {
+      if (ld_shared_volatile(abort_flag)) return false;
+      const uint64_t t = global_timer_ns();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > kWaitLimitNs) {
+        st_shared_volatile(abort_flag, 1u);
+        if (status) atomicOr(status, kDevTimeoutCluster);
+        return false;
+      }
+    }
+  }
 }
 __device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -274,84 +301,46 @@ __device__ __forceinline__ void copy_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
                : "memory");
 }
+
 // Slots sorted by expert: active expert a (in order of number) has the slots
 // slot[off[a]] .. slot[off[a + 1] - 1], by rising slot.
 struct SharedLists {
   int16_t expert[kMaxExperts], off[kMaxExperts + 1], slot[kMaxSlots];
   uint8_t token[kMaxSlots];
-  int16_t k_at[9];   // first 128-column step of each K part
   int nact;
   uint32_t wsum[8];
 };
+static_assert(kMaxTokens == 64, "a token is a bit of an expert's mask");
 
-// Up to 32 slots: one warp, a lane a slot.
-__device__ __forceinline__ void build_small(SharedLists& l, const int32_t* __restrict__ experts,
-                                            int slots, int by_topk) {
-  const int lane = threadIdx.x & 31;
-  const int e = lane < slots ? experts[lane] : INT32_MAX;
-  const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
-  const bool head = (same & ((1u << lane) - 1u)) == 0 && lane < slots;
-  // slots and active experts before this one's
-  int pos = __popc(same & ((1u << lane) - 1u)), act = 0;
-#pragma unroll 4
-  for (int j = 0; j < slots; ++j) {
-    const int other = __shfl_sync(0xFFFFFFFFu, e, j);
-    const bool other_head = __shfl_sync(0xFFFFFFFFu, (int)head, j) != 0;
-    pos += other < e;
-    act += other < e && other_head;
-  }
-  if (lane < slots) {
-    l.slot[pos] = (int16_t)lane;
-    l.token[pos] = (uint8_t)(lane * by_topk >> 16);
-    if (head) {
-      l.expert[act] = (int16_t)e;
-      l.off[act] = (int16_t)pos;
-    }
-  }
-  const int nact = __popc(__ballot_sync(0xFFFFFFFFu, head));
-  if (lane == 0) {
-    l.off[nact] = (int16_t)slots;
-    l.nact = nact;
-  }
-}
-
-// Any number (all threads; `scratch`: 32 E + 4 kMaxSlots + 2 E bytes).
-__device__ __forceinline__ void build_lists(SharedLists& l, uint8_t* scratch,
+// Builds the lists (all threads).  mask[e]: the tokens that chose expert e, zero on
+// entry; a token chooses an expert once, so its place is the number of lower bits.
+// chosen: the expert of each slot; first: slots before an expert's.
+__device__ __forceinline__ void build_lists(SharedLists& l, unsigned long long* mask,
+                                            int16_t* chosen, int16_t* first,
                                             const int32_t* __restrict__ experts, int slots, int E,
                                             int by_topk) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int groups = (slots + 31) / 32;
-  uint8_t* count = scratch;   // [groups][E]: slots of an expert in a group of 32 slots
-  int16_t* se = reinterpret_cast<int16_t*>(scratch + 32 * kMaxExperts);
-  int16_t* sp = se + kMaxSlots;
-  int16_t* first = sp + kMaxSlots;
-  for (int i = tid; i < (groups * E + 3) / 4; i += kThreads)
-    reinterpret_cast<uint32_t*>(count)[i] = 0;
-  __syncthreads();
-  for (int g = warp; g < groups; g += kThreads / 32) {
-    const int s = g * 32 + lane, e = s < slots ? experts[s] : -1;
-    const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
-    const int place = __popc(same & ((1u << lane) - 1u));
-    if (e >= 0 && place == 0) count[g * E + e] = (uint8_t)__popc(same);
-    se[s] = (int16_t)e;
-    sp[s] = (int16_t)place;
+#pragma unroll
+  for (int i = 0; i < (kMaxSlots + kThreads - 1) / kThreads; ++i) {
+    const int s = tid + i * kThreads;
+    if (s < slots) {
+      const int e = experts[s], t = s * by_topk >> 16;
+      chosen[s] = (int16_t)e;
+      atomicOr(reinterpret_cast<uint32_t*>(mask + e) + (t >> 5), 1u << (t & 31));
+    }
   }
   __syncthreads();
-  // running counts over the groups, then a scan over experts of (is active, slots)
-  const int per = (E + kThreads - 1) / kThreads;
-  uint32_t mine = 0;
-  for (int e = tid * per; e < min(E, (tid + 1) * per); ++e) {
-    uint32_t run = 0;
-#pragma unroll 4
-    for (int g = 0; g < groups; ++g) {
-      const uint32_t c = count[g * E + e];
-      count[g * E + e] = (uint8_t)run;
-      run += c;
-    }
-    first[e] = (int16_t)run;
-    mine += run ? (1u << 16) | run : 0u;
+  // a scan over experts of (is active, slots) in one word
+  constexpr int kPer = (kMaxExperts + kThreads - 1) / kThreads;
+  uint32_t mine = 0, n[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int e = tid * kPer + i;
+    n[i] = e < E ? (uint32_t)__popcll(mask[e]) : 0u;
+    mine += n[i] ? (1u << 16) | n[i] : 0u;
   }
   uint32_t scan = mine;
+#pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, scan, o);
     if (lane >= o) scan += u;
@@ -359,17 +348,19 @@ __device__ __forceinline__ void build_lists(SharedLists& l, uint8_t* scratch,
   if (lane == 31) l.wsum[warp] = scan;
   __syncthreads();
   uint32_t at = scan - mine, total = 0;
+#pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) at += l.wsum[w];
     total += l.wsum[w];
   }
-  for (int e = tid * per; e < min(E, (tid + 1) * per); ++e) {
-    const uint32_t n = (uint32_t)first[e];
-    first[e] = (int16_t)(at & 0xFFFFu);
-    if (n) {
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int e = tid * kPer + i;
+    if (n[i]) {
+      first[e] = (int16_t)(at & 0xFFFFu);
       l.expert[at >> 16] = (int16_t)e;
       l.off[at >> 16] = (int16_t)(at & 0xFFFFu);
-      at += (1u << 16) | n;
+      at += (1u << 16) | n[i];
     }
   }
   if (tid == 0) {
@@ -378,50 +369,107 @@ __device__ __forceinline__ void build_lists(SharedLists& l, uint8_t* scratch,
   }
   __syncthreads();
   for (int s = tid; s < slots; s += kThreads) {
-    const int pos = first[se[s]] + count[(s >> 5) * E + se[s]] + sp[s];
+    const int t = s * by_topk >> 16, e = chosen[s];
+    const int pos = first[e] + __popcll(mask[e] & ((1ull << t) - 1ull));
     l.slot[pos] = (int16_t)s;
-    l.token[pos] = (uint8_t)(s * by_topk >> 16);
+    l.token[pos] = (uint8_t)t;
   }
   fence_proxy_async_smem();   // the scratch space becomes the copies' ring
+  __syncthreads();
 }
 
-// The units of one block in turn: all row tiles and K parts of an expert, then the next.
-struct Unit {
-  int a, rest;                                    // active expert; tile * splits + part
-  int tile, part, expert, off, n, k0, nk;
-  __device__ __forceinline__ void begin(const GemmArgs& g) {
-    a = g.per > (int)blockIdx.x ? 0 : (int)blockIdx.x * g.by_per >> 16;
-    rest = (int)blockIdx.x - a * g.per;
+// The units of one block in turn.  All units of the layer are numbered, the up
+// products' first (row tiles of an expert, each in `up_parts` parts of K, then the next
+// expert's), the down products' after them, and dealt to the blocks in that order.
+// Walking the numbers needs quotients only once.
+struct Plan {
+  int up_parts, by_up, by_down;        // by_*: ceil(2^16 / parts)
+  int per_up, per_down;                // units of an expert
+  int up_a, up_rest, up_step_a, up_step_rest;
+  int down_a, down_rest, down_step_a, down_step_rest;
+};
+// x / d = x * ceil(2^16 / d) >> 16 while x d < 2^16; for K steps of parts (up to 512 x
+// 16) it may be one more, but is 0 and all at the ends and rises, which is enough.
+__device__ __forceinline__ int reciprocal(int d) { return (65535 + d) / d; }
+
+// One warp; lanes 0..3 take a quotient each.
+__device__ __forceinline__ void make_plan(Plan& p, const ExpertArgs& g, int nact) {
+  const int lane = threadIdx.x & 31, b = (int)blockIdx.x, grid = (int)gridDim.x;
+  const int up_tiles = 2 * g.I / kRows, down_tiles = g.H / kRows;
+  const int units = nact * up_tiles;
+  const int parts = units * 2 > grid ? 1 : min(min(kMaxUpParts, grid / units), g.H / kBK);
+  const int per_up = up_tiles * parts, per_down = down_tiles * g.down_parts;
+  const int num = lane == 0 ? b : lane == 2 ? nact * per_up : grid;
+  const int den = lane < 2 ? per_up : lane == 2 ? grid : per_down;
+  const int q = num / den, r = num - q * den;
+  const int up_left = __shfl_sync(0xFFFFFFFFu, r, 2);   // blocks of the last up round
+  const int first = b >= up_left ? b - up_left : b - up_left + grid;
+  const int first_a = first / per_down;
+  if (lane == 0) {
+    p.up_parts = parts;
+    p.by_up = reciprocal(parts);
+    p.per_up = per_up;
+    p.per_down = per_down;
+    p.up_a = q;
+    p.up_rest = r;
+    p.down_a = first_a;
+    p.down_rest = first - first_a * per_down;
+  } else if (lane == 1) {
+    p.up_step_a = q;
+    p.up_step_rest = r;
+    p.by_down = reciprocal(g.down_parts);
+  } else if (lane == 3) {
+    p.down_step_a = q;
+    p.down_step_rest = r;
   }
-  __device__ __forceinline__ void next(const GemmArgs& g) {
-    a += g.step_a;
-    rest += g.step_rest;
-    if (rest >= g.per) {
-      rest -= g.per;
+}
+
+struct Unit {
+  bool down;
+  int a, rest;                       // active expert; tile * parts + part
+  int tile, part, expert, off, n;    // n tokens from slot[off] on
+  int k0, nk;                        // steps of K
+  __device__ __forceinline__ void begin(const Plan& p) {
+    down = false;
+    a = p.up_a;
+    rest = p.up_rest;
+  }
+  __device__ __forceinline__ void next(const Plan& p) {
+    a += down ? p.down_step_a : p.up_step_a;
+    rest += down ? p.down_step_rest : p.up_step_rest;
+    const int per = down ? p.per_down : p.per_up;
+    if (rest >= per) {
+      rest -= per;
       ++a;
     }
   }
   // false after the last unit
-  __device__ __forceinline__ bool load(const GemmArgs& g, const SharedLists& l) {
+  __device__ __forceinline__ bool load(const Plan& p, const ExpertArgs& g, const SharedLists& l) {
+    if (!down && a >= l.nact) {
+      down = true;
+      a = p.down_a;
+      rest = p.down_rest;
+    }
     if (a >= l.nact) return false;
-    tile = rest * g.by_splits >> 16;
-    part = rest - tile * g.splits;
+    const int parts = down ? g.down_parts : p.up_parts, by = down ? p.by_down : p.by_up;
+    const int kq = (down ? g.I : g.H) / kBK;
+    tile = rest * by >> 16;
+    part = rest - tile * parts;
     expert = l.expert[a];
     off = l.off[a];
     n = l.off[a + 1] - off;
-    k0 = l.k_at[part];
-    nk = l.k_at[part + 1] - k0;
+    k0 = kq * part * by >> 16;
+    nk = (kq * (part + 1) * by >> 16) - k0;
     return true;
   }
 };
 
-// Warps: 0 weights producer, 6 tokens producer, 1 MMAs, 2..5 epilogue.  At 16 KB of
+// Warps: 0 weights producer, 6 activations producer, 1 MMAs, 2..5 epilogue.  At 16 KB of
 // weights a stage the SM's share of HBM leaves each role some 700 cycles a stage: one
 // elected thread runs a role's whole loop with its addresses in registers.
-template <bool UP>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_moe_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmB,
-               const __grid_constant__ GemmArgs g) {
+    k_moe_experts(const __grid_constant__ CUtensorMap tm13, const __grid_constant__ CUtensorMap tm2,
+                  const __grid_constant__ ExpertArgs g) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -430,6 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ int ready;
   __shared__ float token_scale[kMaxTokens];
   __shared__ SharedLists lists;
+  __shared__ Plan plan;
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drain;
   __shared__ uint32_t tmem_slot;
   __shared__ volatile uint32_t abort_flag;
@@ -440,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < g.stages; ++s) {
-      mbar_init(&full[s], UP ? 33 : 2);   // the weights' producer, and the tokens'
+      mbar_init(&full[s], 33);   // the weights' producer, and the lanes of the other
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -450,49 +499,47 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&drain, 1);
     abort_flag = 0u;
     fence_mbar_init();
-    tma_prefetch_desc(&tmW);
-    if (!UP) tma_prefetch_desc(&tmB);
+    tma_prefetch_desc(&tm13);
+    tma_prefetch_desc(&tm2);
   }
   if (warp == 1) {
     tmem_alloc(&tmem_slot, 512);
     tmem_relinquish();
   }
-  if (UP && threadIdx.x >= 64 && threadIdx.x < 192) {
-    // scales of the activations: 1 for hi rows (even), 2^-4 for lo rows
+  if (threadIdx.x >= 64 && threadIdx.x < 192) {
+    // scales of the tokens' rows: 1 for hi rows (even), 2^-4 for lo rows
     reinterpret_cast<uint32_t*>(const_sf)[threadIdx.x - 64] =
         ((threadIdx.x - 64) / 4) & 1 ? 0x7B7B7B7Bu : 0x7F7F7F7Fu;
     fence_proxy_async_smem();
   }
-  if (UP) {
-    grid_dep_wait();
-    grid_dep_launch();
-  }
-  // (down: the choice was complete before the up kernel let this one start)
-  if (!UP) grid_dep_launch();
+  unsigned long long* mask = reinterpret_cast<unsigned long long*>(smem);
+  int16_t* chosen = reinterpret_cast<int16_t*>(mask + kMaxExperts);
+  for (int i = threadIdx.x; i < g.E; i += kThreads) mask[i] = 0ull;
   tc_fence_before();
-  const int slots = g.T * g.topk;
-  if (UP && threadIdx.x < g.T) token_scale[threadIdx.x] = g.xs[threadIdx.x];
-  if (threadIdx.x >= 128 && threadIdx.x <= 128 + g.splits)
-    lists.k_at[threadIdx.x - 128] =
-        (int16_t)((g.K / kBK) * ((int)threadIdx.x - 128) * g.by_splits >> 16);
-  if (slots > 32) build_lists(lists, smem, g.experts, slots, g.E, g.by_topk);
-  else if (warp == 2) build_small(lists, g.experts, slots, g.by_topk);
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
+  grid_dep_wait();
+  const int slots = g.T * g.topk;
+  if (threadIdx.x < g.T) token_scale[threadIdx.x] = g.xs[threadIdx.x];
+  build_lists(lists, mask, chosen, chosen + kMaxSlots, g.experts, slots, g.E, g.by_topk);
+  if (warp == 0) make_plan(plan, g, lists.nact);
+  __syncthreads();
   const uint32_t ring = smem_u32(smem);
-  const int kqs = g.K / kBK;
+  const int up_tiles = 2 * g.I / kRows, down_tiles = g.H / kRows;
 
   if (warp == 0) {
     if (elect_one()) {
-      // codes and scales of the weights; they do not depend on the preceding kernel
       uint32_t st = ring, ph = 1;
       int s = 0;
       bool ok = true;
       Unit u;
-      for (u.begin(g); ok && u.load(g, lists); u.next(g)) {
-        const int row = (u.expert * g.tiles + u.tile) * kRows;
-        const uint8_t* sf = g.w_scales + ((int64_t)(row >> 7) * kqs + u.k0) * 512;
+      for (u.begin(plan); ok && u.load(plan, g, lists); u.next(plan)) {
+        const int kqs = (u.down ? g.I : g.H) / kBK;
+        const int row = (u.expert * (u.down ? down_tiles : up_tiles) + u.tile) * kRows;
+        const uint8_t* sf =
+            (u.down ? g.w2_scales : g.w13_scales) + ((int64_t)(row >> 7) * kqs + u.k0) * 512;
+        const CUtensorMap* map = u.down ? &tm2 : &tm13;
         int x = u.k0 * kBK;
         bool ahead = true;
         for (int k = u.nk; k > 0; k -= 2) {
@@ -501,18 +548,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           // the tensor map unpacks: its bytes are counted as they lie in memory
           const uint32_t half = k > 1 ? 2u : 1u;
           mbar_arrive_expect_tx(&full[s], half * (kWBytes / 2 + 512u));
-          load_2d(st, &tmW, &full[s], x, row);
-          if (k > 1) load_2d(st + kWBytes, &tmW, &full[s], x + kBK, row);
+          load_2d(st, map, &full[s], x, row);
+          if (k > 1) load_2d(st + kWBytes, map, &full[s], x + kBK, row);
           load_bulk(st + 2u * (kWBytes + b_bytes), sf, half * 512u, &full[s]);
           if (ahead) {
             // the next unit lies in other pages: a first access there costs microseconds
             // (address translation) and the ring holds less than two
             Unit v = u;
-            v.next(g);
-            if (v.load(g, lists)) {
-              const int64_t next = (int64_t)(v.expert * g.tiles + v.tile);
-              prefetch_l2(g.w_codes + next * kRows * (g.K / 2) + v.k0 * 64);
-              prefetch_l2(g.w_scales + (next * kqs + v.k0) * 512);
+            v.next(plan);
+            if (v.load(plan, g, lists)) {
+              const int cols = v.down ? g.I : g.H;
+              const int64_t tile = (int64_t)v.expert * (v.down ? down_tiles : up_tiles) + v.tile;
+              prefetch_l2((v.down ? g.w2_codes : g.w13_codes) + tile * kRows * (cols / 2) +
+                          v.k0 * 64);
+              prefetch_l2((v.down ? g.w2_scales : g.w13_scales) +
+                          (tile * (cols / kBK) + v.k0) * 512);
             }
             ahead = false;
           }
@@ -528,83 +578,54 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 6) {
-    if (!UP) {
-      // until the up product has ended HBM would idle: the first unit's weights beyond
-      // the ring go to L2
-      Unit u;
-      u.begin(g);
-      if (u.load(g, lists)) {
-        const uint8_t* at = g.w_codes + (int64_t)(u.expert * g.tiles + u.tile) * kRows * (g.K / 2) +
-                            u.k0 * 64;
-        for (int r = lane; r < kRows; r += 32)
-          bulk_prefetch_l2(at + (int64_t)r * (g.K / 2), (uint32_t)u.nk * 64u);
+    // 16 lanes copy the 256 bytes of each of a token's two rows, 16 bytes a lane, to
+    // where the 128-byte swizzle has them
+    const int r = lane >> 4, c = lane & 15;
+    const uint32_t to = (c >> 3) * b_bytes + (uint32_t)r * 128u;
+    uint32_t st = ring + 2u * kWBytes, ph = 1;
+    int s = 0;
+    bool ok = true;
+    Unit u;
+    for (u.begin(plan); ok && u.load(plan, g, lists); u.next(plan)) {
+      const int cols = u.down ? g.I : g.H;
+      const uint8_t* src = (u.down ? g.hq + (size_t)u.off * 2 * g.I : g.xq) + (size_t)r * cols + c * 16;
+      const int row0 = (u.down ? lane : lane < u.n ? lists.token[u.off + lane] : 0) * 2 * cols;
+      const int row1 =
+          (u.down ? lane + 32 : lane + 32 < u.n ? lists.token[u.off + lane + 32] : 0) * 2 * cols;
+      const uint8_t* sf = g.h_scales + ((int64_t)u.a * (g.I / kBK) + u.k0) * 512 + lane * 16;
+      if (u.down) {
+        // every tile of the expert's h
+        ok = lane != 0 || wait_gpu(&g.up_done[u.a], up_tiles, &abort_flag, g.status);
+        __syncwarp();
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
       }
-      // sorted by expert: sixteen rows a copy
-      grid_dep_wait();
-      if (elect_one()) {
-        uint32_t st = ring + 2u * kWBytes, ph = 1;
-        int s = 0;
-        bool ok = true;
-        for (; ok && u.load(g, lists); u.next(g)) {
-          const uint8_t* sf = g.h_scales + ((int64_t)u.a * kqs + u.k0) * 512;
-          const uint32_t copies = (uint32_t)(u.n + 7) / 8;
-          int x = u.k0 * kBK;
-          for (int k = u.nk; k > 0; k -= 2) {
-            ok = mbar_wait_lazy(&empty[s], ph, &abort_flag, g.status, kDevTimeoutEmpty);
-            if (!ok) break;
-            const uint32_t half = k > 1 ? 2u : 1u;
-            mbar_arrive_expect_tx(&full[s], half * (copies * 2048u + 512u));
-            for (uint32_t q = 0; q < copies; ++q) {
-              load_2d(st + q * 2048u, &tmB, &full[s], x, 2 * u.off + (int)q * 16);
-              if (k > 1)
-                load_2d(st + b_bytes + q * 2048u, &tmB, &full[s], x + kBK, 2 * u.off + (int)q * 16);
-            }
-            load_bulk(st + 2u * b_bytes + 1024u, sf, half * 512u, &full[s]);
-            x += 2 * kBK;
-            sf += 1024;
-            st += stage_bytes;
-            if (++s == g.stages) {
-              s = 0;
-              ph ^= 1u;
-              st = ring + 2u * kWBytes;
-            }
-          }
-        }
-      }
-    } else {
-      // tokens lie in order of the batch; 16 lanes copy the 256 bytes of each of a
-      // token's two rows, 16 bytes a lane, to where the 128-byte swizzle has them
-      const int r = lane >> 4, c = lane & 15;
-      const uint8_t* src = g.xq + (size_t)r * g.K + c * 16;
-      const uint32_t to = (c >> 3) * b_bytes + (uint32_t)r * 128u;
-      uint32_t st = ring + 2u * kWBytes, ph = 1;
-      int s = 0;
-      bool ok = true;
-      Unit u;
-      for (u.begin(g); ok && u.load(g, lists); u.next(g)) {
-        const int row0 = lane < u.n ? lists.token[u.off + lane] * 2 * g.K : 0;
-        const int row1 = lane + 32 < u.n ? lists.token[u.off + lane + 32] * 2 * g.K : 0;
-        int x = u.k0 * kBK;
-        for (int k = u.nk; k > 0; k -= 2) {
-          ok = __all_sync(0xFFFFFFFFu, mbar_wait_lazy(&empty[s], ph, &abort_flag, g.status,
-                                                      kDevTimeoutEmpty));
-          if (!ok) break;
-          uint32_t dst = st + to;
+      int x = u.k0 * kBK;
+      for (int k = u.nk; k > 0; k -= 2) {
+        ok = __all_sync(0xFFFFFFFFu,
+                        mbar_wait_lazy(&empty[s], ph, &abort_flag, g.status, kDevTimeoutEmpty));
+        if (!ok) break;
+        uint32_t dst = st + to;
 #pragma unroll 4
-          for (int j = 0; j < u.n; ++j) {
-            const int row = __shfl_sync(0xFFFFFFFFu, j < 32 ? row0 : row1, j & 31);
-            if (k > 1 || c < 8)
-              copy_async16(dst + (uint32_t)(((c & 7) ^ ((2 * j + r) & 7)) << 4), src + row + x);
-            dst += 256u;
-          }
-          copy_async_arrive(&full[s]);
-          x += 2 * kBK;
-          st += stage_bytes;
-          if (++s == g.stages) {
-            s = 0;
-            ph ^= 1u;
-            st = ring + 2u * kWBytes;
-          }
+        for (int j = 0; j < u.n; ++j) {
+          const int row = __shfl_sync(0xFFFFFFFFu, j < 32 ? row0 : row1, j & 31);
+          if (k > 1 || c < 8)
+            copy_async16(dst + (uint32_t)(((c & 7) ^ ((2 * j + r) & 7)) << 4), src + row + x);
+          dst += 256u;
+        }
+        if (u.down) {
+          const uint32_t f = st + 2u * b_bytes + 1024u + (uint32_t)lane * 16u;
+          copy_async16(f, sf);
+          if (k > 1) copy_async16(f + 512u, sf + 512);
+        }
+        copy_async_arrive(&full[s]);
+        x += 2 * kBK;
+        sf += 1024;
+        st += stage_bytes;
+        if (++s == g.stages) {
+          s = 0;
+          ph ^= 1u;
+          st = ring + 2u * kWBytes;
         }
       }
     }
@@ -614,9 +635,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t st = ring >> 4, ph = 0, cols = tmem + kSfCol;
       int s = 0, local = 0;
       bool ok = true;
-      if (UP) mx4::copy_scales(tmem + kConstCol, mx4::scale_desc_lo(smem_u32(const_sf)));
+      mx4::copy_scales(tmem + kConstCol, mx4::scale_desc_lo(smem_u32(const_sf)));
       Unit u;
-      for (u.begin(g); ok && u.load(g, lists); u.next(g), ++local) {
+      for (u.begin(plan); ok && u.load(plan, g, lists); u.next(plan), ++local) {
         const int buf = local & 1;
         if (!mbar_wait_lazy(&acc_empty[buf], ((uint32_t)(local >> 1) & 1u) ^ 1u, &abort_flag,
                             g.status, kDevTimeoutMma))
@@ -628,16 +649,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = mbar_wait_lazy(&full[s], ph, &abort_flag, g.status, kDevTimeoutFull);
           if (!ok) break;
           tc_fence_after();
-          if (UP) fence_proxy_async_smem();   // the tokens' rows came by ordinary copies
+          fence_proxy_async_smem();   // the activations came by ordinary copies
           const uint32_t w = mx4::code_desc_lo(st << 4), b = w + b_off;
           const uint32_t w1 = w + (kWBytes >> 4), b1 = b + (b_bytes >> 4);
           const uint32_t f = mx4::scale_desc_lo((st + f_off) << 4);
-          const uint32_t sfb = UP ? tmem + kConstCol : cols + 8u, sfb1 = UP ? sfb : sfb + 4u;
+          const uint32_t sfb = u.down ? cols + 8u : tmem + kConstCol, sfb1 = u.down ? sfb + 4u : sfb;
           mx4::copy_scales(cols, f);
-          if (!UP) mx4::copy_scales(sfb, f + 64u);
+          if (u.down) mx4::copy_scales(sfb, f + 64u);
           if (k > 1) {
             mx4::copy_scales(cols + 4u, f + 32u);
-            if (!UP) mx4::copy_scales(sfb1, f + 96u);
+            if (u.down) mx4::copy_scales(sfb1, f + 96u);
           }
 #pragma unroll
           for (uint32_t j = 0; j < 4; ++j)
@@ -670,17 +691,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     const int quarter = warp & 3, row = quarter * 32 + lane, et = (int)threadIdx.x - 64;
-    const int width = g.tiles * kRows;
     int local = 0;
+    bool done = false;
     Unit u;
-    for (u.begin(g); u.load(g, lists); u.next(g), ++local) {
-      const int buf = local & 1;
-      const bool ok = mbar_wait_lazy(&acc_full[buf], (uint32_t)(local >> 1) & 1u, &abort_flag,
-                                     g.status, kDevTimeoutMma);
-      __syncwarp();
-      if (bar_red_or(1, 128, !ok)) break;
-      tc_fence_after();
-      const uint32_t d = tmem + (uint32_t)buf * 128u + ((uint32_t)(quarter * 32) << 16);
+    // The first two passes are rehearsals without tokens, of an up and of a down unit:
+    // their instructions come from memory while the first products are under way, and not
+    // when their sums are waited for.
+    for (int pass = 0;; ++pass) {
+      const bool live = pass > 1;
+      uint32_t d = tmem + ((uint32_t)(quarter * 32) << 16);
+      int n = 0;
+      if (pass < 2) {
+        u.a = u.off = u.tile = u.part = 0;
+        u.down = pass == 1;
+      } else {
+        if (pass == 2) u.begin(plan);
+        if (!u.load(plan, g, lists)) {
+          done = true;
+          break;
+        }
+        const int buf = local & 1;
+        const bool ok = mbar_wait_lazy(&acc_full[buf], (uint32_t)(local >> 1) & 1u, &abort_flag,
+                                       g.status, kDevTimeoutMma);
+        __syncwarp();
+        if (bar_red_or(1, 128, !ok)) break;
+        tc_fence_after();
+        d += (uint32_t)buf * 128u;
+        n = u.n;
+      }
+      const int parts = live && !u.down ? plan.up_parts : 1;
       // eight tokens' values of this row (hi + lo)
       auto read8 = [&](int j0, float (&v)[8]) {
         uint32_t r[16];
@@ -693,32 +732,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto release = [&]() {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&acc_empty[buf]);
+        if (live && lane == 0) mbar_arrive(&acc_empty[local & 1]);
       };
-      if (UP) {
+      if (!u.down) {
+        const int unit = u.a * up_tiles + u.tile;
+        float* part = g.part_up + (size_t)unit * parts * g.T * kRows;
         bool last = true;
-        if (g.splits > 1) {
+        if (parts > 1) {
 #pragma unroll 1
-          for (int j0 = 0; j0 < u.n; j0 += 8) {
+          for (int j0 = 0; j0 < n; j0 += 8) {
             float v[8];
             read8(j0, v);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-              if (j0 + j < u.n)
-                g.part[((size_t)u.part * slots + u.off + j0 + j) * width + u.tile * kRows + row] =
-                    v[j];
+              if (j0 + j < n) part[((size_t)u.part * g.T + j0 + j) * kRows + row] = v[j];
           }
-          release();
           bar_sync(1, 128);
-          if (et == 0)
-            ready = arrive_gpu(&g.counters[u.a * g.tiles + u.tile]) == g.splits - 1;
+          if (et == 0) ready = arrive_gpu(&g.up_joined[unit]) == parts - 1;
           bar_sync(1, 128);
           last = ready != 0;
         }
         if (last) {
+          int j0 = 0;
 #pragma unroll 1
-          for (int j0 = 0; j0 < u.n; j0 += 8) {
-            if (g.splits == 1) {
+          do {
+            if (parts == 1) {
               float v[8];
               read8(j0, v);
 #pragma unroll
@@ -727,21 +765,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // 16 lanes a token, four values of h (eight rows) a lane
             const int j = j0 + et / 16, q = et & 15;
-            const bool mine = j < u.n;
+            const bool mine = j < n;
             float4 p0 = make_float4(0, 0, 0, 0), p1 = p0;
-            if (mine) {
-              if (g.splits == 1) {
-                p0 = *reinterpret_cast<const float4*>(&stage_v[et / 16][q * 8]);
-                p1 = *reinterpret_cast<const float4*>(&stage_v[et / 16][q * 8 + 4]);
-              } else {
-                const float* at = g.part + (size_t)(u.off + j) * width + u.tile * kRows + q * 8;
-                for (int p = 0; p < g.splits; ++p) {
+            if (parts == 1) {
+              p0 = *reinterpret_cast<const float4*>(&stage_v[et / 16][q * 8]);
+              p1 = *reinterpret_cast<const float4*>(&stage_v[et / 16][q * 8 + 4]);
+            } else if (mine) {
+              const float* at = part + (size_t)j * kRows + q * 8;
+#pragma unroll
+              for (int p = 0; p < kMaxUpParts; ++p) {
+                if (p < parts) {
                   const float4 a = __ldcg(reinterpret_cast<const float4*>(at));
                   const float4 b = __ldcg(reinterpret_cast<const float4*>(at + 4));
                   p0.x += a.x; p0.y += a.y; p0.z += a.z; p0.w += a.w;
                   p1.x += b.x; p1.y += b.y; p1.z += b.z; p1.w += b.w;
-                  at += (size_t)slots * width;
                 }
+                at += (size_t)g.T * kRows;
               }
             }
             const float x = mine ? token_scale[lists.token[u.off + j]] : 0.0f;
@@ -778,26 +817,59 @@ __global__ void __launch_bounds__(kThreads, 1)
                     (r >> 5) * 4 + (at & 127) / 32) = (uint16_t)(by | by << 8);
               }
             }
-            if (g.splits == 1) bar_sync(1, 128);   // stage_v is free again
-          }
+            bar_sync(1, 128);   // stage_v is free again; h is written
+            j0 += 8;
+          } while (j0 < n);
+          if (live && et == 0) signal_gpu(&g.up_done[u.a]);
         }
-        if (g.splits == 1) release();
+        release();
       } else {
+        int j0 = 0;
 #pragma unroll 1
-        for (int j0 = 0; j0 < u.n; j0 += 8) {
+        do {
           float v[8];
           read8(j0, v);
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            if (j0 + j < u.n) {
+            if (j0 + j < n) {
               const int slot = lists.slot[u.off + j0 + j];
-              g.part[((size_t)u.part * slots + slot) * width + u.tile * kRows + row] =
+              g.part_down[((size_t)u.part * slots + slot) * g.H + u.tile * kRows + row] =
                   v[j] * __ldg(&g.probs[slot]);
             }
-        }
+          j0 += 8;
+        } while (j0 < n);
         release();
+        bar_sync(1, 128);
+        if (live && et == 0) signal_gpu(&g.down_done[u.tile]);
       }
-      if (UP && g.splits > 1) bar_sync(1, 128);   // `ready` is free again
+      if (live) {
+        u.next(plan);
+        ++local;
+      }
+    }
+    // Y: 128 columns of four tokens an item, a warp a token, four columns a lane
+    const int items = down_tiles * ((g.T + 3) / 4);
+    for (int item = (int)blockIdx.x; done && item < items; item += (int)gridDim.x) {
+      const int tile = item % down_tiles, t = item / down_tiles * 4 + quarter;
+      const bool ok =
+          et != 0 || wait_gpu(&g.down_done[tile], lists.nact * g.down_parts, &abort_flag, g.status);
+      __syncwarp();
+      if (bar_red_or(1, 128, !ok)) break;
+      if (t < g.T) {
+        const int col = tile * kRows + lane * 4;
+        const float* at = g.part_down + (size_t)t * g.topk * g.H + col;
+        float4 y = make_float4(0, 0, 0, 0);
+        for (int p = 0; p < g.down_parts; ++p) {
+#pragma unroll 8
+          for (int c = 0; c < g.topk; ++c) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(at + (size_t)c * g.H));
+            y.x += v.x; y.y += v.y; y.z += v.z; y.w += v.w;
+          }
+          at += (size_t)slots * g.H;
+        }
+        *reinterpret_cast<uint2*>(g.Y + (size_t)t * g.H + col) =
+            make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+      }
     }
   }
   __syncwarp();
@@ -815,32 +887,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_dealloc(tmem, 512);
   }
 }
-// Y[t] = sum of the slots' shares, by K part and then by choice; four columns a thread.
-__global__ void __launch_bounds__(128)
-    k_moe_combine(const float* __restrict__ part, int topk, int splits, int slots, int H,
-                  uint16_t* __restrict__ Y) {
-  const int col = ((int)blockIdx.x * 128 + (int)threadIdx.x) * 4, t = blockIdx.y;
-  grid_dep_wait();
-  if (col >= H) return;
-  float4 y = make_float4(0, 0, 0, 0);
-  const float* at = part + (size_t)t * topk * H + col;
-  for (int p = 0; p < splits; ++p) {
-#pragma unroll 8
-    for (int c = 0; c < topk; ++c) {
-      const float4 v = __ldcs(reinterpret_cast<const float4*>(at + (size_t)c * H));
-      y.x += v.x; y.y += v.y; y.z += v.z; y.w += v.w;
-    }
-    at += (size_t)slots * H;
-  }
-  *reinterpret_cast<uint2*>(Y + (size_t)t * H + col) =
-      make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
-}
 
 // ------------------------------------------------------------------- host ---
-// K parts of a product of `tiles` row tiles of an expected number of experts: the
-// rounds of units over the SMs, each as long as its share of K plus about six of the
-// 128-column steps; `join` is the further cost of a split in such steps.
-static int choose_splits(int64_t T, int64_t E, int topk, int64_t tiles, int64_t K, double join) {
+// K parts of the down product's units for an expected number of experts: the rounds of
+// units over the SMs, each as long as its share of K plus about six of the 128-column
+// steps.  A part costs a row of sums to read at the end.
+static int choose_splits(int64_t T, int64_t E, int topk, int64_t tiles, int64_t K) {
   double miss = 1.0;
   for (int64_t t = 0; t < T; ++t) miss *= 1.0 - (double)topk / (double)E;
   const double n = (double)E * (1.0 - miss);
@@ -848,9 +900,9 @@ static int choose_splits(int64_t T, int64_t E, int topk, int64_t tiles, int64_t 
   const int kq = (int)(K / kBK);
   int best = 1;
   double cost = 1e30;
-  for (int s = 1; s <= 8 && s <= kq; ++s) {
+  for (int s = 1; s <= kMaxDownParts && s <= kq; ++s) {
     const double rounds = (double)((units * s + 147) / 148);
-    const double c = rounds * ((double)kq / s + 6.0) + (s > 1 ? join : 0.0);
+    const double c = rounds * ((double)kq / s + 6.0) + 0.01 * (double)s * (double)(T * topk);
     if (c < cost - 1e-9) {
       cost = c;
       best = s;
@@ -861,7 +913,7 @@ static int choose_splits(int64_t T, int64_t E, int topk, int64_t tiles, int64_t 
 
 struct Layout {
   size_t xq, xs, experts, probs, hq, h_scales, part_up, part_down, counters, total;
-  int splits_up, splits_down, max_act, n_up;
+  int splits_down, max_act, n_counters;
 };
 static Layout layout(int64_t T, int64_t H, int64_t E, int topk, int64_t I) {
   Layout l;
@@ -873,32 +925,19 @@ static Layout layout(int64_t T, int64_t H, int64_t E, int topk, int64_t I) {
   };
   const size_t slots = (size_t)T * topk;
   l.max_act = (int)(slots < (size_t)E ? slots : (size_t)E);
-  // joining the up product's parts takes five round trips to memory at the end of a unit;
-  // the down product's parts are added where the choices are
-  l.splits_up = choose_splits(T, E, topk, 2 * I / kRows, H, 20.0);
-  l.splits_down = choose_splits(T, E, topk, H / kRows, I, 1.0);
-  l.n_up = l.splits_up > 1 ? (int)(l.max_act * (2 * I / kRows)) : 0;
+  l.splits_down = choose_splits(T, E, topk, H / kRows, I);
   l.xq = take((size_t)T * 2 * H);
   l.xs = take((size_t)T * 4);
   l.experts = take(slots * 4);
   l.probs = take(slots * 4);
   l.hq = take(slots * 2 * I);
   l.h_scales = take((size_t)l.max_act * (I / 128) * 512);
-  l.part_up = take(l.splits_up > 1 ? (size_t)l.splits_up * slots * 2 * I * 4 : 0);
+  l.part_up = take((size_t)kMaxGrid * T * kRows * 4);   // units x parts <= blocks
   l.part_down = take((size_t)l.splits_down * slots * H * 4);
-  l.counters = take((size_t)l.n_up * 4);
+  l.n_counters = l.max_act + kMaxGrid + (int)(H / kRows);
+  l.counters = take((size_t)l.n_counters * 4);
   l.total = at;
   return l;
-}
-
-// The unit walk's constants for a grid of `grid` blocks.
-static void set_units(GemmArgs* g, int grid) {
-  g->per = g->tiles * g->splits;
-  g->step_a = grid / g->per;
-  g->step_rest = grid % g->per;
-  g->by_splits = (65536 + g->splits - 1) / g->splits;
-  g->by_topk = (65536 + g->topk - 1) / g->topk;
-  g->by_per = (65536 + g->per - 1) / g->per;
 }
 
 // 4-bit rows unpacked to 16 bytes for each 16 values on the way to shared memory
@@ -947,85 +986,66 @@ cudaError_t launch_moe(const MoeArgs& a, int sm_count, cudaStream_t st) {
   using namespace moe;
   const Layout l = layout(a.T, a.H, a.E, a.topk, a.I);
   uint8_t* w = static_cast<uint8_t*>(a.workspace);
-  const int slots = a.T * a.topk;
-  float* xs = reinterpret_cast<float*>(w + l.xs);
-  int* counters = reinterpret_cast<int*>(w + l.counters);
+  ExpertArgs g;
   int32_t* experts = reinterpret_cast<int32_t*>(w + l.experts);
   float* probs = reinterpret_cast<float*>(w + l.probs);
-
-  CUtensorMap tw13, tw2, th;
-  if (!weights_map(&tw13, a.w13_codes, (uint64_t)a.E * 2 * a.I, (uint64_t)a.H) ||
-      !weights_map(&tw2, a.w2_codes, (uint64_t)a.E * a.H, (uint64_t)a.I) ||
-      !make_tmap_2d(&th, w + l.hq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)slots * 2,
-                    (uint64_t)a.I, 16, 128, CU_TENSOR_MAP_SWIZZLE_128B))
+  float* xs = reinterpret_cast<float*>(w + l.xs);
+  int* counters = reinterpret_cast<int*>(w + l.counters);
+  CUtensorMap tm13, tm2;
+  if (!weights_map(&tm13, a.w13_codes, (uint64_t)a.E * 2 * a.I, (uint64_t)a.H) ||
+      !weights_map(&tm2, a.w2_codes, (uint64_t)a.E * a.H, (uint64_t)a.I))
     return cudaErrorInvalidValue;
-  cudaError_t e = ensure_smem_limit(k_moe_gemm<true>, kMaxDynSmem);
-  if (e == cudaSuccess) e = ensure_smem_limit(k_moe_gemm<false>, kMaxDynSmem);
+  cudaError_t e = ensure_smem_limit(k_moe_experts, kMaxDynSmem);
   if (e != cudaSuccess) return e;
 
   k_moe_route<<<(a.T + kRouteTokens - 1) / kRouteTokens * kRouteCtas, 256, 0, st>>>(
       a.X, a.T, a.H, a.router, a.E, a.topk, a.renorm, experts, probs, a.experts, a.probs, w + l.xq,
-      xs, counters, l.n_up);
+      xs, counters, l.n_counters);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
 
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cfg.stream = st;
-  GemmArgs g;
   g.experts = experts;
   g.probs = probs;
-  g.E = a.E;
-  g.xq = w + l.xq;
+  g.w13_codes = a.w13_codes;
+  g.w13_scales = a.w13_scales;
+  g.w2_codes = a.w2_codes;
+  g.w2_scales = a.w2_scales;
   g.T = a.T;
+  g.E = a.E;
   g.topk = a.topk;
+  g.by_topk = (65535 + a.topk) / a.topk;
+  g.H = a.H;
+  g.I = a.I;
+  g.down_parts = l.splits_down;
   g.b_rows = (2 * a.T + 15) / 16 * 16;
   const int stage_bytes = 2 * (kWBytes + g.b_rows * kBK + 1024);
   g.stages = kRingBytes / stage_bytes < kMaxStages ? kRingBytes / stage_bytes : kMaxStages;
+  g.xq = w + l.xq;
   g.xs = xs;
   g.hq = w + l.hq;
   g.h_scales = w + l.h_scales;
-  g.I = a.I;
+  g.part_up = reinterpret_cast<float*>(w + l.part_up);
+  g.part_down = reinterpret_cast<float*>(w + l.part_down);
+  g.up_done = counters;
+  g.up_joined = counters + l.max_act;
+  g.down_done = counters + l.max_act + kMaxGrid;
+  g.Y = a.Y;
   g.status = a.status;
+
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(sm_count < kMaxGrid ? sm_count : kMaxGrid));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = 1024 + (size_t)g.stages * stage_bytes;
-
-  g.w_codes = a.w13_codes;
-  g.w_scales = a.w13_scales;
-  g.K = a.H;
-  g.tiles = 2 * a.I / kRows;
-  g.splits = l.splits_up;
-  g.part = reinterpret_cast<float*>(w + l.part_up);
-  g.counters = counters;
-  int64_t units = (int64_t)l.max_act * g.tiles * g.splits;
-  cfg.gridDim = dim3((unsigned)(units < sm_count ? units : sm_count));
-  set_units(&g, (int)cfg.gridDim.x);
-  e = cudaLaunchKernelEx(&cfg, k_moe_gemm<true>, tw13, th, g);
-  if (e != cudaSuccess) return e;
-
-  g.w_codes = a.w2_codes;
-  g.w_scales = a.w2_scales;
-  g.K = a.I;
-  g.tiles = a.H / kRows;
-  g.splits = l.splits_down;
-  g.part = reinterpret_cast<float*>(w + l.part_down);
-  units = (int64_t)l.max_act * g.tiles * g.splits;
-  cfg.gridDim = dim3((unsigned)(units < sm_count ? units : sm_count));
-  set_units(&g, (int)cfg.gridDim.x);
-  e = cudaLaunchKernelEx(&cfg, k_moe_gemm<false>, tw2, th, g);
-  if (e != cudaSuccess) return e;
-
-  cfg.gridDim = dim3((unsigned)((a.H + 511) / 512), (unsigned)a.T);
-  cfg.blockDim = dim3(128);
-  cfg.dynamicSmemBytes = 0;
-  e = cudaLaunchKernelEx(&cfg, k_moe_combine, (const float*)g.part, a.topk, g.splits, slots, a.H,
-                         a.Y);
-  if (e != cudaSuccess) return e;
-  return cudaGetLastError();
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, k_moe_experts, tm13, tm2, g);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace e8
