@@ -60,7 +60,7 @@ __device__ __forceinline__ uint32_t to_pair(float v) {
 }
 
 // ------------------------------------------------------------------ router ---
-constexpr int kRouteCtas = 8, kRouteTokens = 4;   // a cluster takes 4 tokens
+constexpr int kRouteCtas = 8;
 
 // Sums 16 values over the warp's lanes; lane l returns the sum of v[l >> 1].
 __device__ __forceinline__ double warp_sum16(double (&v)[16], int lane) {
@@ -76,12 +76,14 @@ __device__ __forceinline__ double warp_sum16(double (&v)[16], int lane) {
   return v[0] + __shfl_xor_sync(0xFFFFFFFFu, v[0], 1);
 }
 
-// One cluster of 8 CTAs for 4 tokens: each CTA takes an eighth of the experts, its
-// warps 4 experts x 4 tokens of a part of H each (16 fp64 sums a lane; converting
-// bf16 to fp64 costs four times an fp64 product, so every converted value is used
-// four times).  The logits of token j go to CTA j, which chooses; CTAs 4..7 write
-// the tokens' e4m3 rows meanwhile.  One launch and no counters: the logits cross
+// One cluster of 8 CTAs for NT tokens (4; 1 for small batches, whose time is latency):
+// each CTA takes an eighth of the experts, its warps 4 experts x NT tokens of a part of H
+// each (4 NT fp64 sums a lane; converting bf16 to fp64 costs four times an fp64 product,
+// so converted values are used several times).  A step's loads are under way while the
+// step before is computed.  The logits of token j go to CTA j, which chooses; CTAs 4..7
+// write the tokens' e4m3 rows meanwhile.  One launch and no counters: the logits cross
 // CTAs in distributed shared memory.
+template <int NT>
 __global__ void __cluster_dims__(kRouteCtas, 1, 1) __launch_bounds__(256)
     k_moe_route(const uint16_t* __restrict__ X, int T, int H, const uint16_t* __restrict__ R,
                 int E, int topk, int renorm, int32_t* __restrict__ experts,
@@ -94,56 +96,75 @@ __global__ void __cluster_dims__(kRouteCtas, 1, 1) __launch_bounds__(256)
   __shared__ int chosen[kMaxTopk];
   __shared__ uint32_t wmax[8];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rank = (int)cluster_ctarank(), t0 = (int)blockIdx.x / kRouteCtas * kRouteTokens;
-  const int nt = min(kRouteTokens, T - t0);
+  const int rank = (int)cluster_ctarank(), t0 = (int)blockIdx.x / kRouteCtas * NT;
+  const int nt = min(NT, T - t0);
   grid_dep_launch();
   cluster_arrive();   // (the wait below: every CTA of the cluster has started)
-  for (int i = blockIdx.x * 256 + tid; i < n_counters; i += gridDim.x * 256) counters[i] = 0;
-
   const int per = (E + kRouteCtas - 1) / kRouteCtas, e0 = rank * per;
   const int ne = min(per, E - e0), groups = ne > 0 ? (ne + 3) / 4 : 0;
   const int parts = groups > 0 && groups < 8 ? 8 / groups : 1, chunks = (H + 255) / 256;
   for (int item = warp; item < groups * parts; item += 8) {
     const int e = e0 + item / parts * 4, p = item % parts;
-    double acc[16] = {};
-    for (int c = chunks * p / parts; c < chunks * (p + 1) / parts; ++c) {
+    const int end = chunks * (p + 1) / parts;
+    double acc[4 * NT] = {};
+    uint4 r[4], x[NT];
+    auto load = [&](int c) {
       const int k = c * 256 + lane * 8;
-      uint4 r[4], x[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        r[j] = x[j] = make_uint4(0, 0, 0, 0);
-        if (k < H && e + j < e0 + ne)
-          r[j] = *reinterpret_cast<const uint4*>(R + (size_t)(e + j) * H + k);
-        if (k < H && j < nt)
-          x[j] = *reinterpret_cast<const uint4*>(X + (size_t)(t0 + j) * H + k);
-      }
+      for (int j = 0; j < 4; ++j)
+        r[j] = k < H && e + j < e0 + ne
+                   ? *reinterpret_cast<const uint4*>(R + (size_t)(e + j) * H + k)
+                   : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        x[j] = k < H && j < nt ? *reinterpret_cast<const uint4*>(X + (size_t)(t0 + j) * H + k)
+                               : make_uint4(0, 0, 0, 0);
+    };
+    int c = chunks * p / parts;
+    if (c < end) load(c);
+#pragma unroll 2
+    for (; c < end; ++c) {
+      uint4 rn[4], xn[NT];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) rn[j] = r[j];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) xn[j] = x[j];
+      if (c + 1 < end) load(c + 1);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         double rd[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint32_t w = i < 2 ? r[j].x : i < 4 ? r[j].y : i < 6 ? r[j].z : r[j].w;
+          const uint32_t w = i < 2 ? rn[j].x : i < 4 ? rn[j].y : i < 6 ? rn[j].z : rn[j].w;
           rd[j] = (double)((i & 1) ? bf16_hi_to_f32(w) : bf16_lo_to_f32(w));
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (j >= nt) break;
-          const uint32_t w = i < 2 ? x[j].x : i < 4 ? x[j].y : i < 6 ? x[j].z : x[j].w;
+        for (int j = 0; j < NT; ++j) {
+          const uint32_t w = i < 2 ? xn[j].x : i < 4 ? xn[j].y : i < 6 ? xn[j].z : xn[j].w;
           const double xd = (double)((i & 1) ? bf16_hi_to_f32(w) : bf16_lo_to_f32(w));
 #pragma unroll
-          for (int q = 0; q < 4; ++q) acc[q * 4 + j] = fma(rd[q], xd, acc[q * 4 + j]);
+          for (int q = 0; q < 4; ++q) acc[q * NT + j] = fma(rd[q], xd, acc[q * NT + j]);
         }
       }
     }
-    const double s = warp_sum16(acc, lane);
-    if (!(lane & 1)) part[item][lane >> 1] = s;
+    if constexpr (NT == 4) {
+      const double s = warp_sum16(acc, lane);
+      if (!(lane & 1)) part[item][lane >> 1] = s;
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        for (int o = 16; o; o >>= 1) acc[q] += __shfl_xor_sync(0xFFFFFFFFu, acc[q], o);
+        if (lane == 0) part[item][q] = acc[q];
+      }
+    }
   }
+  for (int i = blockIdx.x * 256 + tid; i < n_counters; i += gridDim.x * 256) counters[i] = 0;
   __syncthreads();
   cluster_wait();
-  if (tid < ne * kRouteTokens) {
-    const int el = tid / kRouteTokens, j = tid % kRouteTokens;
+  if (tid < ne * NT) {
+    const int el = tid / NT, j = tid % NT;
     double s = 0.0;
-    for (int p = 0; p < parts; ++p) s += part[el / 4 * parts + p][(el & 3) * 4 + j];
+    for (int p = 0; p < parts; ++p) s += part[el / 4 * parts + p][(el & 3) * NT + j];
     asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(
                      mapa_shared(smem_u32(&logit[e0 + el]), (uint32_t)j)),
                  "d"(s)
@@ -151,9 +172,9 @@ __global__ void __cluster_dims__(kRouteCtas, 1, 1) __launch_bounds__(256)
   }
   __syncwarp();
   cluster_arrive();
-  if (rank >= kRouteTokens && rank - kRouteTokens < nt) {
+  if (rank >= 4 && rank - 4 < nt) {
     // hi and lo rows of one token
-    const int t = t0 + rank - kRouteTokens;
+    const int t = t0 + rank - 4;
     const uint4* x = reinterpret_cast<const uint4*>(X + (size_t)t * H);
     uint32_t m = 0;
     for (int k = tid; k < H / 8; k += 256) {
@@ -192,7 +213,8 @@ __global__ void __cluster_dims__(kRouteCtas, 1, 1) __launch_bounds__(256)
   cluster_wait();
   if (rank >= nt) return;
   // this CTA chooses for token t0 + rank: an expert's place is the number of experts
-  // before it (larger logit, or the same and a lower number; NaN comes last)
+  // before it (larger logit, or the same and a lower number; NaN comes last); `ways`
+  // neighbouring threads share an expert's comparisons
   const int t = t0 + rank;
   for (int e = tid; e < E; e += 256) {
     const double v = logit[e] + 0.0;   // -0 becomes 0
@@ -200,12 +222,15 @@ __global__ void __cluster_dims__(kRouteCtas, 1, 1) __launch_bounds__(256)
     key[e] = v != v ? 0ull : (u >> 63 ? ~u : u | (1ull << 63));
   }
   __syncthreads();
-  for (int e = tid; e < E; e += 256) {
-    const uint64_t mine = key[e];
+  const int ways = E <= 32 ? 8 : E <= 64 ? 4 : E <= 128 ? 2 : 1;
+  for (int i = tid; i < (E * ways + 31) / 32 * 32; i += 256) {
+    const int e = i / ways, w = i & (ways - 1);
+    const uint64_t mine = e < E ? key[e] : 0ull;
     int place = 0;
-#pragma unroll 4
-    for (int j = 0; j < E; ++j) place += key[j] > mine || (key[j] == mine && j < e);
-    if (place < topk) chosen[place] = e;
+#pragma unroll 8
+    for (int j = w; j < E; j += ways) place += key[j] > mine || (key[j] == mine && j < e);
+    for (int o = 1; o < ways; o <<= 1) place += __shfl_xor_sync(0xFFFFFFFFu, place, o);
+    if (w == 0 && e < E && place < topk) chosen[place] = e;
   }
   __syncthreads();
   if (warp) return;
@@ -228,13 +253,13 @@ __global__ void __cluster_dims__(kRouteCtas, 1, 1) __launch_bounds__(256)
 }
 
 // ----------------------------------------------------------------- experts ---
-constexpr int kThreads = 224;
+constexpr int kThreads = 256;
 constexpr int kRows = 128;                 // rows of a unit
 constexpr int kBK = 128;                   // columns of a step: a tile of scales
 constexpr int kWBytes = kRows * kBK;       // 16 values in 16 bytes, 8 of them used
 constexpr int kMaxStages = 5;              // of two steps: one barrier round for 16 KB of weights
 constexpr int kConstCol = 256, kSfCol = 264;   // tensor-memory columns of the scales
-constexpr int kRingBytes = 212 * 1024;
+constexpr int kRingBytes = 212 * 1024;     // at least three stages, and one block an SM
 constexpr int kMaxGrid = 160;              // blocks
 constexpr int kMaxUpParts = 8, kMaxDownParts = 16;   // K parts of a unit
 
@@ -243,15 +268,16 @@ struct ExpertArgs {
   const float* probs;
   const uint8_t *w13_codes, *w13_scales, *w2_codes, *w2_scales;
   int T, E, topk, by_topk, H, I;   // by_topk = ceil(2^16 / topk): a slot's token without a divide
-  int down_parts, stages, b_rows;
+  int down_parts;
   const uint8_t* xq;       // the tokens' hi and lo rows
   const float* xs;         // scale of each token's pair
   uint8_t* hq;             // the slots' hi and lo rows of h, sorted by expert
   uint8_t* h_scales;       // [active expert][I / 128][512]
-  float* part_up;          // [up unit * parts + part][T][128]
+  float* part_up;          // [unit of the last up round * parts + part][T][128]
   float* part_down;        // [part][slot][H]
   int* up_done;            // [active expert]: finished tiles
-  int* up_joined;          // [up unit]: arrived parts
+  int* up_total;           // finished tiles of all
+  int* up_joined;          // [unit of the last up round]: arrived parts
   int* down_done;          // [tile]: finished units
   uint16_t* Y;
   uint32_t* status;
@@ -273,14 +299,17 @@ __device__ __forceinline__ int arrive_gpu(int* counter) {
   asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(old) : "l"(counter) : "memory");
   return old;
 }
+__device__ __forceinline__ int ld_acquire_gpu(const int* p) {
+  int v;
+  asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
 // Waits until *counter has reached `want`; bounded as mbar_wait_lazy is.
 __device__ __forceinline__ bool wait_gpu(const int* counter, int want,
                                          volatile uint32_t* abort_flag, uint32_t* status) {
   uint64_t t0 = 0;
   for (uint32_t it = 1;; ++it) {
-    int v;
-    asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(counter) : "memory");
-    if (v >= want) return true;
+    if (ld_acquire_gpu(counter) >= want) return true;
     if ((it & 31u) == 0) {
       if (ld_shared_volatile(abort_flag)) return false;
       const uint64_t t = global_timer_ns();
@@ -308,11 +337,44 @@ struct SharedLists {
   int16_t expert[kMaxExperts], off[kMaxExperts + 1], slot[kMaxSlots];
   uint8_t token[kMaxSlots];
   int nact;
-  uint32_t wsum[8];
+  uint32_t most;   // tokens of the fullest expert
+  uint32_t wsum[kThreads / 32];
 };
 static_assert(kMaxTokens == 64, "a token is a bit of an expert's mask");
 
-// Builds the lists (all threads).  mask[e]: the tokens that chose expert e, zero on
+// Builds the lists of up to 32 slots (one warp, a lane a slot).
+__device__ __forceinline__ void build_small(SharedLists& l, const int32_t* __restrict__ experts,
+                                            int slots, int by_topk) {
+  const int lane = threadIdx.x & 31;
+  const int e = lane < slots ? experts[lane] : INT32_MAX;
+  const uint32_t same = __match_any_sync(0xFFFFFFFFu, e), lower = (1u << lane) - 1u;
+  const bool head = (same & lower) == 0 && lane < slots;
+  // slots and active experts before this one's
+  int pos = __popc(same & lower), act = 0;
+#pragma unroll 1
+  for (int j = 0; j < slots; ++j) {
+    const int other = __shfl_sync(0xFFFFFFFFu, head ? e : e | (1 << 30), j);
+    pos += (other & ~(1 << 30)) < e;
+    act += other < e;
+  }
+  if (lane < slots) {
+    l.slot[pos] = (int16_t)lane;
+    l.token[pos] = (uint8_t)(lane * by_topk >> 16);
+    if (head) {
+      l.expert[act] = (int16_t)e;
+      l.off[act] = (int16_t)pos;
+    }
+  }
+  const int nact = __popc(__ballot_sync(0xFFFFFFFFu, head));
+  const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, lane < slots ? __popc(same) : 0);
+  if (lane == 0) {
+    l.off[nact] = (int16_t)slots;
+    l.nact = nact;
+    l.most = most;
+  }
+}
+
+// Builds the lists (all threads; l.most 0 on entry).  mask[e]: the tokens that chose expert e, zero on
 // entry; a token chooses an expert once, so its place is the number of lower bits.
 // chosen: the expert of each slot; first: slots before an expert's.
 __device__ __forceinline__ void build_lists(SharedLists& l, unsigned long long* mask,
@@ -332,13 +394,16 @@ __device__ __forceinline__ void build_lists(SharedLists& l, unsigned long long* 
   __syncthreads();
   // a scan over experts of (is active, slots) in one word
   constexpr int kPer = (kMaxExperts + kThreads - 1) / kThreads;
-  uint32_t mine = 0, n[kPer];
+  uint32_t mine = 0, n[kPer], most = 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int e = tid * kPer + i;
     n[i] = e < E ? (uint32_t)__popcll(mask[e]) : 0u;
     mine += n[i] ? (1u << 16) | n[i] : 0u;
+    most = max(most, n[i]);
   }
+  most = __reduce_max_sync(0xFFFFFFFFu, most);
+  if (lane == 0) atomicMax(&l.most, most);
   uint32_t scan = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -379,65 +444,102 @@ __device__ __forceinline__ void build_lists(SharedLists& l, unsigned long long* 
 }
 
 // The units of one block in turn.  All units of the layer are numbered, the up
-// products' first (row tiles of an expert, each in `up_parts` parts of K, then the next
-// expert's), the down products' after them, and dealt to the blocks in that order.
-// Walking the numbers needs quotients only once.
+// products' first (row tiles of an expert, then the next expert's), the down products'
+// after them (each tile in `down_parts` parts of K), and dealt to the blocks in that
+// order, with two exceptions that keep blocks from waiting: the up units that fill no
+// whole round of the blocks are split over K between them, and come first, so that the
+// joining of their parts is over long before the down products ask for it; and the
+// blocks that have such a part (the first `extra`) sit out as many rounds of the down
+// units as it is worth.  Walking the numbers needs quotients only once.
+struct Deal {
+  int a, rest, step_a, step_rest;      // first unit and step, in experts and units of one
+};
 struct Plan {
-  int up_parts, by_up, by_down;        // by_*: ceil(2^16 / parts)
-  int per_up, per_down;                // units of an expert
-  int up_a, up_rest, up_step_a, up_step_rest;
-  int down_a, down_rest, down_step_a, down_step_rest;
+  int rounds;                          // of whole up units
+  int tail_a, tail_tile, tail_index;   // this block's split up unit (a < 0: none)
+  int tail_part, tail_parts, by_tail;  // by_*: ceil(2^16 / parts)
+  int by_down, per_down;               // per_down: units of an expert
+  int early;                           // down units of this block before all blocks take part
+  Deal up, down_early, down;
 };
 // x / d = x * ceil(2^16 / d) >> 16 while x d < 2^16; for K steps of parts (up to 512 x
 // 16) it may be one more, but is 0 and all at the ends and rises, which is enough.
 __device__ __forceinline__ int reciprocal(int d) { return (65535 + d) / d; }
 
-// One warp; lanes 0..3 take a quotient each.
+// One warp; a lane a quotient.
 __device__ __forceinline__ void make_plan(Plan& p, const ExpertArgs& g, int nact) {
   const int lane = threadIdx.x & 31, b = (int)blockIdx.x, grid = (int)gridDim.x;
-  const int up_tiles = 2 * g.I / kRows, down_tiles = g.H / kRows;
+  const int up_tiles = 2 * g.I / kRows, per_down = g.H / kRows * g.down_parts;
   const int units = nact * up_tiles;
-  const int parts = units * 2 > grid ? 1 : min(min(kMaxUpParts, grid / units), g.H / kBK);
-  const int per_up = up_tiles * parts, per_down = down_tiles * g.down_parts;
-  const int num = lane == 0 ? b : lane == 2 ? nact * per_up : grid;
-  const int den = lane < 2 ? per_up : lane == 2 ? grid : per_down;
-  const int q = num / den, r = num - q * den;
-  const int up_left = __shfl_sync(0xFFFFFFFFu, r, 2);   // blocks of the last up round
-  const int first = b >= up_left ? b - up_left : b - up_left + grid;
-  const int first_a = first / per_down;
+  const int rounds = units / grid, rest = units - rounds * grid;
+  const int parts = rest ? min(min(kMaxUpParts, grid / rest), g.H / kBK) : 1;
+  const int extra = rest * parts, others = grid - extra, by_parts = reciprocal(parts);
+  const int index = b * by_parts >> 16, tail = rounds * grid + index;
+  // a tail unit's worth in down units
+  int num = 2 * g.H * g.down_parts + g.I * parts, den = 2 * g.I * parts;   // lane 0
+  if (lane == 1) { num = b; den = up_tiles; }
+  if (lane == 2) { num = grid; den = up_tiles; }
+  if (lane == 3) { num = tail; den = up_tiles; }
+  if (lane == 4) { num = grid; den = per_down; }
+  if (lane == 5) { num = others; den = per_down; }
+  if (lane == 6) { num = b - extra; den = per_down; }   // (unused if negative)
+  int q = num / den, r = num - q * den;
+  const int skip = rounds && extra ? __shfl_sync(0xFFFFFFFFu, q, 0) : 0;
+  if (lane == 7) {
+    num = skip * others + b + (skip || b >= extra ? 0 : grid) - (skip ? 0 : extra);
+    q = num / per_down;
+    r = num - q * per_down;
+  }
+  Deal* d = lane < 3 ? &p.up : lane == 5 || lane == 6 ? &p.down_early : &p.down;
   if (lane == 0) {
-    p.up_parts = parts;
-    p.by_up = reciprocal(parts);
-    p.per_up = per_up;
-    p.per_down = per_down;
-    p.up_a = q;
-    p.up_rest = r;
-    p.down_a = first_a;
-    p.down_rest = first - first_a * per_down;
-  } else if (lane == 1) {
-    p.up_step_a = q;
-    p.up_step_rest = r;
+    p.rounds = rounds;
+    p.tail_part = b - index * parts;
+    p.tail_parts = parts;
+    p.by_tail = by_parts;
+    p.tail_index = index;
     p.by_down = reciprocal(g.down_parts);
+    p.per_down = per_down;
+    p.early = b >= extra ? skip : 0;
   } else if (lane == 3) {
-    p.down_step_a = q;
-    p.down_step_rest = r;
+    p.tail_a = index < rest ? q : -1;
+    p.tail_tile = r;
+  } else if (lane == 1 || lane == 6 || lane == 7) {
+    d->a = q;
+    d->rest = r;
+  } else if (lane == 2 || lane == 4 || lane == 5) {
+    d->step_a = q;
+    d->step_rest = r;
   }
 }
 
 struct Unit {
-  bool down;
-  int a, rest;                       // active expert; tile * parts + part
-  int tile, part, expert, off, n;    // n tokens from slot[off] on
+  int phase;                         // 0 a split up unit, 1 whole ones, 2 down
+  int left;                          // whole up units; then early down units
+  int a, rest;                       // active expert; tile (down: * parts + part)
+  int active, tile, part, parts, expert, off, n;   // n tokens from slot[off] on
   int k0, nk;                        // steps of K
+  __device__ __forceinline__ bool down() const { return phase == 2; }
   __device__ __forceinline__ void begin(const Plan& p) {
-    down = false;
-    a = p.up_a;
-    rest = p.up_rest;
+    phase = p.tail_a >= 0 ? 0 : 1;
+    left = p.rounds;
+    a = p.up.a;
+    rest = p.up.rest;
   }
-  __device__ __forceinline__ void next(const Plan& p) {
-    a += down ? p.down_step_a : p.up_step_a;
-    rest += down ? p.down_step_rest : p.up_step_rest;
-    const int per = down ? p.per_down : p.per_up;
+  __device__ __forceinline__ void next(const Plan& p, int up_tiles) {
+    if (phase == 0) {
+      phase = 1;
+      return;
+    }
+    --left;
+    if (phase == 2 && left == 0) {
+      a = p.down.a;
+      rest = p.down.rest;
+      return;
+    }
+    const Deal& d = phase == 1 ? p.up : left > 0 ? p.down_early : p.down;
+    a += d.step_a;
+    rest += d.step_rest;
+    const int per = phase == 1 ? up_tiles : p.per_down;
     if (rest >= per) {
       rest -= per;
       ++a;
@@ -445,26 +547,41 @@ struct Unit {
   }
   // false after the last unit
   __device__ __forceinline__ bool load(const Plan& p, const ExpertArgs& g, const SharedLists& l) {
-    if (!down && a >= l.nact) {
-      down = true;
-      a = p.down_a;
-      rest = p.down_rest;
+    if (phase == 1 && left <= 0) {
+      phase = 2;
+      left = p.early;
+      a = left > 0 ? p.down_early.a : p.down.a;
+      rest = left > 0 ? p.down_early.rest : p.down.rest;
     }
-    if (a >= l.nact) return false;
-    const int parts = down ? g.down_parts : p.up_parts, by = down ? p.by_down : p.by_up;
-    const int kq = (down ? g.I : g.H) / kBK;
-    tile = rest * by >> 16;
-    part = rest - tile * parts;
-    expert = l.expert[a];
-    off = l.off[a];
-    n = l.off[a + 1] - off;
+    int by = 65536;
+    active = a;
+    tile = rest;
+    part = 0;
+    parts = 1;
+    if (phase == 0) {
+      active = p.tail_a;
+      tile = p.tail_tile;
+      part = p.tail_part;
+      parts = p.tail_parts;
+      by = p.by_tail;
+    } else if (phase == 2) {
+      if (a >= l.nact) return false;
+      parts = g.down_parts;
+      by = p.by_down;
+      tile = rest * by >> 16;
+      part = rest - tile * parts;
+    }
+    const int kq = (phase == 2 ? g.I : g.H) / kBK;
+    expert = l.expert[active];
+    off = l.off[active];
+    n = l.off[active + 1] - off;
     k0 = kq * part * by >> 16;
     nk = (kq * (part + 1) * by >> 16) - k0;
     return true;
   }
 };
 
-// Warps: 0 weights producer, 6 activations producer, 1 MMAs, 2..5 epilogue.  At 16 KB of
+// Warps: 0 weights producer, 6 and 7 activations producers, 1 MMAs, 2..5 epilogue.  At 16 KB of
 // weights a stage the SM's share of HBM leaves each role some 700 cycles a stage: one
 // elected thread runs a role's whole loop with its addresses in registers.
 __global__ void __launch_bounds__(kThreads, 1)
@@ -478,17 +595,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ int ready;
   __shared__ float token_scale[kMaxTokens];
   __shared__ SharedLists lists;
-  __shared__ Plan plan;
+  __shared__ Plan shared_plan;
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drain;
   __shared__ uint32_t tmem_slot;
   __shared__ volatile uint32_t abort_flag;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t b_bytes = (uint32_t)(g.b_rows * 128);
-  const uint32_t stage_bytes = 2u * (kWBytes + b_bytes + 1024u);
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < g.stages; ++s) {
+    lists.most = 0;
+    for (int s = 0; s < kMaxStages; ++s) {
       mbar_init(&full[s], 33);   // the weights' producer, and the lanes of the other
       mbar_init(&empty[s], 1);
     }
@@ -522,9 +638,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dep_wait();
   const int slots = g.T * g.topk;
   if (threadIdx.x < g.T) token_scale[threadIdx.x] = g.xs[threadIdx.x];
-  build_lists(lists, mask, chosen, chosen + kMaxSlots, g.experts, slots, g.E, g.by_topk);
-  if (warp == 0) make_plan(plan, g, lists.nact);
+  if (slots > 32)
+    build_lists(lists, mask, chosen, chosen + kMaxSlots, g.experts, slots, g.E, g.by_topk);
+  else if (warp == 0)
+    build_small(lists, g.experts, slots, g.by_topk);
+  __syncwarp();
+  if (warp == 0) make_plan(shared_plan, g, lists.nact);
   __syncthreads();
+  const Plan plan = shared_plan;
+  // a stage holds two steps: weights, the rows of the fullest expert's tokens, scales
+  const uint32_t b_bytes = (2u * lists.most + 15u) / 16u * 16u * 128u;
+  const uint32_t stage_bytes = 2u * (kWBytes + b_bytes + 1024u);
+  const int stages = min(kMaxStages, (int)((uint32_t)kRingBytes / stage_bytes));
   const uint32_t ring = smem_u32(smem);
   const int up_tiles = 2 * g.I / kRows, down_tiles = g.H / kRows;
 
@@ -533,13 +658,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t st = ring, ph = 1;
       int s = 0;
       bool ok = true;
-      Unit u;
-      for (u.begin(plan); ok && u.load(plan, g, lists); u.next(plan)) {
-        const int kqs = (u.down ? g.I : g.H) / kBK;
-        const int row = (u.expert * (u.down ? down_tiles : up_tiles) + u.tile) * kRows;
+      Unit u, v;
+      u.begin(plan);
+      for (bool more = u.load(plan, g, lists); ok && more; u = v) {
+        v = u;
+        v.next(plan, up_tiles);
+        more = v.load(plan, g, lists);
+        const int kqs = (u.down() ? g.I : g.H) / kBK;
+        const int row = (u.expert * (u.down() ? down_tiles : up_tiles) + u.tile) * kRows;
         const uint8_t* sf =
-            (u.down ? g.w2_scales : g.w13_scales) + ((int64_t)(row >> 7) * kqs + u.k0) * 512;
-        const CUtensorMap* map = u.down ? &tm2 : &tm13;
+            (u.down() ? g.w2_scales : g.w13_scales) + ((int64_t)(row >> 7) * kqs + u.k0) * 512;
+        const CUtensorMap* map = u.down() ? &tm2 : &tm13;
         int x = u.k0 * kBK;
         bool ahead = true;
         for (int k = u.nk; k > 0; k -= 2) {
@@ -554,14 +683,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (ahead) {
             // the next unit lies in other pages: a first access there costs microseconds
             // (address translation) and the ring holds less than two
-            Unit v = u;
-            v.next(plan);
-            if (v.load(plan, g, lists)) {
-              const int cols = v.down ? g.I : g.H;
-              const int64_t tile = (int64_t)v.expert * (v.down ? down_tiles : up_tiles) + v.tile;
-              prefetch_l2((v.down ? g.w2_codes : g.w13_codes) + tile * kRows * (cols / 2) +
+            if (more) {
+              const int cols = v.down() ? g.I : g.H;
+              const int64_t tile = (int64_t)v.expert * (v.down() ? down_tiles : up_tiles) + v.tile;
+              prefetch_l2((v.down() ? g.w2_codes : g.w13_codes) + tile * kRows * (cols / 2) +
                           v.k0 * 64);
-              prefetch_l2((v.down ? g.w2_scales : g.w13_scales) +
+              prefetch_l2((v.down() ? g.w2_scales : g.w13_scales) +
                           (tile * (cols / kBK) + v.k0) * 512);
             }
             ahead = false;
@@ -569,7 +696,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           x += 2 * kBK;
           sf += 1024;
           st += stage_bytes;
-          if (++s == g.stages) {
+          if (++s == stages) {
             s = 0;
             ph ^= 1u;
             st = ring;
@@ -577,52 +704,60 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-  } else if (warp == 6) {
-    // 16 lanes copy the 256 bytes of each of a token's two rows, 16 bytes a lane, to
+  } else if (warp >= 6) {
+    // The two warps take turns, a stage each.  16 lanes copy the 256 bytes of each of a token's two rows, 16 bytes a lane, to
     // where the 128-byte swizzle has them
     const int r = lane >> 4, c = lane & 15;
     const uint32_t to = (c >> 3) * b_bytes + (uint32_t)r * 128u;
     uint32_t st = ring + 2u * kWBytes, ph = 1;
-    int s = 0;
-    bool ok = true;
+    int s = 0, turn = warp & 1;
+    bool ok = true, all_up = false;
     Unit u;
-    for (u.begin(plan); ok && u.load(plan, g, lists); u.next(plan)) {
-      const int cols = u.down ? g.I : g.H;
-      const uint8_t* src = (u.down ? g.hq + (size_t)u.off * 2 * g.I : g.xq) + (size_t)r * cols + c * 16;
-      const int row0 = (u.down ? lane : lane < u.n ? lists.token[u.off + lane] : 0) * 2 * cols;
+    for (u.begin(plan); ok && u.load(plan, g, lists); u.next(plan, up_tiles)) {
+      const int cols = u.down() ? g.I : g.H;
+      const uint8_t* src = (u.down() ? g.hq + (size_t)u.off * 2 * g.I : g.xq) + (size_t)r * cols + c * 16;
+      const int row0 = (u.down() ? lane : lane < u.n ? lists.token[u.off + lane] : 0) * 2 * cols;
       const int row1 =
-          (u.down ? lane + 32 : lane + 32 < u.n ? lists.token[u.off + lane + 32] : 0) * 2 * cols;
-      const uint8_t* sf = g.h_scales + ((int64_t)u.a * (g.I / kBK) + u.k0) * 512 + lane * 16;
-      if (u.down) {
-        // every tile of the expert's h
-        ok = lane != 0 || wait_gpu(&g.up_done[u.a], up_tiles, &abort_flag, g.status);
-        __syncwarp();
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
+          (u.down() ? lane + 32 : lane + 32 < u.n ? lists.token[u.off + lane + 32] : 0) * 2 * cols;
+      const uint8_t* sf = g.h_scales + ((int64_t)u.active * (g.I / kBK) + u.k0) * 512 + lane * 16;
+      if (u.down()) {
+        // every tile of the expert's h; once all experts' are there nothing is asked again
+        if (!all_up) {
+          if (lane == 0) {
+            all_up = ld_acquire_gpu(g.up_total) == lists.nact * up_tiles;
+            ok = all_up || wait_gpu(&g.up_done[u.active], up_tiles, &abort_flag, g.status);
+          }
+          __syncwarp();
+          all_up = __shfl_sync(0xFFFFFFFFu, (int)all_up, 0) != 0;
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
+        }
       }
       int x = u.k0 * kBK;
-      for (int k = u.nk; k > 0; k -= 2) {
-        ok = __all_sync(0xFFFFFFFFu,
-                        mbar_wait_lazy(&empty[s], ph, &abort_flag, g.status, kDevTimeoutEmpty));
-        if (!ok) break;
-        uint32_t dst = st + to;
+      for (int k = u.nk; k > 0; k -= 2, turn ^= 1) {
+        if (turn == 0) {
+          ok = __all_sync(0xFFFFFFFFu,
+                          mbar_wait_lazy(&empty[s], ph, &abort_flag, g.status, kDevTimeoutEmpty));
+          if (!ok) break;
+          uint32_t dst = st + to;
 #pragma unroll 4
-        for (int j = 0; j < u.n; ++j) {
-          const int row = __shfl_sync(0xFFFFFFFFu, j < 32 ? row0 : row1, j & 31);
-          if (k > 1 || c < 8)
-            copy_async16(dst + (uint32_t)(((c & 7) ^ ((2 * j + r) & 7)) << 4), src + row + x);
-          dst += 256u;
+          for (int j = 0; j < u.n; ++j) {
+            const int row = __shfl_sync(0xFFFFFFFFu, j < 32 ? row0 : row1, j & 31);
+            if (k > 1 || c < 8)
+              copy_async16(dst + (uint32_t)(((c & 7) ^ ((2 * j + r) & 7)) << 4), src + row + x);
+            dst += 256u;
+          }
+          if (u.down()) {
+            const uint32_t f = st + 2u * b_bytes + 1024u + (uint32_t)lane * 16u;
+            copy_async16(f, sf);
+            if (k > 1) copy_async16(f + 512u, sf + 512);
+          }
+          copy_async_arrive(&full[s]);
         }
-        if (u.down) {
-          const uint32_t f = st + 2u * b_bytes + 1024u + (uint32_t)lane * 16u;
-          copy_async16(f, sf);
-          if (k > 1) copy_async16(f + 512u, sf + 512);
-        }
-        copy_async_arrive(&full[s]);
         x += 2 * kBK;
         sf += 1024;
         st += stage_bytes;
-        if (++s == g.stages) {
+        if (++s == stages) {
           s = 0;
           ph ^= 1u;
           st = ring + 2u * kWBytes;
@@ -637,7 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       mx4::copy_scales(tmem + kConstCol, mx4::scale_desc_lo(smem_u32(const_sf)));
       Unit u;
-      for (u.begin(plan); ok && u.load(plan, g, lists); u.next(plan), ++local) {
+      for (u.begin(plan); ok && u.load(plan, g, lists); u.next(plan, up_tiles), ++local) {
         const int buf = local & 1;
         if (!mbar_wait_lazy(&acc_empty[buf], ((uint32_t)(local >> 1) & 1u) ^ 1u, &abort_flag,
                             g.status, kDevTimeoutMma))
@@ -653,12 +788,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t w = mx4::code_desc_lo(st << 4), b = w + b_off;
           const uint32_t w1 = w + (kWBytes >> 4), b1 = b + (b_bytes >> 4);
           const uint32_t f = mx4::scale_desc_lo((st + f_off) << 4);
-          const uint32_t sfb = u.down ? cols + 8u : tmem + kConstCol, sfb1 = u.down ? sfb + 4u : sfb;
+          const uint32_t sfb = u.down() ? cols + 8u : tmem + kConstCol, sfb1 = u.down() ? sfb + 4u : sfb;
           mx4::copy_scales(cols, f);
-          if (u.down) mx4::copy_scales(sfb, f + 64u);
+          if (u.down()) mx4::copy_scales(sfb, f + 64u);
           if (k > 1) {
             mx4::copy_scales(cols + 4u, f + 32u);
-            if (u.down) mx4::copy_scales(sfb1, f + 96u);
+            if (u.down()) mx4::copy_scales(sfb1, f + 96u);
           }
 #pragma unroll
           for (uint32_t j = 0; j < 4; ++j)
@@ -674,7 +809,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_commit(&empty[s]);
           st += stage_bytes >> 4;
           cols += 16u;
-          if (++s == g.stages) {
+          if (++s == stages) {
             s = 0;
             ph ^= 1u;
             st = ring >> 4;
@@ -702,8 +837,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t d = tmem + ((uint32_t)(quarter * 32) << 16);
       int n = 0;
       if (pass < 2) {
-        u.a = u.off = u.tile = u.part = 0;
-        u.down = pass == 1;
+        u.active = u.off = u.tile = u.part = 0;
+        u.parts = 1;
+        u.phase = pass + 1;
       } else {
         if (pass == 2) u.begin(plan);
         if (!u.load(plan, g, lists)) {
@@ -719,7 +855,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         d += (uint32_t)buf * 128u;
         n = u.n;
       }
-      const int parts = live && !u.down ? plan.up_parts : 1;
+      const int parts = u.parts;
       // eight tokens' values of this row (hi + lo)
       auto read8 = [&](int j0, float (&v)[8]) {
         uint32_t r[16];
@@ -734,9 +870,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (live && lane == 0) mbar_arrive(&acc_empty[local & 1]);
       };
-      if (!u.down) {
-        const int unit = u.a * up_tiles + u.tile;
-        float* part = g.part_up + (size_t)unit * parts * g.T * kRows;
+      if (!u.down()) {
+        float* part = g.part_up + (size_t)plan.tail_index * parts * g.T * kRows;
         bool last = true;
         if (parts > 1) {
 #pragma unroll 1
@@ -748,7 +883,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (j0 + j < n) part[((size_t)u.part * g.T + j0 + j) * kRows + row] = v[j];
           }
           bar_sync(1, 128);
-          if (et == 0) ready = arrive_gpu(&g.up_joined[unit]) == parts - 1;
+          if (et == 0) ready = arrive_gpu(&g.up_joined[plan.tail_index]) == parts - 1;
           bar_sync(1, 128);
           last = ready != 0;
         }
@@ -813,14 +948,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int r = 2 * j + q, at = u.tile * 64;
                 const uint32_t by = q && byte != 255u ? byte - 4u : byte;
                 *reinterpret_cast<uint16_t*>(
-                    g.h_scales + ((int64_t)u.a * (g.I / 128) + at / 128) * 512 + (r & 31) * 16 +
+                    g.h_scales + ((int64_t)u.active * (g.I / 128) + at / 128) * 512 + (r & 31) * 16 +
                     (r >> 5) * 4 + (at & 127) / 32) = (uint16_t)(by | by << 8);
               }
             }
             bar_sync(1, 128);   // stage_v is free again; h is written
             j0 += 8;
           } while (j0 < n);
-          if (live && et == 0) signal_gpu(&g.up_done[u.a]);
+          if (live && et == 0) {
+            signal_gpu(&g.up_done[u.active]);
+            signal_gpu(g.up_total);
+          }
         }
         release();
       } else {
@@ -843,7 +981,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (live && et == 0) signal_gpu(&g.down_done[u.tile]);
       }
       if (live) {
-        u.next(plan);
+        u.next(plan, up_tiles);
         ++local;
       }
     }
@@ -889,26 +1027,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------------- host ---
-// K parts of the down product's units for an expected number of experts: the rounds of
-// units over the SMs, each as long as its share of K plus about six of the 128-column
-// steps.  A part costs a row of sums to read at the end.
+// K parts of the down product's units: eight stages a unit, so that a block that waits
+// for one expert's h has other units to do, and that the last round is short; more when
+// even so the units are fewer than the SMs.
 static int choose_splits(int64_t T, int64_t E, int topk, int64_t tiles, int64_t K) {
-  double miss = 1.0;
-  for (int64_t t = 0; t < T; ++t) miss *= 1.0 - (double)topk / (double)E;
-  const double n = (double)E * (1.0 - miss);
-  const int64_t units = (int64_t)(n + 0.5 < 1.0 ? 1.0 : n + 0.5) * tiles;
   const int kq = (int)(K / kBK);
-  int best = 1;
-  double cost = 1e30;
-  for (int s = 1; s <= kMaxDownParts && s <= kq; ++s) {
-    const double rounds = (double)((units * s + 147) / 148);
-    const double c = rounds * ((double)kq / s + 6.0) + 0.01 * (double)s * (double)(T * topk);
-    if (c < cost - 1e-9) {
-      cost = c;
-      best = s;
-    }
-  }
-  return best;
+  const int64_t slots = T * topk, units = (slots < E ? slots : E) * tiles;
+  int64_t s = (kq + 15) / 16, few = 148 / units;
+  if (s < few) s = few < kq / 2 ? few : kq / 2;
+  if (s > kMaxDownParts) s = kMaxDownParts;
+  return s < 1 ? 1 : (int)s;
 }
 
 struct Layout {
@@ -934,7 +1062,7 @@ static Layout layout(int64_t T, int64_t H, int64_t E, int topk, int64_t I) {
   l.h_scales = take((size_t)l.max_act * (I / 128) * 512);
   l.part_up = take((size_t)kMaxGrid * T * kRows * 4);   // units x parts <= blocks
   l.part_down = take((size_t)l.splits_down * slots * H * 4);
-  l.n_counters = l.max_act + kMaxGrid + (int)(H / kRows);
+  l.n_counters = 1 + l.max_act + kMaxGrid + (int)(H / kRows);
   l.counters = take((size_t)l.n_counters * 4);
   l.total = at;
   return l;
@@ -998,9 +1126,15 @@ cudaError_t launch_moe(const MoeArgs& a, int sm_count, cudaStream_t st) {
   cudaError_t e = ensure_smem_limit(k_moe_experts, kMaxDynSmem);
   if (e != cudaSuccess) return e;
 
-  k_moe_route<<<(a.T + kRouteTokens - 1) / kRouteTokens * kRouteCtas, 256, 0, st>>>(
-      a.X, a.T, a.H, a.router, a.E, a.topk, a.renorm, experts, probs, a.experts, a.probs, w + l.xq,
-      xs, counters, l.n_counters);
+  // one token a cluster while all clusters are resident at once (8 CTAs each)
+  if (a.T * kRouteCtas <= sm_count)
+    k_moe_route<1><<<a.T * kRouteCtas, 256, 0, st>>>(
+        a.X, a.T, a.H, a.router, a.E, a.topk, a.renorm, experts, probs, a.experts, a.probs,
+        w + l.xq, xs, counters, l.n_counters);
+  else
+    k_moe_route<4><<<(a.T + 3) / 4 * kRouteCtas, 256, 0, st>>>(
+        a.X, a.T, a.H, a.router, a.E, a.topk, a.renorm, experts, probs, a.experts, a.probs,
+        w + l.xq, xs, counters, l.n_counters);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
 
@@ -1017,25 +1151,23 @@ cudaError_t launch_moe(const MoeArgs& a, int sm_count, cudaStream_t st) {
   g.H = a.H;
   g.I = a.I;
   g.down_parts = l.splits_down;
-  g.b_rows = (2 * a.T + 15) / 16 * 16;
-  const int stage_bytes = 2 * (kWBytes + g.b_rows * kBK + 1024);
-  g.stages = kRingBytes / stage_bytes < kMaxStages ? kRingBytes / stage_bytes : kMaxStages;
   g.xq = w + l.xq;
   g.xs = xs;
   g.hq = w + l.hq;
   g.h_scales = w + l.h_scales;
   g.part_up = reinterpret_cast<float*>(w + l.part_up);
   g.part_down = reinterpret_cast<float*>(w + l.part_down);
-  g.up_done = counters;
-  g.up_joined = counters + l.max_act;
-  g.down_done = counters + l.max_act + kMaxGrid;
+  g.up_total = counters;
+  g.up_done = counters + 1;
+  g.up_joined = g.up_done + l.max_act;
+  g.down_done = g.up_joined + kMaxGrid;
   g.Y = a.Y;
   g.status = a.status;
 
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(sm_count < kMaxGrid ? sm_count : kMaxGrid));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = 1024 + (size_t)g.stages * stage_bytes;
+  cfg.dynamicSmemBytes = 1024 + kRingBytes;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeCooperative;
