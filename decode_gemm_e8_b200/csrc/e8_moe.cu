@@ -4,12 +4,14 @@
 //
 //   k_moe_route   router logits (products exact in fp32 and summed in fp64), top-k and
 //                 probabilities, and the activations as two e4m3 rows a token
-//   k_moe_experts everything else, one block an SM, launched cooperatively because its
-//                 blocks wait for one another's results: first the up products' units,
-//                 then the down products', then the weighted sums.  The ring of weight
-//                 tiles runs through all of it, so HBM is busy while a block waits for
-//                 the activations of its next product (as three kernels, the starts and
-//                 ends of each cost 15 us together).
+//   k_moe_experts everything else, one block an SM: the up products' units, the down
+//                 products', the weighted sums, claimed in this order from one counter
+//                 by the blocks as they go.  A block waits only for units with lower
+//                 numbers, which running blocks have claimed, so the launch needs no
+//                 co-residence and no end of a phase leaves blocks idle; the ring of
+//                 weight tiles runs through all of it, so HBM is busy while a block
+//                 waits for the activations of its next product (as three kernels, the
+//                 starts and ends of each cost 15 us together).
 //     The tensor cores take the 4-bit weights as they are (tcgen05.mma.kind::mxf8f6f4,
 //     e2m1 x e4m3): 128 rows of an expert's matrix on the M side, its tokens on the N
 //     side.  The activations enter as hi + lo, hi = e4m3(x / s), lo = e4m3(16 (x / s -
@@ -24,7 +26,7 @@
 //     sums        a token's slots are added in the order of its choices
 // Few up units are split over K, their partial sums added in order by the unit that
 // arrives last; the down units' parts are added with the slots.  No result depends on
-// timing.
+// timing or on which block claimed what.
 #include "e8_internal.h"
 #include "e8_mx4.cuh"
 #include "e8_tmap.h"
@@ -253,7 +255,8 @@ __global__ void __cluster_dims__(kRouteCtas, 1, 1) __launch_bounds__(256)
 }
 
 // ----------------------------------------------------------------- experts ---
-constexpr int kThreads = 256;
+constexpr int kThreads = 320;
+constexpr int kSlots = 4;                  // claimed units a block has in hand
 constexpr int kRows = 128;                 // rows of a unit
 constexpr int kBK = 128;                   // columns of a step: a tile of scales
 constexpr int kWBytes = kRows * kBK;       // 16 values in 16 bytes, 8 of them used
@@ -273,11 +276,12 @@ struct ExpertArgs {
   const float* xs;         // scale of each token's pair
   uint8_t* hq;             // the slots' hi and lo rows of h, sorted by expert
   uint8_t* h_scales;       // [active expert][I / 128][512]
-  float* part_up;          // [unit of the last up round * parts + part][T][128]
+  float* part_up;          // [up unit * parts + part][T][128], where units are split
   float* part_down;        // [part][slot][H]
-  int* up_done;            // [active expert]: finished tiles
-  int* up_total;           // finished tiles of all
-  int* up_joined;          // [unit of the last up round]: arrived parts
+  int* claimed;            // units so far
+  int* up_done;            // [active expert]: finished up units
+  int* up_total;           // finished up units of all
+  int* up_joined;          // [up unit]: arrived parts
   int* down_done;          // [tile]: finished units
   uint16_t* Y;
   uint32_t* status;
@@ -443,145 +447,21 @@ __device__ __forceinline__ void build_lists(SharedLists& l, unsigned long long* 
   __syncthreads();
 }
 
-// The units of one block in turn.  All units of the layer are numbered, the up
-// products' first (row tiles of an expert, then the next expert's), the down products'
-// after them (each tile in `down_parts` parts of K), and dealt to the blocks in that
-// order, with two exceptions that keep blocks from waiting: the up units that fill no
-// whole round of the blocks are split over K between them, and come first, so that the
-// joining of their parts is over long before the down products ask for it; and the
-// blocks that have such a part (the first `extra`) sit out as many rounds of the down
-// units as it is worth.  Walking the numbers needs quotients only once.
-struct Deal {
-  int a, rest, step_a, step_rest;      // first unit and step, in experts and units of one
-};
-struct Plan {
-  int rounds;                          // of whole up units
-  int tail_a, tail_tile, tail_index;   // this block's split up unit (a < 0: none)
-  int tail_part, tail_parts, by_tail;  // by_*: ceil(2^16 / parts)
-  int by_down, per_down;               // per_down: units of an expert
-  int early;                           // down units of this block before all blocks take part
-  Deal up, down_early, down;
-};
-// x / d = x * ceil(2^16 / d) >> 16 while x d < 2^16; for K steps of parts (up to 512 x
-// 16) it may be one more, but is 0 and all at the ends and rises, which is enough.
-__device__ __forceinline__ int reciprocal(int d) { return (65535 + d) / d; }
-
-// One warp; a lane a quotient.
-__device__ __forceinline__ void make_plan(Plan& p, const ExpertArgs& g, int nact) {
-  const int lane = threadIdx.x & 31, b = (int)blockIdx.x, grid = (int)gridDim.x;
-  const int up_tiles = 2 * g.I / kRows, per_down = g.H / kRows * g.down_parts;
-  const int units = nact * up_tiles;
-  const int rounds = units / grid, rest = units - rounds * grid;
-  const int parts = rest ? min(min(kMaxUpParts, grid / rest), g.H / kBK) : 1;
-  const int extra = rest * parts, others = grid - extra, by_parts = reciprocal(parts);
-  const int index = b * by_parts >> 16, tail = rounds * grid + index;
-  // a tail unit's worth in down units
-  int num = 2 * g.H * g.down_parts + g.I * parts, den = 2 * g.I * parts;   // lane 0
-  if (lane == 1) { num = b; den = up_tiles; }
-  if (lane == 2) { num = grid; den = up_tiles; }
-  if (lane == 3) { num = tail; den = up_tiles; }
-  if (lane == 4) { num = grid; den = per_down; }
-  if (lane == 5) { num = others; den = per_down; }
-  if (lane == 6) { num = b - extra; den = per_down; }   // (unused if negative)
-  int q = num / den, r = num - q * den;
-  const int skip = rounds && extra ? __shfl_sync(0xFFFFFFFFu, q, 0) : 0;
-  if (lane == 7) {
-    num = skip * others + b + (skip || b >= extra ? 0 : grid) - (skip ? 0 : extra);
-    q = num / per_down;
-    r = num - q * per_down;
-  }
-  Deal* d = lane < 3 ? &p.up : lane == 5 || lane == 6 ? &p.down_early : &p.down;
-  if (lane == 0) {
-    p.rounds = rounds;
-    p.tail_part = b - index * parts;
-    p.tail_parts = parts;
-    p.by_tail = by_parts;
-    p.tail_index = index;
-    p.by_down = reciprocal(g.down_parts);
-    p.per_down = per_down;
-    p.early = b >= extra ? skip : 0;
-  } else if (lane == 3) {
-    p.tail_a = index < rest ? q : -1;
-    p.tail_tile = r;
-  } else if (lane == 1 || lane == 6 || lane == 7) {
-    d->a = q;
-    d->rest = r;
-  } else if (lane == 2 || lane == 4 || lane == 5) {
-    d->step_a = q;
-    d->step_rest = r;
-  }
-}
-
+// A unit as the scheduler warp writes it down for the others.  The numbers run over the
+// up products (row tiles of an expert, each in parts of K, then the next expert's), the
+// down products in the same way, and the sums (128 columns of four tokens).
+enum : int { kUp = 0, kDown = 1, kSum = 2, kEnd = 3 };
 struct Unit {
-  int phase;                         // 0 a split up unit, 1 whole ones, 2 down
-  int left;                          // whole up units; then early down units
-  int a, rest;                       // active expert; tile (down: * parts + part)
-  int active, tile, part, parts, expert, off, n;   // n tokens from slot[off] on
-  int k0, nk;                        // steps of K
-  __device__ __forceinline__ bool down() const { return phase == 2; }
-  __device__ __forceinline__ void begin(const Plan& p) {
-    phase = p.tail_a >= 0 ? 0 : 1;
-    left = p.rounds;
-    a = p.up.a;
-    rest = p.up.rest;
-  }
-  __device__ __forceinline__ void next(const Plan& p, int up_tiles) {
-    if (phase == 0) {
-      phase = 1;
-      return;
-    }
-    --left;
-    if (phase == 2 && left == 0) {
-      a = p.down.a;
-      rest = p.down.rest;
-      return;
-    }
-    const Deal& d = phase == 1 ? p.up : left > 0 ? p.down_early : p.down;
-    a += d.step_a;
-    rest += d.step_rest;
-    const int per = phase == 1 ? up_tiles : p.per_down;
-    if (rest >= per) {
-      rest -= per;
-      ++a;
-    }
-  }
-  // false after the last unit
-  __device__ __forceinline__ bool load(const Plan& p, const ExpertArgs& g, const SharedLists& l) {
-    if (phase == 1 && left <= 0) {
-      phase = 2;
-      left = p.early;
-      a = left > 0 ? p.down_early.a : p.down.a;
-      rest = left > 0 ? p.down_early.rest : p.down.rest;
-    }
-    int by = 65536;
-    active = a;
-    tile = rest;
-    part = 0;
-    parts = 1;
-    if (phase == 0) {
-      active = p.tail_a;
-      tile = p.tail_tile;
-      part = p.tail_part;
-      parts = p.tail_parts;
-      by = p.by_tail;
-    } else if (phase == 2) {
-      if (a >= l.nact) return false;
-      parts = g.down_parts;
-      by = p.by_down;
-      tile = rest * by >> 16;
-      part = rest - tile * parts;
-    }
-    const int kq = (phase == 2 ? g.I : g.H) / kBK;
-    expert = l.expert[active];
-    off = l.off[active];
-    n = l.off[active + 1] - off;
-    k0 = kq * part * by >> 16;
-    nk = (kq * (part + 1) * by >> 16) - k0;
-    return true;
-  }
+  int kind;
+  int active, tile, part, parts;   // active expert; row tile; part of K
+  int expert, off, n;              // n tokens from slot[off] on
+  int k0, nk;                      // 128-column steps of K
+  int up_units;                    // of each expert, parts counted
 };
 
-// Warps: 0 weights producer, 6 and 7 activations producers, 1 MMAs, 2..5 epilogue.  At 16 KB of
+// Warps: 0 weights producer, 6 and 7 activations producers, 1 MMAs, 2..5 epilogue, 8
+// scheduler, 9 tells other blocks of finished units (a release to the whole GPU takes a
+// microsecond or two under load, which the epilogue does not wait for).  At 16 KB of
 // weights a stage the SM's share of HBM leaves each role some 700 cycles a stage: one
 // elected thread runs a role's whole loop with its addresses in registers.
 __global__ void __launch_bounds__(kThreads, 1)
@@ -595,7 +475,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ int ready;
   __shared__ float token_scale[kMaxTokens];
   __shared__ SharedLists lists;
-  __shared__ Plan shared_plan;
+  __shared__ Unit units[kSlots];
+  __shared__ uint64_t unit_full[kSlots], unit_empty[kSlots], told_full[2], told_empty[2];
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drain;
   __shared__ uint32_t tmem_slot;
   __shared__ volatile uint32_t abort_flag;
@@ -611,6 +492,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
       mbar_init(&acc_empty[b], 4);
+    }
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&unit_full[i], 1);
+      mbar_init(&unit_empty[i], 9);   // three threads and six warps read it
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&told_full[i], 4);
+      mbar_init(&told_empty[i], 1);
     }
     mbar_init(&drain, 1);
     abort_flag = 0u;
@@ -637,15 +526,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = tmem_slot;
   grid_dep_wait();
   const int slots = g.T * g.topk;
+  int claim = 0;
+  if (threadIdx.x == 256) claim = atomicAdd(g.claimed, 1);
   if (threadIdx.x < g.T) token_scale[threadIdx.x] = g.xs[threadIdx.x];
   if (slots > 32)
     build_lists(lists, mask, chosen, chosen + kMaxSlots, g.experts, slots, g.E, g.by_topk);
   else if (warp == 0)
     build_small(lists, g.experts, slots, g.by_topk);
-  __syncwarp();
-  if (warp == 0) make_plan(shared_plan, g, lists.nact);
   __syncthreads();
-  const Plan plan = shared_plan;
   // a stage holds two steps: weights, the rows of the fullest expert's tokens, scales
   const uint32_t b_bytes = (2u * lists.most + 15u) / 16u * 16u * 128u;
   const uint32_t stage_bytes = 2u * (kWBytes + b_bytes + 1024u);
@@ -653,24 +541,120 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t ring = smem_u32(smem);
   const int up_tiles = 2 * g.I / kRows, down_tiles = g.H / kRows;
 
-  if (warp == 0) {
+  // The next unit of a role that is one thread, and of one that is a warp; false when the
+  // block gives up.  Every role takes all units.
+  int slot_at = 0;
+  uint32_t slot_ph = 0;
+  auto look = [&](Unit& u) {
+    const bool ok = mbar_wait_lazy(&unit_full[slot_at], slot_ph, &abort_flag, g.status,
+                                   kDevTimeoutFull);
+    u = units[slot_at];
+    return ok;
+  };
+  auto taken = [&]() {
+    mbar_arrive(&unit_empty[slot_at]);
+  };
+  auto advance = [&]() {
+    if (++slot_at == kSlots) {
+      slot_at = 0;
+      slot_ph ^= 1u;
+    }
+  };
+  auto take = [&](Unit& u) {
+    const bool ok = look(u);
+    if (ok) taken();
+    advance();
+    return ok && u.kind != kEnd;
+  };
+  auto take_warp = [&](Unit& u) {
+    const bool ok = __all_sync(0xFFFFFFFFu, look(u));
+    __syncwarp();
+    if (ok && lane == 0) taken();
+    advance();
+    return ok && u.kind != kEnd;
+  };
+
+  if (warp == 9) {
+    if (lane == 0) {
+      Unit u;
+      int i = 0;
+      while (take(u)) {
+        if (u.kind == kSum) continue;
+        if (!mbar_wait_lazy(&told_full[i & 1], (uint32_t)(i >> 1) & 1u, &abort_flag, g.status,
+                            kDevTimeoutMma))
+          break;
+        // the four epilogue warps' writes came before; a part of a unit counts as one of it
+        if (u.kind == kDown) {
+          signal_gpu(&g.down_done[u.tile]);
+        } else {
+          signal_gpu(&g.up_done[u.active]);
+          signal_gpu(g.up_total);
+        }
+        mbar_arrive(&told_empty[i & 1]);
+        ++i;
+      }
+    }
+  } else if (warp == 8) {
+    if (lane == 0) {
+      const int nact = lists.nact, ups = nact * up_tiles, grid = (int)gridDim.x;
+      const int up_parts = ups * 2 > grid ? 1 : min(min(kMaxUpParts, grid / ups), g.H / kBK);
+      const int per_up = up_tiles * up_parts, per_down = down_tiles * g.down_parts;
+      const int n_up = nact * per_up, n_down = n_up + nact * per_down;
+      const int n_all = n_down + down_tiles * ((g.T + 3) / 4);
+      int s = 0;
+      uint32_t ph = 1;
+      for (;;) {
+        Unit u = {};
+        u.up_units = per_up;
+        u.kind = claim < n_up ? kUp : claim < n_down ? kDown : claim < n_all ? kSum : kEnd;
+        if (u.kind < kSum) {
+          const bool down = u.kind == kDown;
+          const int i = down ? claim - n_up : claim, per = down ? per_down : per_up;
+          u.parts = down ? g.down_parts : up_parts;
+          u.active = i / per;
+          const int rest = i - u.active * per, kq = (down ? g.I : g.H) / kBK;
+          u.tile = rest / u.parts;
+          u.part = rest - u.tile * u.parts;
+          u.expert = lists.expert[u.active];
+          u.off = lists.off[u.active];
+          u.n = lists.off[u.active + 1] - u.off;
+          u.k0 = kq * u.part / u.parts;
+          u.nk = kq * (u.part + 1) / u.parts - u.k0;
+          // a first access to other pages costs microseconds (address translation), and
+          // the ring holds less than two
+          const int64_t tile = (int64_t)u.expert * (down ? down_tiles : up_tiles) + u.tile;
+          prefetch_l2((down ? g.w2_codes : g.w13_codes) + tile * kRows * (kq * 64) + u.k0 * 64);
+          prefetch_l2((down ? g.w2_scales : g.w13_scales) + (tile * kq + u.k0) * 512);
+        } else if (u.kind == kSum) {
+          u.active = (claim - n_down) / down_tiles;   // four tokens
+          u.tile = claim - n_down - u.active * down_tiles;
+        }
+        if (!mbar_wait_lazy(&unit_empty[s], ph, &abort_flag, g.status, kDevTimeoutEmpty)) break;
+        units[s] = u;
+        mbar_arrive(&unit_full[s]);
+        if (u.kind == kEnd) break;
+        if (++s == kSlots) {
+          s = 0;
+          ph ^= 1u;
+        }
+        claim = atomicAdd(g.claimed, 1);
+      }
+    }
+  } else if (warp == 0) {
     if (elect_one()) {
       uint32_t st = ring, ph = 1;
       int s = 0;
       bool ok = true;
-      Unit u, v;
-      u.begin(plan);
-      for (bool more = u.load(plan, g, lists); ok && more; u = v) {
-        v = u;
-        v.next(plan, up_tiles);
-        more = v.load(plan, g, lists);
-        const int kqs = (u.down() ? g.I : g.H) / kBK;
-        const int row = (u.expert * (u.down() ? down_tiles : up_tiles) + u.tile) * kRows;
+      Unit u;
+      while (ok && take(u)) {
+        if (u.kind == kSum) continue;
+        const bool down = u.kind == kDown;
+        const int kqs = (down ? g.I : g.H) / kBK;
+        const int row = (u.expert * (down ? down_tiles : up_tiles) + u.tile) * kRows;
         const uint8_t* sf =
-            (u.down() ? g.w2_scales : g.w13_scales) + ((int64_t)(row >> 7) * kqs + u.k0) * 512;
-        const CUtensorMap* map = u.down() ? &tm2 : &tm13;
+            (down ? g.w2_scales : g.w13_scales) + ((int64_t)(row >> 7) * kqs + u.k0) * 512;
+        const CUtensorMap* map = down ? &tm2 : &tm13;
         int x = u.k0 * kBK;
-        bool ahead = true;
         for (int k = u.nk; k > 0; k -= 2) {
           ok = mbar_wait_lazy(&empty[s], ph, &abort_flag, g.status, kDevTimeoutEmpty);
           if (!ok) break;
@@ -680,19 +664,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           load_2d(st, map, &full[s], x, row);
           if (k > 1) load_2d(st + kWBytes, map, &full[s], x + kBK, row);
           load_bulk(st + 2u * (kWBytes + b_bytes), sf, half * 512u, &full[s]);
-          if (ahead) {
-            // the next unit lies in other pages: a first access there costs microseconds
-            // (address translation) and the ring holds less than two
-            if (more) {
-              const int cols = v.down() ? g.I : g.H;
-              const int64_t tile = (int64_t)v.expert * (v.down() ? down_tiles : up_tiles) + v.tile;
-              prefetch_l2((v.down() ? g.w2_codes : g.w13_codes) + tile * kRows * (cols / 2) +
-                          v.k0 * 64);
-              prefetch_l2((v.down() ? g.w2_scales : g.w13_scales) +
-                          (tile * (cols / kBK) + v.k0) * 512);
-            }
-            ahead = false;
-          }
           x += 2 * kBK;
           sf += 1024;
           st += stage_bytes;
@@ -713,19 +684,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     int s = 0, turn = warp & 1;
     bool ok = true, all_up = false;
     Unit u;
-    for (u.begin(plan); ok && u.load(plan, g, lists); u.next(plan, up_tiles)) {
-      const int cols = u.down() ? g.I : g.H;
-      const uint8_t* src = (u.down() ? g.hq + (size_t)u.off * 2 * g.I : g.xq) + (size_t)r * cols + c * 16;
-      const int row0 = (u.down() ? lane : lane < u.n ? lists.token[u.off + lane] : 0) * 2 * cols;
+    while (ok && take_warp(u)) {
+      if (u.kind == kSum) continue;
+      const bool down = u.kind == kDown;
+      const int cols = down ? g.I : g.H;
+      const uint8_t* src = (down ? g.hq + (size_t)u.off * 2 * g.I : g.xq) + (size_t)r * cols + c * 16;
+      const int row0 = (down ? lane : lane < u.n ? lists.token[u.off + lane] : 0) * 2 * cols;
       const int row1 =
-          (u.down() ? lane + 32 : lane + 32 < u.n ? lists.token[u.off + lane + 32] : 0) * 2 * cols;
+          (down ? lane + 32 : lane + 32 < u.n ? lists.token[u.off + lane + 32] : 0) * 2 * cols;
       const uint8_t* sf = g.h_scales + ((int64_t)u.active * (g.I / kBK) + u.k0) * 512 + lane * 16;
-      if (u.down()) {
+      if (down) {
         // every tile of the expert's h; once all experts' are there nothing is asked again
         if (!all_up) {
           if (lane == 0) {
-            all_up = ld_acquire_gpu(g.up_total) == lists.nact * up_tiles;
-            ok = all_up || wait_gpu(&g.up_done[u.active], up_tiles, &abort_flag, g.status);
+            all_up = ld_acquire_gpu(g.up_total) == lists.nact * u.up_units;
+            ok = all_up || wait_gpu(&g.up_done[u.active], u.up_units, &abort_flag, g.status);
           }
           __syncwarp();
           all_up = __shfl_sync(0xFFFFFFFFu, (int)all_up, 0) != 0;
@@ -747,7 +720,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               copy_async16(dst + (uint32_t)(((c & 7) ^ ((2 * j + r) & 7)) << 4), src + row + x);
             dst += 256u;
           }
-          if (u.down()) {
+          if (down) {
             const uint32_t f = st + 2u * b_bytes + 1024u + (uint32_t)lane * 16u;
             copy_async16(f, sf);
             if (k > 1) copy_async16(f + 512u, sf + 512);
@@ -772,7 +745,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       mx4::copy_scales(tmem + kConstCol, mx4::scale_desc_lo(smem_u32(const_sf)));
       Unit u;
-      for (u.begin(plan); ok && u.load(plan, g, lists); u.next(plan, up_tiles), ++local) {
+      while (ok && take(u)) {
+        if (u.kind == kSum) continue;
+        const bool down = u.kind == kDown;
         const int buf = local & 1;
         if (!mbar_wait_lazy(&acc_empty[buf], ((uint32_t)(local >> 1) & 1u) ^ 1u, &abort_flag,
                             g.status, kDevTimeoutMma))
@@ -788,12 +763,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t w = mx4::code_desc_lo(st << 4), b = w + b_off;
           const uint32_t w1 = w + (kWBytes >> 4), b1 = b + (b_bytes >> 4);
           const uint32_t f = mx4::scale_desc_lo((st + f_off) << 4);
-          const uint32_t sfb = u.down() ? cols + 8u : tmem + kConstCol, sfb1 = u.down() ? sfb + 4u : sfb;
+          const uint32_t sfb = down ? cols + 8u : tmem + kConstCol, sfb1 = down ? sfb + 4u : sfb;
           mx4::copy_scales(cols, f);
-          if (u.down()) mx4::copy_scales(sfb, f + 64u);
+          if (down) mx4::copy_scales(sfb, f + 64u);
           if (k > 1) {
             mx4::copy_scales(cols + 4u, f + 32u);
-            if (u.down()) mx4::copy_scales(sfb1, f + 96u);
+            if (down) mx4::copy_scales(sfb1, f + 96u);
           }
 #pragma unroll
           for (uint32_t j = 0; j < 4; ++j)
@@ -817,6 +792,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (ok) mma_commit(&acc_full[buf]);
+        ++local;
       }
       // every MMA of this thread has finished once `drain` flips
       mma_commit(&drain);
@@ -827,24 +803,41 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     const int quarter = warp & 3, row = quarter * 32 + lane, et = (int)threadIdx.x - 64;
     int local = 0;
-    bool done = false;
-    Unit u;
+    Unit u = {};
+    u.parts = 1;
     // The first two passes are rehearsals without tokens, of an up and of a down unit:
     // their instructions come from memory while the first products are under way, and not
     // when their sums are waited for.
     for (int pass = 0;; ++pass) {
       const bool live = pass > 1;
       uint32_t d = tmem + ((uint32_t)(quarter * 32) << 16);
-      int n = 0;
-      if (pass < 2) {
-        u.active = u.off = u.tile = u.part = 0;
-        u.parts = 1;
-        u.phase = pass + 1;
-      } else {
-        if (pass == 2) u.begin(plan);
-        if (!u.load(plan, g, lists)) {
-          done = true;
-          break;
+      u.kind = pass == 1 ? kDown : kUp;
+      if (live) {
+        const bool got = take_warp(u);
+        if (bar_red_or(1, 128, !got)) break;
+        if (u.kind == kSum) {
+          // Y: 128 columns of four tokens, a warp a token, four columns a lane
+          const bool ok = et != 0 || wait_gpu(&g.down_done[u.tile], lists.nact * g.down_parts,
+                                              &abort_flag, g.status);
+          __syncwarp();
+          if (bar_red_or(1, 128, !ok)) break;
+          const int t = u.active * 4 + quarter;
+          if (t < g.T) {
+            const int col = u.tile * kRows + lane * 4;
+            const float* at = g.part_down + (size_t)t * g.topk * g.H + col;
+            float4 y = make_float4(0, 0, 0, 0);
+            for (int p = 0; p < g.down_parts; ++p) {
+#pragma unroll 8
+              for (int c = 0; c < g.topk; ++c) {
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(at + (size_t)c * g.H));
+                y.x += v.x; y.y += v.y; y.z += v.z; y.w += v.w;
+              }
+              at += (size_t)slots * g.H;
+            }
+            *reinterpret_cast<uint2*>(g.Y + (size_t)t * g.H + col) =
+                make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+          }
+          continue;
         }
         const int buf = local & 1;
         const bool ok = mbar_wait_lazy(&acc_full[buf], (uint32_t)(local >> 1) & 1u, &abort_flag,
@@ -853,9 +846,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (bar_red_or(1, 128, !ok)) break;
         tc_fence_after();
         d += (uint32_t)buf * 128u;
-        n = u.n;
       }
-      const int parts = u.parts;
+      const int parts = u.parts, n = u.n;
       // eight tokens' values of this row (hi + lo)
       auto read8 = [&](int j0, float (&v)[8]) {
         uint32_t r[16];
@@ -870,8 +862,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (live && lane == 0) mbar_arrive(&acc_empty[local & 1]);
       };
-      if (!u.down()) {
-        float* part = g.part_up + (size_t)plan.tail_index * parts * g.T * kRows;
+      if (u.kind == kUp) {
+        const int unit = u.active * up_tiles + u.tile;
+        float* part = g.part_up + (size_t)unit * parts * g.T * kRows;
         bool last = true;
         if (parts > 1) {
 #pragma unroll 1
@@ -883,7 +876,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (j0 + j < n) part[((size_t)u.part * g.T + j0 + j) * kRows + row] = v[j];
           }
           bar_sync(1, 128);
-          if (et == 0) ready = arrive_gpu(&g.up_joined[plan.tail_index]) == parts - 1;
+          if (et == 0) ready = arrive_gpu(&g.up_joined[unit]) == parts - 1;
           bar_sync(1, 128);
           last = ready != 0;
         }
@@ -952,13 +945,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     (r >> 5) * 4 + (at & 127) / 32) = (uint16_t)(by | by << 8);
               }
             }
-            bar_sync(1, 128);   // stage_v is free again; h is written
+            bar_sync(1, 128);   // stage_v is free again
             j0 += 8;
           } while (j0 < n);
-          if (live && et == 0) {
-            signal_gpu(&g.up_done[u.active]);
-            signal_gpu(g.up_total);
-          }
         }
         release();
       } else {
@@ -977,36 +966,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           j0 += 8;
         } while (j0 < n);
         release();
-        bar_sync(1, 128);
-        if (live && et == 0) signal_gpu(&g.down_done[u.tile]);
       }
       if (live) {
-        u.next(plan, up_tiles);
+        // (two units back the other warp has told)
+        const bool ok = mbar_wait_lazy(&told_empty[local & 1], ((uint32_t)(local >> 1) & 1u) ^ 1u,
+                                       &abort_flag, g.status, kDevTimeoutMma);
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(&told_full[local & 1]);
         ++local;
-      }
-    }
-    // Y: 128 columns of four tokens an item, a warp a token, four columns a lane
-    const int items = down_tiles * ((g.T + 3) / 4);
-    for (int item = (int)blockIdx.x; done && item < items; item += (int)gridDim.x) {
-      const int tile = item % down_tiles, t = item / down_tiles * 4 + quarter;
-      const bool ok =
-          et != 0 || wait_gpu(&g.down_done[tile], lists.nact * g.down_parts, &abort_flag, g.status);
-      __syncwarp();
-      if (bar_red_or(1, 128, !ok)) break;
-      if (t < g.T) {
-        const int col = tile * kRows + lane * 4;
-        const float* at = g.part_down + (size_t)t * g.topk * g.H + col;
-        float4 y = make_float4(0, 0, 0, 0);
-        for (int p = 0; p < g.down_parts; ++p) {
-#pragma unroll 8
-          for (int c = 0; c < g.topk; ++c) {
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(at + (size_t)c * g.H));
-            y.x += v.x; y.y += v.y; y.z += v.z; y.w += v.w;
-          }
-          at += (size_t)slots * g.H;
-        }
-        *reinterpret_cast<uint2*>(g.Y + (size_t)t * g.H + col) =
-            make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
       }
     }
   }
@@ -1062,7 +1029,7 @@ static Layout layout(int64_t T, int64_t H, int64_t E, int topk, int64_t I) {
   l.h_scales = take((size_t)l.max_act * (I / 128) * 512);
   l.part_up = take((size_t)kMaxGrid * T * kRows * 4);   // units x parts <= blocks
   l.part_down = take((size_t)l.splits_down * slots * H * 4);
-  l.n_counters = 1 + l.max_act + kMaxGrid + (int)(H / kRows);
+  l.n_counters = 2 + l.max_act + kMaxGrid + (int)(H / kRows);
   l.counters = take((size_t)l.n_counters * 4);
   l.total = at;
   return l;
@@ -1157,8 +1124,9 @@ cudaError_t launch_moe(const MoeArgs& a, int sm_count, cudaStream_t st) {
   g.h_scales = w + l.h_scales;
   g.part_up = reinterpret_cast<float*>(w + l.part_up);
   g.part_down = reinterpret_cast<float*>(w + l.part_down);
-  g.up_total = counters;
-  g.up_done = counters + 1;
+  g.claimed = counters;
+  g.up_total = counters + 1;
+  g.up_done = counters + 2;
   g.up_joined = g.up_done + l.max_act;
   g.down_done = g.up_joined + kMaxGrid;
   g.Y = a.Y;
@@ -1169,13 +1137,11 @@ cudaError_t launch_moe(const MoeArgs& a, int sm_count, cudaStream_t st) {
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = 1024 + kRingBytes;
   cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeCooperative;
-  attr[0].val.cooperative = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, k_moe_experts, tm13, tm2, g);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
