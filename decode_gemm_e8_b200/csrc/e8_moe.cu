@@ -276,12 +276,12 @@ struct ExpertArgs {
   const float* xs;         // scale of each token's pair
   uint8_t* hq;             // the slots' hi and lo rows of h, sorted by expert
   uint8_t* h_scales;       // [active expert][I / 128][512]
-  float* part_up;          // [up unit * parts + part][T][128], where units are split
+  float* part_up;          // [split up unit * parts + part][T][128]
   float* part_down;        // [part][slot][H]
   int* claimed;            // units so far
   int* up_done;            // [active expert]: finished up units
   int* up_total;           // finished up units of all
-  int* up_joined;          // [up unit]: arrived parts
+  int* up_joined;          // [split up unit]: arrived parts
   int* down_done;          // [tile]: finished units
   uint16_t* Y;
   uint32_t* status;
@@ -295,8 +295,11 @@ __device__ __forceinline__ void prefetch_l2(const void* p) {
 }
 // One thread tells (or counts) for its block after a barrier that the others' writes
 // came before.
-__device__ __forceinline__ void signal_gpu(int* counter) {
-  asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(counter) : "memory");
+__device__ __forceinline__ void fence_gpu() {
+  asm volatile("fence.acq_rel.gpu;" ::: "memory");
+}
+__device__ __forceinline__ void add_gpu(int* counter) {
+  asm volatile("red.relaxed.gpu.global.add.s32 [%0], 1;" ::"l"(counter) : "memory");
 }
 __device__ __forceinline__ int arrive_gpu(int* counter) {
   int old;
@@ -448,15 +451,18 @@ __device__ __forceinline__ void build_lists(SharedLists& l, unsigned long long* 
 }
 
 // A unit as the scheduler warp writes it down for the others.  The numbers run over the
-// up products (row tiles of an expert, each in parts of K, then the next expert's), the
-// down products in the same way, and the sums (128 columns of four tokens).
+// up products (row tiles of an expert, then the next expert's), the down products (each
+// tile in parts of K), and the sums (128 columns of four tokens).  The up units that
+// fill no whole round of the blocks are split over K between them and come first, so
+// that the joining of their parts is over long before the down products ask for it.
 enum : int { kUp = 0, kDown = 1, kSum = 2, kEnd = 3 };
 struct Unit {
   int kind;
   int active, tile, part, parts;   // active expert; row tile; part of K
   int expert, off, n;              // n tokens from slot[off] on
   int k0, nk;                      // 128-column steps of K
-  int up_units;                    // of each expert, parts counted
+  int joined;                      // number of a split up unit
+  int want, want_all;              // up units, parts counted, of this expert and of all
 };
 
 // Warps: 0 weights producer, 6 and 7 activations producers, 1 MMAs, 2..5 epilogue, 8
@@ -477,6 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ SharedLists lists;
   __shared__ Unit units[kSlots];
   __shared__ uint64_t unit_full[kSlots], unit_empty[kSlots], told_full[2], told_empty[2];
+  __shared__ uint64_t weights_took;
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drain;
   __shared__ uint32_t tmem_slot;
   __shared__ volatile uint32_t abort_flag;
@@ -501,6 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&told_full[i], 4);
       mbar_init(&told_empty[i], 1);
     }
+    mbar_init(&weights_took, 1);
     mbar_init(&drain, 1);
     abort_flag = 0u;
     fence_mbar_init();
@@ -584,11 +592,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                             kDevTimeoutMma))
           break;
         // the four epilogue warps' writes came before; a part of a unit counts as one of it
+        fence_gpu();
         if (u.kind == kDown) {
-          signal_gpu(&g.down_done[u.tile]);
+          add_gpu(&g.down_done[u.tile]);
         } else {
-          signal_gpu(&g.up_done[u.active]);
-          signal_gpu(g.up_total);
+          add_gpu(&g.up_done[u.active]);
+          add_gpu(g.up_total);
         }
         mbar_arrive(&told_empty[i & 1]);
         ++i;
@@ -597,24 +606,44 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 8) {
     if (lane == 0) {
       const int nact = lists.nact, ups = nact * up_tiles, grid = (int)gridDim.x;
-      const int up_parts = ups * 2 > grid ? 1 : min(min(kMaxUpParts, grid / ups), g.H / kBK);
-      const int per_up = up_tiles * up_parts, per_down = down_tiles * g.down_parts;
-      const int n_up = nact * per_up, n_down = n_up + nact * per_down;
+      const int whole = ups / grid * grid, rest = ups - whole;
+      const int up_parts = rest ? min(min(kMaxUpParts, grid / rest), g.H / kBK) : 1;
+      const int n_split = rest * up_parts, n_up = n_split + whole;
+      const int per_down = down_tiles * g.down_parts, n_down = n_up + nact * per_down;
       const int n_all = n_down + down_tiles * ((g.T + 3) / 4);
-      int s = 0;
-      uint32_t ph = 1;
+      int s = 0, ahead = 0;
+      uint32_t ph = 1, took_ph = 0;
       for (;;) {
         Unit u = {};
-        u.up_units = per_up;
         u.kind = claim < n_up ? kUp : claim < n_down ? kDown : claim < n_all ? kSum : kEnd;
         if (u.kind < kSum) {
           const bool down = u.kind == kDown;
-          const int i = down ? claim - n_up : claim, per = down ? per_down : per_up;
-          u.parts = down ? g.down_parts : up_parts;
-          u.active = i / per;
-          const int rest = i - u.active * per, kq = (down ? g.I : g.H) / kBK;
-          u.tile = rest / u.parts;
-          u.part = rest - u.tile * u.parts;
+          const int kq = (down ? g.I : g.H) / kBK;
+          u.parts = 1;
+          u.part = 0;
+          if (down) {
+            const int i = claim - n_up;
+            u.active = i / per_down;
+            const int at = i - u.active * per_down;
+            u.parts = g.down_parts;
+            u.tile = at / u.parts;
+            u.part = at - u.tile * u.parts;
+            // of this expert's up tiles, those that were split
+            const int split = min(up_tiles, max(0, (u.active + 1) * up_tiles - whole));
+            u.want = up_tiles + split * (up_parts - 1);
+            u.want_all = n_up;
+          } else {
+            int i = claim - n_split;
+            if (i < 0) {
+              const int unit = claim / up_parts;
+              u.parts = up_parts;
+              u.part = claim - unit * up_parts;
+              u.joined = unit;
+              i = whole + unit;
+            }
+            u.active = i / up_tiles;
+            u.tile = i - u.active * up_tiles;
+          }
           u.expert = lists.expert[u.active];
           u.off = lists.off[u.active];
           u.n = lists.off[u.active + 1] - u.off;
@@ -637,6 +666,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           s = 0;
           ph ^= 1u;
         }
+        // The next one when the weights' producer begins this unit, or the one before if
+        // it is short: claimed in time, and not kept from blocks that would be sooner.
+        if (u.kind < kSum && u.nk <= 8 && ahead == 0) {
+          ahead = 1;
+        } else {
+          if (!mbar_wait_lazy(&weights_took, took_ph, &abort_flag, g.status, kDevTimeoutEmpty))
+            break;
+          took_ph ^= 1u;
+        }
         claim = atomicAdd(g.claimed, 1);
       }
     }
@@ -647,6 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       Unit u;
       while (ok && take(u)) {
+        mbar_arrive(&weights_took);
         if (u.kind == kSum) continue;
         const bool down = u.kind == kDown;
         const int kqs = (down ? g.I : g.H) / kBK;
@@ -697,8 +736,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // every tile of the expert's h; once all experts' are there nothing is asked again
         if (!all_up) {
           if (lane == 0) {
-            all_up = ld_acquire_gpu(g.up_total) == lists.nact * u.up_units;
-            ok = all_up || wait_gpu(&g.up_done[u.active], u.up_units, &abort_flag, g.status);
+            all_up = ld_acquire_gpu(g.up_total) == u.want_all;
+            ok = all_up || wait_gpu(&g.up_done[u.active], u.want, &abort_flag, g.status);
           }
           __syncwarp();
           all_up = __shfl_sync(0xFFFFFFFFu, (int)all_up, 0) != 0;
@@ -863,8 +902,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (live && lane == 0) mbar_arrive(&acc_empty[local & 1]);
       };
       if (u.kind == kUp) {
-        const int unit = u.active * up_tiles + u.tile;
-        float* part = g.part_up + (size_t)unit * parts * g.T * kRows;
+        float* part = g.part_up + (size_t)u.joined * parts * g.T * kRows;
         bool last = true;
         if (parts > 1) {
 #pragma unroll 1
@@ -876,7 +914,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (j0 + j < n) part[((size_t)u.part * g.T + j0 + j) * kRows + row] = v[j];
           }
           bar_sync(1, 128);
-          if (et == 0) ready = arrive_gpu(&g.up_joined[unit]) == parts - 1;
+          if (et == 0) ready = arrive_gpu(&g.up_joined[u.joined]) == parts - 1;
           bar_sync(1, 128);
           last = ready != 0;
         }
@@ -994,16 +1032,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------------- host ---
-// K parts of the down product's units: eight stages a unit, so that a block that waits
-// for one expert's h has other units to do, and that the last round is short; more when
-// even so the units are fewer than the SMs.
+// K parts of the down product's units: at most eight stages a unit, so that the end is
+// even and a block that waits for one expert's h has other units to do; more when even so
+// there are not two units for three SMs, down to two stages each.
 static int choose_splits(int64_t T, int64_t E, int topk, int64_t tiles, int64_t K) {
   const int kq = (int)(K / kBK);
   const int64_t slots = T * topk, units = (slots < E ? slots : E) * tiles;
-  int64_t s = (kq + 15) / 16, few = 148 / units;
-  if (s < few) s = few < kq / 2 ? few : kq / 2;
-  if (s > kMaxDownParts) s = kMaxDownParts;
-  return s < 1 ? 1 : (int)s;
+  int64_t s = (kq + 15) / 16, few = 148 * 2 / 3 / units;
+  if (few > kq / 4) few = kq / 4;
+  if (s < few) s = few;
+  return s > kMaxDownParts ? kMaxDownParts : (int)s;
 }
 
 struct Layout {
