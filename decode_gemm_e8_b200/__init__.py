@@ -15,6 +15,7 @@ vector) and the "Bit widths" table (one global scale per layer).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -118,8 +119,8 @@ def load_library(path: str = LIB_PATH):
         "e8_mx4_encode": ([P, P, c.c_int, I64, I64, I64, I64, P, P, P], c.c_int),
         "e8_mx4_decode_to_bf16": ([P, P, P, I64, I64, I64, P, P], c.c_int),
         "e8_mx4_gemm_codes": ([P, P, P, I64, P, P, I64, I64, P, P, c.c_size_t, P], c.c_int),
-        "e8_mx4_gemm": ([P, P, c.c_int, I64, I64, P, P, I64, I64, P, P, c.c_size_t, P], c.c_int),
         "e8_mx4_gemm_codes_workspace_bytes": ([I64, I64, I64], c.c_size_t),
+        "e8_mx4_gemm": ([P, P, c.c_int, I64, I64, P, P, I64, I64, P, P, c.c_size_t, P], c.c_int),
         "e8_mx4_gemm_workspace_bytes": ([I64, I64, I64], c.c_size_t),
         "e8_mx4_moe": ([P, P, I64, I64, P, I64, c.c_int, c.c_int, P, P, I64, P, P, P, P, P, P,
                         c.c_size_t, P], c.c_int),
@@ -547,44 +548,75 @@ class Mx4Matrix:
     power-of-two scale each, as e8_mx4_encode writes it: codes uint8
     [(batch,) rows, 16 ceil(K / 32)] and scales uint8 [(batch,) bytes in tiles]."""
 
+    __slots__ = ("codes", "scales", "rows", "K", "batch")
+
     def __init__(self, codes, scales, rows: int, K: int, batch: int | None = None):
         self.codes, self.scales = codes, scales
-        self.rows, self.K, self.batch = int(rows), int(K), None if batch is None else int(batch)
-        lib = load_library()
-        n = 1 if self.batch is None else self.batch
-        if codes.numel() != n * lib.e8_mx4_code_bytes(self.rows, self.K) or \
-                scales.numel() != n * lib.e8_mx4_scale_bytes(self.rows, self.K):
+        self.rows = rows = int(rows)
+        self.K = K = int(K)
+        self.batch = None if batch is None else int(batch)
+        n = 1 if batch is None else self.batch
+        # e8_mx4_code_bytes and e8_mx4_scale_bytes
+        if rows < 0 or K < 1 or codes.numel() != n * rows * ((K + 31) // 32 * 16) or \
+                scales.numel() != n * ((rows + 127) // 128) * ((K + 127) // 128) * 512:
             raise E8Error(E8_EINVAL, "Mx4Matrix")
 
 
+_mx4_dtypes = {}
+
+
 def _mx4_dtype(X) -> int:
-    import torch
-    return {torch.bfloat16: E8_DT_BF16, torch.float16: E8_DT_F16,
-            torch.float32: E8_DT_F32}.get(X.dtype, -1)
+    if not _mx4_dtypes:
+        import torch
+        _mx4_dtypes.update({torch.bfloat16: E8_DT_BF16, torch.float16: E8_DT_F16,
+                            torch.float32: E8_DT_F32})
+    return _mx4_dtypes.get(X.dtype, -1)
 
 
 def _mx4_check(cb: Codebook, where: str, *tensors):
     """Device tensors of the codebook's device, densely laid out."""
+    dev = cb.device
     for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda or t.device.index != cb.device:
-            raise E8Error(E8_EDEVICE, where)
-        if not t.is_contiguous():
-            raise E8Error(E8_EINVAL, where)
+        if t is not None:
+            if t.get_device() != dev:
+                raise E8Error(E8_EDEVICE, where)
+            if not t.is_contiguous():
+                raise E8Error(E8_EINVAL, where)
 
 
-def _mx4_out(out, shape, dtype, like, stream, where):
-    """The caller's output after a check, or a new one owned by the stream that writes it."""
-    import torch
-    if out is not None:
-        if tuple(out.shape) != tuple(shape) or out.dtype != dtype:
-            raise E8Error(E8_EINVAL, where)
-        return out
+def _mx4_new(shape, dtype, like, stream):
+    """A new tensor that belongs to the stream that will write it."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
+    import torch
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
+
+
+def _mx4_out(out, shape, dtype, where):
+    if out.shape != shape or out.dtype != dtype:
+        raise E8Error(E8_EINVAL, where)
+
+
+def _mx4_stream(cb: Codebook, stream):
+    import torch
+    return torch._C._cuda_getCurrentRawStream(cb.device) if stream is None else stream.cuda_stream
+
+
+def _mx4_row_stride(cb: Codebook, X, where: str) -> int:
+    if X.get_device() != cb.device:
+        raise E8Error(E8_EDEVICE, where)
+    if X.is_contiguous():
+        return X.shape[-1]
+    rows, K = X.shape[-2:]
+    if K > 1 and X.stride(-1) != 1:
+        raise E8Error(E8_EINVAL, where)
+    return K if rows == 1 else X.stride(-2)
+
+
+@functools.lru_cache(maxsize=1024)
+def _mx4_ws_bytes(call: str, *args) -> int:
+    return getattr(load_library(), call)(*args)
 
 
 def e8_mx4_encode(cb: Codebook, X, out: Mx4Matrix | None = None, stream=None) -> Mx4Matrix:
@@ -593,87 +625,101 @@ def e8_mx4_encode(cb: Codebook, X, out: Mx4Matrix | None = None, stream=None) ->
     The last dimension must be dense; rows may be further apart (a slice of a wider
     matrix), matrices rows * row stride apart."""
     import torch
-    if X.dim() not in (2, 3):
-        raise E8Error(E8_EINVAL, "e8_mx4_encode")
-    batch = X.shape[0] if X.dim() == 3 else None
-    rows, K = X.shape[-2:]
-    ldx = _mx4_row_stride(cb, X, "e8_mx4_encode")
-    if batch is not None and batch > 1 and rows > 0:
+    where = "e8_mx4_encode"
+    shape = X.shape
+    if len(shape) == 2:
+        batch, n, lead = None, 1, ()
+        rows, K = shape
+    elif len(shape) == 3:
+        batch, rows, K = shape
+        n, lead = batch, (batch,)
+    else:
+        raise E8Error(E8_EINVAL, where)
+    ldx = _mx4_row_stride(cb, X, where)
+    if n > 1 and rows > 0:
         if rows == 1:
             ldx = X.stride(0)
         elif X.stride(0) != rows * ldx:
-            raise E8Error(E8_EINVAL, "e8_mx4_encode")
-    lib = load_library()
-    n = 1 if batch is None else batch
-    lead = () if batch is None else (batch,)
+            raise E8Error(E8_EINVAL, where)
     if out is None:
-        cs, sb = lib.e8_mx4_code_bytes(rows, K), lib.e8_mx4_scale_bytes(rows, K)
-        if cs < 0:
-            raise E8Error(E8_EINVAL, "e8_mx4_encode")
-        codes = _mx4_out(None, lead + (rows, cs // max(rows, 1)), torch.uint8, X, stream, "")
-        scales = _mx4_out(None, lead + (sb,), torch.uint8, X, stream, "")
-        out = Mx4Matrix(codes, scales, rows, K, batch)
-    elif (out.rows, out.K, out.batch) != (rows, K, batch):
-        raise E8Error(E8_EINVAL, "e8_mx4_encode")
-    _mx4_check(cb, "e8_mx4_encode", out.codes, out.scales)
-    _check(lib.e8_mx4_encode(cb.handle, _ptr(X), _mx4_dtype(X), n, rows, K, ldx, _ptr(out.codes),
-                             _ptr(out.scales), _stream(stream)), "e8_mx4_encode")
+        if K < 1:
+            raise E8Error(E8_EINVAL, where)
+        u8 = torch.uint8
+        out = Mx4Matrix(_mx4_new(lead + (rows, (K + 31) // 32 * 16), u8, X, stream),
+                        _mx4_new(lead + (((rows + 127) // 128) * ((K + 127) // 128) * 512,), u8, X,
+                                 stream), rows, K, batch)
+    else:
+        if (out.rows, out.K, out.batch) != (rows, K, batch):
+            raise E8Error(E8_EINVAL, where)
+        _mx4_check(cb, where, out.codes, out.scales)
+    rc = (_lib or load_library()).e8_mx4_encode(
+        cb.handle, X.data_ptr(), _mx4_dtype(X), n, rows, K, ldx, out.codes.data_ptr(),
+        out.scales.data_ptr(), _mx4_stream(cb, stream))
+    if rc:
+        _check(rc, where)
     return out
-
-
-def _mx4_row_stride(cb: Codebook, X, where: str) -> int:
-    if not X.is_cuda or X.device.index != cb.device:
-        raise E8Error(E8_EDEVICE, where)
-    rows, K = X.shape[-2:]
-    if K > 1 and X.stride(-1) != 1:
-        raise E8Error(E8_EINVAL, where)
-    return K if X.numel() == 0 or rows == 1 else X.stride(-2)
 
 
 def e8_mx4_decode_to_bf16(cb: Codebook, m: Mx4Matrix, out=None, stream=None):
     """bf16 [(batch,) rows, K] values of an Mx4Matrix."""
     import torch
+    where = "e8_mx4_decode_to_bf16"
     shape = (m.rows, m.K) if m.batch is None else (m.batch, m.rows, m.K)
-    out = _mx4_out(out, shape, torch.bfloat16, m.codes, stream, "e8_mx4_decode_to_bf16")
-    _mx4_check(cb, "e8_mx4_decode_to_bf16", m.codes, m.scales, out)
-    _check(load_library().e8_mx4_decode_to_bf16(
-        cb.handle, _ptr(m.codes), _ptr(m.scales), 1 if m.batch is None else m.batch, m.rows, m.K,
-        _ptr(out), _stream(stream)), "e8_mx4_decode_to_bf16")
+    _mx4_check(cb, where, m.codes, m.scales, out)
+    if out is None:
+        out = _mx4_new(shape, torch.bfloat16, m.codes, stream)
+    else:
+        _mx4_out(out, shape, torch.bfloat16, where)
+    rc = (_lib or load_library()).e8_mx4_decode_to_bf16(
+        cb.handle, m.codes.data_ptr(), m.scales.data_ptr(), 1 if m.batch is None else m.batch,
+        m.rows, m.K, out.data_ptr(), _mx4_stream(cb, stream))
+    if rc:
+        _check(rc, where)
     return out
 
 
 def e8_mx4_gemm(cb: Codebook, X, m: Mx4Matrix, Y=None, workspace=None, stream=None):
     """Y bf16 [M, N] = X [M, K] (bf16, fp16 or fp32, encoded on the way) times m transposed."""
     import torch
-    if X.dim() != 2 or X.shape[1] != m.K or m.batch is not None:
-        raise E8Error(E8_EINVAL, "e8_mx4_gemm")
-    M = X.shape[0]
-    ldx = _mx4_row_stride(cb, X, "e8_mx4_gemm")
-    lib = load_library()
-    Y = _mx4_out(Y, (M, m.rows), torch.bfloat16, X, stream, "e8_mx4_gemm")
-    ws = workspace if workspace is not None else _mx4_out(
-        None, (max(16, lib.e8_mx4_gemm_workspace_bytes(M, m.rows, m.K)),), torch.uint8, X, stream, "")
-    _mx4_check(cb, "e8_mx4_gemm", m.codes, m.scales, Y, ws)
-    _check(lib.e8_mx4_gemm(cb.handle, _ptr(X), _mx4_dtype(X), M, ldx, _ptr(m.codes), _ptr(m.scales),
-                           m.rows, m.K, _ptr(Y), _ptr(ws), ws.numel(), _stream(stream)),
-           "e8_mx4_gemm")
+    where = "e8_mx4_gemm"
+    shape = X.shape
+    if len(shape) != 2 or shape[1] != m.K or m.batch is not None:
+        raise E8Error(E8_EINVAL, where)
+    M, N, K = shape[0], m.rows, m.K
+    ldx = _mx4_row_stride(cb, X, where)
+    _mx4_check(cb, where, m.codes, m.scales, Y, workspace)
+    if Y is None:
+        Y = _mx4_new((M, N), torch.bfloat16, X, stream)
+    else:
+        _mx4_out(Y, (M, N), torch.bfloat16, where)
+    if workspace is None:
+        workspace = _mx4_new((_mx4_ws_bytes("e8_mx4_gemm_workspace_bytes", M, N, K),), torch.uint8,
+                             X, stream)
+    rc = (_lib or load_library()).e8_mx4_gemm(
+        cb.handle, X.data_ptr(), _mx4_dtype(X), M, ldx, m.codes.data_ptr(), m.scales.data_ptr(), N,
+        K, Y.data_ptr(), workspace.data_ptr(), workspace.numel(), _mx4_stream(cb, stream))
+    if rc:
+        _check(rc, where)
     return Y
 
 
 def e8_mx4_gemm_codes(cb: Codebook, a: Mx4Matrix, m: Mx4Matrix, Y=None, workspace=None, stream=None):
-    """Y bf16 [M, N] = a [M, K] times m [N, K] transposed, both encoded."""
+    """Y bf16 [M, N] = a [M, K] times m [N, K] transposed, both encoded (no workspace needed)."""
     import torch
+    where = "e8_mx4_gemm_codes"
     if a.K != m.K or a.batch is not None or m.batch is not None:
-        raise E8Error(E8_EINVAL, "e8_mx4_gemm_codes")
-    lib = load_library()
-    Y = _mx4_out(Y, (a.rows, m.rows), torch.bfloat16, a.codes, stream, "e8_mx4_gemm_codes")
-    ws = workspace if workspace is not None else _mx4_out(
-        None, (max(16, lib.e8_mx4_gemm_codes_workspace_bytes(a.rows, m.rows, m.K)),), torch.uint8,
-        a.codes, stream, "")
-    _mx4_check(cb, "e8_mx4_gemm_codes", a.codes, a.scales, m.codes, m.scales, Y, ws)
-    _check(lib.e8_mx4_gemm_codes(cb.handle, _ptr(a.codes), _ptr(a.scales), a.rows, _ptr(m.codes),
-                                 _ptr(m.scales), m.rows, m.K, _ptr(Y), _ptr(ws), ws.numel(),
-                                 _stream(stream)), "e8_mx4_gemm_codes")
+        raise E8Error(E8_EINVAL, where)
+    _mx4_check(cb, where, a.codes, a.scales, m.codes, m.scales, Y, workspace)
+    if Y is None:
+        Y = _mx4_new((a.rows, m.rows), torch.bfloat16, a.codes, stream)
+    else:
+        _mx4_out(Y, (a.rows, m.rows), torch.bfloat16, where)
+    rc = (_lib or load_library()).e8_mx4_gemm_codes(
+        cb.handle, a.codes.data_ptr(), a.scales.data_ptr(), a.rows, m.codes.data_ptr(),
+        m.scales.data_ptr(), m.rows, m.K, Y.data_ptr(), _ptr(workspace),
+        0 if workspace is None else workspace.numel(), _mx4_stream(cb, stream))
+    if rc:
+        _check(rc, where)
     return Y
 
 
@@ -687,27 +733,34 @@ def e8_mx4_moe(cb: Codebook, X, router, w13: Mx4Matrix, w2: Mx4Matrix, topk: int
     (int32 [T, topk]) and probs (fp32 [T, topk]) are filled when given."""
     import torch
     where = "e8_mx4_moe"
-    if X.dim() != 2 or router.dim() != 2 or X.dtype != torch.bfloat16 or \
-            router.dtype != torch.bfloat16 or w13.batch is None or w2.batch is None:
+    bf16 = torch.bfloat16
+    shape, E, inner, topk = X.shape, w13.batch, w2.K, int(topk)
+    if len(shape) != 2 or X.dtype != bf16 or router.dtype != bf16 or E is None:
         raise E8Error(E8_EINVAL, where)
-    (T, H), E, inner = X.shape, router.shape[0], w2.K
-    if (router.shape[1], w13.batch, w2.batch, w13.rows, w13.K, w2.rows) != \
-            (H, E, E, 2 * inner, H, H):
+    T, H = shape
+    if router.shape != (E, H) or w2.batch != E or w13.rows != 2 * inner or w13.K != H or \
+            w2.rows != H:
         raise E8Error(E8_EINVAL, where)
-    lib = load_library()
-    for t, kind in ((experts, torch.int32), (probs, torch.float32)):
-        if t is not None and (tuple(t.shape) != (T, topk) or t.dtype != kind):
-            raise E8Error(E8_EINVAL, where)
-    Y = _mx4_out(Y, (T, H), torch.bfloat16, X, stream, where)
-    ws = workspace if workspace is not None else _mx4_out(
-        None, (max(16, lib.e8_mx4_moe_workspace_bytes(T, H, E, int(topk), inner)),), torch.uint8, X,
-        stream, "")
+    if experts is not None:
+        _mx4_out(experts, (T, topk), torch.int32, where)
+    if probs is not None:
+        _mx4_out(probs, (T, topk), torch.float32, where)
     _mx4_check(cb, where, X, router, w13.codes, w13.scales, w2.codes, w2.scales, Y, experts, probs,
-               ws)
-    _check(lib.e8_mx4_moe(cb.handle, _ptr(X), T, H, _ptr(router), E, int(topk), int(bool(renormalize)),
-                          _ptr(w13.codes), _ptr(w13.scales), inner, _ptr(w2.codes), _ptr(w2.scales),
-                          _ptr(Y), _ptr(experts), _ptr(probs), _ptr(ws), ws.numel(),
-                          _stream(stream)), where)
+               workspace)
+    if Y is None:
+        Y = _mx4_new(shape, bf16, X, stream)
+    else:
+        _mx4_out(Y, shape, bf16, where)
+    if workspace is None:
+        workspace = _mx4_new((_mx4_ws_bytes("e8_mx4_moe_workspace_bytes", T, H, E, topk, inner),),
+                             torch.uint8, X, stream)
+    rc = (_lib or load_library()).e8_mx4_moe(
+        cb.handle, X.data_ptr(), T, H, router.data_ptr(), E, topk, 1 if renormalize else 0,
+        w13.codes.data_ptr(), w13.scales.data_ptr(), inner, w2.codes.data_ptr(),
+        w2.scales.data_ptr(), Y.data_ptr(), _ptr(experts), _ptr(probs), workspace.data_ptr(),
+        workspace.numel(), _mx4_stream(cb, stream))
+    if rc:
+        _check(rc, where)
     return Y
 
 
