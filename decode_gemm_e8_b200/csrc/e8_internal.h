@@ -228,11 +228,16 @@ cudaError_t launch_mx4_encode(const void* X, int dtype, int64_t batch, int64_t r
                               cudaStream_t st);
 cudaError_t launch_mx4_decode(const uint8_t* codes, const uint8_t* scales, int64_t batch,
                               int64_t rows, int64_t K, uint16_t* out, cudaStream_t st);
-size_t mx4_gemm_workspace(int64_t M, int64_t N, int64_t K);
 cudaError_t launch_mx4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int64_t M,
                             const uint8_t* w_codes, const uint8_t* w_scales, int64_t N, int64_t K,
-                            uint16_t* Y, void* ws, uint32_t* status, int sm_count, int early,
+                            uint16_t* Y, uint32_t* status, int sm_count, int early,
                             cudaStream_t st);
+// Up to kMx4Small tokens that are not encoded yet, in one launch.
+constexpr int kMx4Small = 8;
+cudaError_t launch_mx4_gemm_small(const void* X, int dtype, int64_t M, int64_t ldx,
+                                  const uint8_t* w_codes, const uint8_t* w_scales, int64_t N,
+                                  int64_t K, uint16_t* Y, uint32_t* status, int sm_count,
+                                  cudaStream_t st);
 
 // Mixture-of-experts layer for a few tokens (e8_moe.cu).
 struct MoeArgs {

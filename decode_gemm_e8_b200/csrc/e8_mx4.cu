@@ -10,11 +10,9 @@
 // own rule) and the warp writes 128 consecutive bytes of codes.  The scale exponent
 // is the exponent field of the maximum, and the division by it is an exact
 // multiplication.  The decoder looks codes up as bf16 bytes (byte permutation) and
-// scales pairs.  Rows that do not start on 16 bytes go one value a lane, so that every
-// load or store of a warp is still of neighbouring values: a block is then a whole
-// warp's, and nibbles or codes travel by shuffles.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
+// scales pairs.  Rows that do not start on 16 bytes still move in aligned 16-byte words,
+// which neighbouring lanes share by shuffles and a funnel shift.
+#include <type_traits>
 
 #include "e8_internal.h"
 #include "e8_mx4.cuh"
@@ -26,84 +24,77 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kRows = 4;   // rows a warp has in flight at once
 
-template <int DT> struct Elem;
-template <> struct Elem<0> { using T = uint16_t; };
-template <> struct Elem<1> { using T = uint16_t; };
-template <> struct Elem<2> { using T = float; };
-
+// Rows that start anywhere.  Lane l reads the 16-byte words (2 of them in fp32) that
+// hold its first value; what is missing at their end it gets from lane l + 1, lane 31
+// from memory.  A word that is not wholly inside the row is read value by value.
 template <int DT>
-__device__ __forceinline__ float to_float(typename Elem<DT>::T v) {
-  if constexpr (DT == 0) return __uint_as_float((uint32_t)v << 16);
-  else if constexpr (DT == 1) return __half2float(__ushort_as_half(v));
-  else return v;
-}
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
+struct Shifted {
+  static constexpr int kPer = DT == 2 ? 4 : 8;     // values a word
+  static constexpr int kWords = DT == 2 ? 2 : 1;
+  uint32_t w[4 * kWords], next[4];
+  int shift;   // values between the word's start and the lane's first value: one for a row
 
-// Eight values of a row from column c on (zeros past K), as they lie in memory.
-template <int DT>
-struct Eight {
-  uint32_t w[DT == 2 ? 8 : 4];
-  __device__ __forceinline__ void load(const typename Elem<DT>::T* __restrict__ row, int64_t c,
-                                       int64_t K) {
-    if (c + 8 <= K) {
+  static __device__ __forceinline__ void word(const typename Elem<DT>::T* __restrict__ row,
+                                              int64_t c, int64_t K, uint32_t* to) {
+    if (c >= 0 && c + kPer <= K) {
       const uint4 a = __ldcs(reinterpret_cast<const uint4*>(row + c));
-      w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-      if constexpr (DT == 2) {
-        const uint4 b = __ldcs(reinterpret_cast<const uint4*>(row + c + 4));
-        w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
-      }
+      to[0] = a.x; to[1] = a.y; to[2] = a.z; to[3] = a.w;
     } else {
-      zero();
+      to[0] = to[1] = to[2] = to[3] = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (c + i < K) {
-          if constexpr (DT == 2) w[i] = __float_as_uint(row[c + i]);
-          else w[i / 2] |= (uint32_t)row[c + i] << (16 * (i & 1));
+      for (int i = 0; i < kPer; ++i)
+        if (c + i >= 0 && c + i < K) {
+          if constexpr (DT == 2) to[i] = __float_as_uint(row[c + i]);
+          else to[i / 2] |= (uint32_t)row[c + i] << (16 * (i & 1));
         }
     }
   }
+  __device__ __forceinline__ void load(const typename Elem<DT>::T* __restrict__ row, int64_t c,
+                                       int64_t K) {
+    shift = (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(*row));
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) word(row, c - shift + i * kPer, K, w + 4 * i);
+    next[0] = next[1] = next[2] = next[3] = 0;
+    if ((threadIdx.x & 31) == 31) word(row, c - shift + kWords * kPer, K, next);
+  }
   __device__ __forceinline__ void zero() {
+    shift = 0;
 #pragma unroll
     for (uint32_t& v : w) v = 0;
+    next[0] = next[1] = next[2] = next[3] = 0;
   }
-  // bits of the largest magnitude over the lanes of a block, as fp32: magnitudes
-  // compare as integers, and a NaN or an infinity wins
-  __device__ __forceinline__ float block_max() const {
-    uint32_t m = 0;
-    if constexpr (DT == 2) {
+  __device__ __forceinline__ Eight<DT> get() const {
+    constexpr int n = 4 * kWords;
+    uint32_t t[n + 4];
 #pragma unroll
-      for (uint32_t v : w) m = max(m, v & 0x7FFFFFFFu);
-      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-      return __uint_as_float(m);
-    } else {
+    for (int i = 0; i < n; ++i) t[i] = w[i];
 #pragma unroll
-      for (uint32_t v : w) m = max_u16x2(m, v & 0x7FFF7FFFu);
-      m = max_u16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-      m = max_u16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-      return to_float<DT>((uint16_t)max(m & 0xFFFFu, m >> 16));
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t v = __shfl_down_sync(0xFFFFFFFFu, w[i], 1);
+      t[n + i] = (threadIdx.x & 31) == 31 ? next[i] : v;
     }
-  }
-  __device__ __forceinline__ uint32_t codes(float inv) const {
-    float v[8];
+    // by 4-byte words first, then by half a word
+    const int words = DT == 2 ? shift : shift >> 1;
+    if (words & 2) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if constexpr (DT == 2) v[i] = __uint_as_float(w[i]) * inv;
-      else if constexpr (DT == 0)
-        v[i] = ((i & 1) ? bf16_hi_to_f32(w[i / 2]) : bf16_lo_to_f32(w[i / 2])) * inv;
-      else v[i] = to_float<1>((uint16_t)(w[i / 2] >> (16 * (i & 1)))) * inv;
+      for (int i = 0; i < n + 2; ++i) t[i] = t[i + 2];
     }
-    return pack8(v);
+    if (words & 1) {
+#pragma unroll
+      for (int i = 0; i < n + 1; ++i) t[i] = t[i + 1];
+    }
+    Eight<DT> e;
+#pragma unroll
+    for (int i = 0; i < n; ++i)
+      e.w[i] = DT == 2 ? t[i] : __funnelshift_r(t[i], t[i + 1], 16 * (shift & 1));
+    return e;
   }
 };
 
-// Grid: x 256-column chunks, y blocks of 8 x kRows rows, z matrices.  Rows run to the
+// Grid: x 256-column chunks, y blocks of 8 x R rows, z matrices.  Rows run to the
 // next multiple of 128 so that the padding rows' scales are written as zero.
-template <int DT>
+// WIDE: every row starts on 16 bytes.
+template <int DT, bool WIDE, int R>
 __global__ void __launch_bounds__(kThreads, 4)
     k_mx4_encode(const typename Elem<DT>::T* __restrict__ X, int64_t batch, int64_t rows,
                  int64_t rows_padded, int64_t K, int64_t ldx, uint8_t* __restrict__ codes,
@@ -118,79 +109,28 @@ __global__ void __launch_bounds__(kThreads, 4)
     const typename Elem<DT>::T* x = X + b * rows * ldx;
     uint8_t* to = codes + b * rows * cs + c / 2;
     uint8_t* sc = scales + b * rows_padded / 128 * kqs * 512;
-    for (int64_t row0 = ((int64_t)blockIdx.y * kWarps + warp) * kRows; row0 < rows_padded;
-         row0 += (int64_t)gridDim.y * kWarps * kRows) {
-      Eight<DT> v[kRows];
+    for (int64_t row0 = ((int64_t)blockIdx.y * kWarps + warp) * R; row0 < rows_padded;
+         row0 += (int64_t)gridDim.y * kWarps * R) {
+      std::conditional_t<WIDE, Eight<DT>, Shifted<DT>> in[R];
 #pragma unroll
-      for (int r = 0; r < kRows; ++r) {
-        if (row0 + r < rows) v[r].load(x + (row0 + r) * ldx, c, K);
-        else v[r].zero();
+      for (int r = 0; r < R; ++r) {
+        if (row0 + r < rows) in[r].load(x + (row0 + r) * ldx, c, K);
+        else in[r].zero();
       }
 #pragma unroll
-      for (int r = 0; r < kRows; ++r) {
+      for (int r = 0; r < R; ++r) {
         const int64_t row = row0 + r;
-        const uint32_t byte = scale_byte(v[r].block_max());
-        const uint32_t code = byte == 255u ? 0u : v[r].codes(inv_scale(byte));
+        Eight<DT> v;
+        if constexpr (WIDE) v = in[r];
+        else v = in[r].get();
+        const uint32_t byte = scale_byte(v.block_max());
+        const uint32_t code = byte == 255u ? 0u : v.codes(inv_scale(byte));
         if (row < rows && code_lane) *reinterpret_cast<uint32_t*>(to + row * cs) = code;
         // the four bytes of a 128-column tile meet in lanes 0 and 16 (blocks past the
         // matrix hold zeros, whose byte is 0)
         uint32_t q = byte | __shfl_down_sync(0xFFFFFFFFu, byte, 4) << 8;
         q |= __shfl_down_sync(0xFFFFFFFFu, q, 8) << 16;
         if (scale_lane) *reinterpret_cast<uint32_t*>(sc + scale_at(row, kq, kqs)) = q;
-      }
-    }
-  }
-}
-
-// The same for rows that do not start on 16 bytes: load i of a warp is its block i.
-template <int DT>
-__global__ void __launch_bounds__(kThreads, 4)
-    k_mx4_encode_any(const typename Elem<DT>::T* __restrict__ X, int64_t batch, int64_t rows,
-                     int64_t rows_padded, int64_t K, int64_t ldx, uint8_t* __restrict__ codes,
-                     uint8_t* __restrict__ scales, int release) {
-  if (release) grid_dep_launch();
-  constexpr int kR = 2;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t cs = code_stride(K), kqs = scale_tiles(K);
-  const int64_t c0 = (int64_t)blockIdx.x * 256;
-  for (int64_t b = blockIdx.z; b < batch; b += gridDim.z) {
-    const typename Elem<DT>::T* x = X + b * rows * ldx + c0 + lane;
-    uint8_t* to = codes + b * rows * cs + c0 / 2;
-    uint8_t* sc = scales + b * rows_padded / 128 * kqs * 512;
-    for (int64_t row0 = ((int64_t)blockIdx.y * kWarps + warp) * kR; row0 < rows_padded;
-         row0 += (int64_t)gridDim.y * kWarps * kR) {
-      float v[kR][8];
-#pragma unroll
-      for (int r = 0; r < kR; ++r)
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          v[r][i] = row0 + r < rows && c0 + 32 * i + lane < K
-                        ? to_float<DT>(__ldcs(x + (row0 + r) * ldx + 32 * i)) : 0.0f;
-#pragma unroll
-      for (int r = 0; r < kR; ++r) {
-        const int64_t row = row0 + r;
-        uint32_t word = 0, q[2] = {0, 0};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t m =
-              __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v[r][i]) & 0x7FFFFFFFu);
-          const uint32_t byte = scale_byte(__uint_as_float(m));
-          q[i / 4] |= byte << (8 * (i & 3));
-          float e[8] = {byte == 255u ? 0.0f : v[r][i] * inv_scale(byte)};
-          // the code is the low nibble of lane % 8; eight lanes make a word
-          uint32_t n = (pack8(e) & 15u) << (4 * (lane & 7));
-          n |= __shfl_xor_sync(0xFFFFFFFFu, n, 1);
-          n |= __shfl_xor_sync(0xFFFFFFFFu, n, 2);
-          n |= __shfl_xor_sync(0xFFFFFFFFu, n, 4);
-          // lane 4 i + j keeps word j of block i
-          const uint32_t mine = __shfl_sync(0xFFFFFFFFu, n, (lane & 3) * 8);
-          if (lane >> 2 == i) word = mine;
-        }
-        if (row < rows && c0 / 2 + lane * 4 < cs)
-          *reinterpret_cast<uint32_t*>(to + row * cs + lane * 4) = word;
-        if (lane < 2 && (int64_t)blockIdx.x * 2 + lane < kqs)
-          *reinterpret_cast<uint32_t*>(sc + scale_at(row, (int64_t)blockIdx.x * 2 + lane, kqs)) =
-              lane ? q[1] : q[0];
       }
     }
   }
@@ -253,18 +193,55 @@ __global__ void __launch_bounds__(kThreads, 4)
           if (c < K)
             __stcs(reinterpret_cast<uint4*>(to + row * K + c), make_uint4(v[0], v[1], v[2], v[3]));
         } else {
-          // store i: 32 neighbouring values, value `lane` of which is element lane % 8
-          // of lane 4 i + lane / 8
+          // The aligned 16-byte word that holds the lane's first value: its start comes
+          // from the lane before.  Words that are not wholly this warp's are stored
+          // value by value, and lane 31 stores the values after its word.
+          uint16_t* first = to + row * K + c;
+          const int shift = (int)((reinterpret_cast<uintptr_t>(first) & 15) / 2);
+          uint32_t t[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int src = 4 * i + (lane >> 3);
-            const uint32_t p0 = __shfl_sync(0xFFFFFFFFu, v[0], src),
-                           p1 = __shfl_sync(0xFFFFFFFFu, v[1], src),
-                           p2 = __shfl_sync(0xFFFFFFFFu, v[2], src),
-                           p3 = __shfl_sync(0xFFFFFFFFu, v[3], src);
-            const uint32_t p = lane & 4 ? (lane & 2 ? p3 : p2) : (lane & 2 ? p1 : p0);
-            if (c0 + 32 * i + lane < K)
-              to[row * K + c0 + 32 * i + lane] = (uint16_t)(lane & 1 ? p >> 16 : p);
+          for (int i = 0; i < 4; ++i) {
+            t[i] = __shfl_up_sync(0xFFFFFFFFu, v[i], 1);
+            t[4 + i] = v[i];
+          }
+          // values 8 - shift .. of the eight pairs-of-values words, shift may be 0
+          const int skip = 8 - shift;
+          uint32_t o[4];
+          {
+            uint32_t u[9];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) u[i] = t[i];
+            u[8] = 0;
+            if (skip & 8) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) u[i] = u[i + 4];
+            } else {
+              if (skip & 4) {
+#pragma unroll
+                for (int i = 0; i < 6; ++i) u[i] = u[i + 2];
+              }
+              if (skip & 2) {
+#pragma unroll
+                for (int i = 0; i < 5; ++i) u[i] = u[i + 1];
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = __funnelshift_r(u[i], u[i + 1], 16 * (skip & 1));
+          }
+          if (lane > 0 && c - shift + 8 <= K) {
+            __stcs(reinterpret_cast<uint4*>(first - shift), make_uint4(o[0], o[1], o[2], o[3]));
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int64_t at = c - shift + i;
+              if (at >= (lane > 0 ? 0 : c) && at < K)
+                first[i - shift] = (uint16_t)(o[i / 2] >> (16 * (i & 1)));
+            }
+          }
+          if (lane == 31) {
+#pragma unroll
+            for (int i = 1; i < 8; ++i)
+              if (i >= skip && c + i < K) first[i] = (uint16_t)(v[i / 2] >> (16 * (i & 1)));
           }
         }
       }
@@ -279,19 +256,13 @@ static dim3 grid_of(int64_t batch, int64_t rows, int64_t K, int rows_a_block) {
               (unsigned)(batch < 65535 ? batch : 65535));
 }
 
-template <int DT>
+template <int DT, bool WIDE, int R>
 static cudaError_t encode_as(const void* X, int64_t batch, int64_t rows, int64_t K, int64_t ldx,
                              uint8_t* codes, uint8_t* scales, int release, cudaStream_t st) {
-  using T = typename Elem<DT>::T;
-  const T* x = static_cast<const T*>(X);
   const int64_t padded = (rows + 127) / 128 * 128;
-  // 16-byte loads need every row to start on 16 bytes
-  if (aligned16(X) && (ldx * (int64_t)sizeof(T)) % 16 == 0)
-    k_mx4_encode<DT><<<grid_of(batch, padded, K, kWarps * kRows), kThreads, 0, st>>>(
-        x, batch, rows, padded, K, ldx, codes, scales, release);
-  else
-    k_mx4_encode_any<DT><<<grid_of(batch, padded, K, kWarps * 2), kThreads, 0, st>>>(
-        x, batch, rows, padded, K, ldx, codes, scales, release);
+  k_mx4_encode<DT, WIDE, R><<<grid_of(batch, padded, K, kWarps * R), kThreads, 0, st>>>(
+      static_cast<const typename Elem<DT>::T*>(X), batch, rows, padded, K, ldx, codes, scales,
+      release);
   return cudaGetLastError();
 }
 
@@ -300,9 +271,12 @@ static cudaError_t encode_as(const void* X, int64_t batch, int64_t rows, int64_t
 cudaError_t launch_mx4_encode(const void* X, int dtype, int64_t batch, int64_t rows, int64_t K,
                               int64_t ldx, uint8_t* codes, uint8_t* scales, int release,
                               cudaStream_t st) {
-  if (dtype == 0) return mx4::encode_as<0>(X, batch, rows, K, ldx, codes, scales, release, st);
-  if (dtype == 1) return mx4::encode_as<1>(X, batch, rows, K, ldx, codes, scales, release, st);
-  return mx4::encode_as<2>(X, batch, rows, K, ldx, codes, scales, release, st);
+  using namespace mx4;
+  const auto go = [&](auto f) { return f(X, batch, rows, K, ldx, codes, scales, release, st); };
+  const bool wide = aligned16(X) && (batch * rows == 1 || ldx * (dtype == 2 ? 4 : 2) % 16 == 0);
+  if (dtype == 0) return wide ? go(encode_as<0, true, kRows>) : go(encode_as<0, false, kRows>);
+  if (dtype == 1) return wide ? go(encode_as<1, true, kRows>) : go(encode_as<1, false, kRows>);
+  return wide ? go(encode_as<2, true, kRows>) : go(encode_as<2, false, 2>);
 }
 
 cudaError_t launch_mx4_decode(const uint8_t* codes, const uint8_t* scales, int64_t batch,

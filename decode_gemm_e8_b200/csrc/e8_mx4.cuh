@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cstdint>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "e8_common.cuh"
@@ -58,6 +59,85 @@ __device__ __forceinline__ uint32_t pack8(const float (&v)[8]) {
 __device__ __forceinline__ float code_value(uint32_t c) {
   return __uint_as_float(((c & 8u) << 28) | ((c & 7u) << 22)) * 0x1p126f;
 }
+
+// ------------------------------------------------------------ encoding ---
+// DT: E8_DT_* (0 bf16, 1 fp16, 2 fp32).
+template <int DT> struct Elem;
+template <> struct Elem<0> { using T = uint16_t; };
+template <> struct Elem<1> { using T = uint16_t; };
+template <> struct Elem<2> { using T = float; };
+
+template <int DT>
+__device__ __forceinline__ float to_float(typename Elem<DT>::T v) {
+  if constexpr (DT == 0) return __uint_as_float((uint32_t)v << 16);
+  else if constexpr (DT == 1) return __half2float(__ushort_as_half(v));
+  else return v;
+}
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Eight values of a row from column c on (zeros past K), as they lie in memory; one
+// lane's share of a block, four lanes a block.
+template <int DT>
+struct Eight {
+  uint32_t w[DT == 2 ? 8 : 4];
+  // wide: the row starts on 16 bytes
+  __device__ __forceinline__ void load(const typename Elem<DT>::T* __restrict__ row, int64_t c,
+                                       int64_t K, bool wide = true) {
+    if (wide && c + 8 <= K) {
+      const uint4 a = __ldcs(reinterpret_cast<const uint4*>(row + c));
+      w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+      if constexpr (DT == 2) {
+        const uint4 b = __ldcs(reinterpret_cast<const uint4*>(row + c + 4));
+        w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+      }
+    } else {
+      zero();
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (c + i < K) {
+          if constexpr (DT == 2) w[i] = __float_as_uint(row[c + i]);
+          else w[i / 2] |= (uint32_t)row[c + i] << (16 * (i & 1));
+        }
+    }
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (uint32_t& v : w) v = 0;
+  }
+  // bits of the largest magnitude over the lanes of a block, as fp32: magnitudes
+  // compare as integers, and a NaN or an infinity wins
+  __device__ __forceinline__ float block_max() const {
+    uint32_t m = 0;
+    if constexpr (DT == 2) {
+#pragma unroll
+      for (uint32_t v : w) m = max(m, v & 0x7FFFFFFFu);
+      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+      return __uint_as_float(m);
+    } else {
+#pragma unroll
+      for (uint32_t v : w) m = max_u16x2(m, v & 0x7FFF7FFFu);
+      m = max_u16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+      m = max_u16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+      return to_float<DT>((uint16_t)max(m & 0xFFFFu, m >> 16));
+    }
+  }
+  __device__ __forceinline__ uint32_t codes(float inv) const {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (DT == 2) v[i] = __uint_as_float(w[i]) * inv;
+      else if constexpr (DT == 0)
+        v[i] = ((i & 1) ? bf16_hi_to_f32(w[i / 2]) : bf16_lo_to_f32(w[i / 2])) * inv;
+      else v[i] = to_float<1>((uint16_t)(w[i / 2] >> (16 * (i & 1)))) * inv;
+    }
+    return pack8(v);
+  }
+};
 
 // ------------------------------------------------------- tensor cores ---
 // Their callers run in a branch that elect.sync chose the thread of: under any other

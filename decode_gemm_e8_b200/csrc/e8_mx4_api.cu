@@ -68,33 +68,27 @@ int e8_mx4_decode_to_bf16(const e8_codebook* cb, const uint8_t* codes, const uin
       e8::launch_mx4_decode(codes, scales, batch, rows, K, out, (cudaStream_t)stream));
 }
 
-size_t e8_mx4_gemm_codes_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-  if (!valid_shape(M, K) || !valid_shape(N, K) || M == 0 || N == 0) return 0;
-  return round256(e8::mx4_gemm_workspace(M, N, K));
-}
+// The partial sums of a split product stay in the SMs of its cluster.
+size_t e8_mx4_gemm_codes_workspace_bytes(int64_t, int64_t, int64_t) { return 0; }
 
-// [codes of X][scales of X][the workspace of e8_mx4_gemm_codes], each part on 256 bytes
+// [codes of X][scales of X], each on 256 bytes
 size_t e8_mx4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   if (!valid_shape(M, K) || !valid_shape(N, K) || M == 0 || N == 0) return 0;
-  return round256((size_t)e8_mx4_code_bytes(M, K)) + round256((size_t)e8_mx4_scale_bytes(M, K)) +
-         e8_mx4_gemm_codes_workspace_bytes(M, N, K);
+  return round256((size_t)e8_mx4_code_bytes(M, K)) + round256((size_t)e8_mx4_scale_bytes(M, K));
 }
 
 int e8_mx4_gemm_codes(const e8_codebook* cb, const uint8_t* a_codes, const uint8_t* a_scales,
                       int64_t M, const uint8_t* w_codes, const uint8_t* w_scales, int64_t N,
-                      int64_t K, uint16_t* Y, void* workspace, size_t ws_bytes, void* stream) {
+                      int64_t K, uint16_t* Y, void*, size_t, void* stream) {
   if (!cb || !valid_shape(M, K) || !valid_shape(N, K)) return E8_EINVAL;
   if (M == 0 || N == 0) return E8_OK;
   if (!a_codes || !a_scales || !w_codes || !w_scales || !Y || !aligned16(a_codes) ||
       !aligned16(a_scales) || !aligned16(w_codes) || !aligned16(w_scales) || !aligned16(Y))
     return E8_EINVAL;
-  const size_t need = e8_mx4_gemm_codes_workspace_bytes(M, N, K);
-  if (need && (!workspace || !aligned16(workspace) || ws_bytes < need)) return E8_EWORKSPACE;
   const int rc = check_device(cb);
   if (rc != E8_OK) return rc;
   return cuda_status(e8::launch_mx4_gemm(a_codes, a_scales, M, w_codes, w_scales, N, K, Y,
-                                         workspace, cb->status, cb->sm_count, 0,
-                                         (cudaStream_t)stream));
+                                         cb->status, cb->sm_count, 0, (cudaStream_t)stream));
 }
 
 int e8_mx4_gemm(const e8_codebook* cb, const void* X, int dtype, int64_t M, int64_t ldx,
@@ -111,14 +105,16 @@ int e8_mx4_gemm(const e8_codebook* cb, const void* X, int dtype, int64_t M, int6
   if (!workspace || !aligned16(workspace) || ws_bytes < need) return E8_EWORKSPACE;
   const int rc = check_device(cb);
   if (rc != E8_OK) return rc;
+  cudaStream_t st = (cudaStream_t)stream;
+  if (M <= e8::kMx4Small)
+    return cuda_status(e8::launch_mx4_gemm_small(X, dtype, M, ldx, w_codes, w_scales, N, K, Y,
+                                                 cb->status, cb->sm_count, st));
   uint8_t* codes = static_cast<uint8_t*>(workspace);
   uint8_t* scales = codes + round256((size_t)e8_mx4_code_bytes(M, K));
-  uint8_t* rest = scales + round256((size_t)e8_mx4_scale_bytes(M, K));
-  cudaStream_t st = (cudaStream_t)stream;
   if (e8::launch_mx4_encode(X, dtype, 1, M, K, ldx, codes, scales, 1, st) != cudaSuccess)
     return E8_ECUDA;
-  return cuda_status(e8::launch_mx4_gemm(codes, scales, M, w_codes, w_scales, N, K, Y, rest,
-                                         cb->status, cb->sm_count, 1, st));
+  return cuda_status(e8::launch_mx4_gemm(codes, scales, M, w_codes, w_scales, N, K, Y, cb->status,
+                                         cb->sm_count, 1, st));
 }
 
 static bool moe_shape(int64_t T, int64_t H, int64_t E, int topk, int64_t I) {

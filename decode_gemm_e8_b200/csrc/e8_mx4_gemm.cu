@@ -27,7 +27,12 @@ namespace mx4 {
 //              tensor memory (a slot of its own for each stage, so that no copy
 //              meets an MMA that still reads) and issues the MMAs
 //   warps 2-5  epilogue
-constexpr int kStreamThreads = 224;
+//   warps 2-9  with up to 8 tokens that are not encoded yet (DT >= 0), instead of warp
+//              6: each encodes the tokens of one of the 8 ring slots, every CTA for
+//              itself.  Against the encoder's launch, in us at N x K = 4096 x 4096 and
+//              14336 x 4096: 1 token 6.9 / 7.6 and 10.2 / 11.7, 8 tokens 8.2 / 8.6 and
+//              11.1 / 11.8, 16 tokens 10.0 / 9.3 and 14.1 / 11.7
+constexpr int kStreamThreads = 224, kStreamThreadsX = 320;
 constexpr int kStreamRows = 128;
 constexpr int kBK = 256;               // K of a stage: 128 bytes of codes
 constexpr int kCodeTile = 128 * 128;   // bytes of 128 rows
@@ -41,6 +46,9 @@ struct StreamArgs {
   int M, N, K;
   int bn, stages, splits;
   int early;   // the weights may be read before the preceding kernel has ended
+  const void* X;   // tokens to encode, row stride ldx; wide: its rows start on 16 bytes
+  int64_t ldx;
+  int wide;
   uint32_t* status;
 };
 
@@ -48,7 +56,8 @@ __host__ __device__ __forceinline__ int stream_stage_bytes(int bn) {
   return kCodeTile + bn * 128 + 1024 + 1024 * ((bn + 127) / 128);
 }
 
-__global__ void __launch_bounds__(kStreamThreads, 1)
+template <int DT>
+__global__ void __launch_bounds__(DT < 0 ? kStreamThreads : kStreamThreadsX, 1)
     k_mx4_stream(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA,
                  const __grid_constant__ StreamArgs a) {
   extern __shared__ uint8_t smem_raw[];
@@ -69,14 +78,14 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < a.stages; ++s) {
-      mbar_init(&full[s], 2);   // both producers
+      mbar_init(&full[s], 2);   // W's producer and the tokens'
       mbar_init(&empty[s], 1);
     }
     mbar_init(&done, 1);
     abort_flag = 0u;
     fence_mbar_init();
     tma_prefetch_desc(&tmW);
-    tma_prefetch_desc(&tmA);
+    if (DT < 0) tma_prefetch_desc(&tmA);
   }
   if (warp == 1) {
     tmem_alloc(&tmem_slot, 512);
@@ -111,7 +120,53 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         }
       }
     }
-  } else if (warp == 6) {
+  } else if (DT >= 0 && warp >= 2) {
+    if constexpr (DT >= 0) {
+      // the tokens of slot warp - 2, all rows' loads in flight before the first is encoded
+      const typename Elem<DT>::T* x = static_cast<const typename Elem<DT>::T*>(a.X);
+      const int e = warp - 2;
+      const uint32_t st = ring + (uint32_t)(e * stage_bytes) + kCodeTile;
+      uint32_t ph = 1;
+      for (int i = e; i < nkb; i += kMaxStages) {
+        const int64_t c = (int64_t)(kb0 + i) * kBK + lane * 8;
+        Eight<DT> v[kMx4Small];
+#pragma unroll
+        for (int r = 0; r < kMx4Small; ++r) {
+          if (r < a.M) v[r].load(x + r * a.ldx, c, a.K, a.wide != 0);
+          else v[r].zero();
+        }
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait_lazy(&empty[e], ph, &abort_flag, a.status,
+                                                    kDevTimeoutEmpty)))
+          break;
+        ph ^= 1u;
+#pragma unroll
+        for (int g = 0; g < kMx4Small; g += 4) {
+          if (g < a.M) {
+#pragma unroll
+            for (int r = g; r < g + 4; ++r) {
+              const uint32_t byte = scale_byte(v[r].block_max());
+              const uint32_t code = byte == 255u ? 0u : v[r].codes(inv_scale(byte));
+              uint32_t f = byte | __shfl_down_sync(0xFFFFFFFFu, byte, 4) << 8;
+              f |= __shfl_down_sync(0xFFFFFFFFu, f, 8) << 16;
+              const uint32_t at = st + (uint32_t)(r * 128 + (((lane >> 2) ^ (r & 7)) << 4)) +
+                                  (uint32_t)(lane & 3) * 4u;
+              asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(code) : "memory");
+              // the four scales of 128 columns, in lanes 0 and 16
+              if ((lane & 15) == 0)
+                asm volatile("st.shared.u32 [%0], %1;" ::"r"(
+                                 st + (uint32_t)a.bn * 128u + 1024u + (uint32_t)(lane >> 4) * 512u +
+                                 (uint32_t)r * 16u),
+                             "r"(f)
+                             : "memory");
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[e]);
+      }
+    }
+  } else if (DT < 0 && warp == 6) {
     if (a.early) grid_dep_wait();
     if (elect_one()) {
       // codes and scales of the tokens
@@ -242,10 +297,12 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   }
 }
 
-static cudaError_t launch_stream(const uint8_t* a_codes, const uint8_t* a_scales, int64_t M,
-                                 const uint8_t* w_codes, const uint8_t* w_scales, int64_t N,
-                                 int64_t K, uint16_t* Y, uint32_t* status, int sm_count, int early,
-                                 cudaStream_t st) {
+// DT < 0: encoded tokens a_codes / a_scales; else X.
+template <int DT>
+static cudaError_t launch_stream(const void* X, int64_t ldx, const uint8_t* a_codes,
+                                 const uint8_t* a_scales, int64_t M, const uint8_t* w_codes,
+                                 const uint8_t* w_scales, int64_t N, int64_t K, uint16_t* Y,
+                                 uint32_t* status, int sm_count, int early, cudaStream_t st) {
   StreamArgs a;
   a.w_scales = w_scales;
   a.a_scales = a_scales;
@@ -257,7 +314,12 @@ static cudaError_t launch_stream(const uint8_t* a_codes, const uint8_t* a_scales
   a.bn = M >= 256 ? 256 : (int)((M + 15) / 16 * 16);
   a.stages = kStreamSmem / stream_stage_bytes(a.bn);
   if (a.stages > kMaxStages) a.stages = kMaxStages;
+  // (slot e's tokens are warp 2 + e's)
+  static_assert(kMx4Small <= 16 && kStreamSmem / (kCodeTile + 16 * 128 + 2048) >= kMaxStages, "");
   a.early = early;
+  a.X = X;
+  a.ldx = ldx;
+  a.wide = aligned16(X) && (M == 1 || (ldx * (DT == 2 ? 4 : 2)) % 16 == 0);
   a.status = status;
   const int64_t tiles_n = (N + kStreamRows - 1) / kStreamRows, tiles_m = (M + a.bn - 1) / a.bn;
   const int kblocks = (int)((K + kBK - 1) / kBK);
@@ -266,17 +328,17 @@ static cudaError_t launch_stream(const uint8_t* a_codes, const uint8_t* a_scales
   a.splits = S;
   if (tiles_m > 65535 || tiles_n * S > INT32_MAX) return cudaErrorInvalidValue;
   const int64_t cs = code_stride(K);
-  CUtensorMap tw, ta;
+  CUtensorMap tw, ta = {};
   if (!make_tmap_2d(&tw, w_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)N, (uint64_t)cs, 128,
                     128, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !make_tmap_2d(&ta, a_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)M, (uint64_t)cs,
-                    (uint32_t)a.bn, 128, CU_TENSOR_MAP_SWIZZLE_128B))
+      (DT < 0 && !make_tmap_2d(&ta, a_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)M,
+                               (uint64_t)cs, (uint32_t)a.bn, 128, CU_TENSOR_MAP_SWIZZLE_128B)))
     return cudaErrorInvalidValue;
-  cudaError_t e = ensure_smem_limit(k_mx4_stream, kMaxDynSmem);
+  cudaError_t e = ensure_smem_limit(k_mx4_stream<DT>, kMaxDynSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles_n * S), (unsigned)tiles_m);
-  cfg.blockDim = dim3(kStreamThreads);
+  cfg.blockDim = dim3(DT < 0 ? kStreamThreads : kStreamThreadsX);
   cfg.dynamicSmemBytes = 1024 + (size_t)a.stages * stream_stage_bytes(a.bn);
   // room for the partial tile of a split product
   const size_t part = 1024 + (size_t)a.bn * 512;
@@ -291,7 +353,7 @@ static cudaError_t launch_stream(const uint8_t* a_codes, const uint8_t* a_scales
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = early ? 2 : 1;
-  e = cudaLaunchKernelEx(&cfg, k_mx4_stream, tw, ta, a);
+  e = cudaLaunchKernelEx(&cfg, k_mx4_stream<DT>, tw, ta, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -633,22 +695,30 @@ static cudaError_t launch_pair(const uint8_t* a_codes, const uint8_t* a_scales, 
 
 cudaError_t launch_mx4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int64_t M,
                             const uint8_t* w_codes, const uint8_t* w_scales, int64_t N, int64_t K,
-                            uint16_t* Y, void* ws, uint32_t* status, int sm_count, int early,
+                            uint16_t* Y, uint32_t* status, int sm_count, int early,
                             cudaStream_t st) {
-  (void)ws;
   // The pair kernel where its 256 x 192 tiles occupy at least a quarter of the SM pairs.
   const int64_t tiles = ((M + 255) / 256) * ((N + 191) / 192);
   const int64_t scale_rows = ((M > N ? M : N) + 127) / 128 * mx4::scale_tiles(K);
   if (M > 256 && tiles * 8 >= sm_count && scale_rows <= INT32_MAX)
     return mx4::launch_pair(a_codes, a_scales, M, w_codes, w_scales, N, K, Y, status, sm_count,
                             early, st);
-  return mx4::launch_stream(a_codes, a_scales, M, w_codes, w_scales, N, K, Y, status, sm_count,
-                            early, st);
+  return mx4::launch_stream<-1>(nullptr, 0, a_codes, a_scales, M, w_codes, w_scales, N, K, Y,
+                                status, sm_count, early, st);
 }
 
-size_t mx4_gemm_workspace(int64_t M, int64_t N, int64_t K) {
-  (void)M; (void)N; (void)K;
-  return 0;
+cudaError_t launch_mx4_gemm_small(const void* X, int dtype, int64_t M, int64_t ldx,
+                                  const uint8_t* w_codes, const uint8_t* w_scales, int64_t N,
+                                  int64_t K, uint16_t* Y, uint32_t* status, int sm_count,
+                                  cudaStream_t st) {
+  if (dtype == 0)
+    return mx4::launch_stream<0>(X, ldx, nullptr, nullptr, M, w_codes, w_scales, N, K, Y, status,
+                                 sm_count, 0, st);
+  if (dtype == 1)
+    return mx4::launch_stream<1>(X, ldx, nullptr, nullptr, M, w_codes, w_scales, N, K, Y, status,
+                                 sm_count, 0, st);
+  return mx4::launch_stream<2>(X, ldx, nullptr, nullptr, M, w_codes, w_scales, N, K, Y, status,
+                               sm_count, 0, st);
 }
 
 }  // namespace e8

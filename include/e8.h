@@ -432,23 +432,25 @@ int e8_mx4_decode_to_bf16(const e8_codebook* cb, const uint8_t* codes, const uin
                           int64_t batch, int64_t rows, int64_t K, uint16_t* out, void* stream);
 
 /* Product of two encoded matrices: Y bf16 [M][N] = bf16_rne(sum_k A[m][k] W[n][k]),
- * products exact, sums in fp32, for A [M][K] and W [N][K] in the form above.
- * workspace: at least e8_mx4_gemm_codes_workspace_bytes(M, N, K) bytes, contents
- * ignored; the K range of an output may be split, its partial sums are added in
- * a fixed order (results do not vary from run to run). */
+ * products exact, sums in fp32, for A [M][K] and W [N][K] in the form above.  The K
+ * range of an output may be split, its partial sums are added in a fixed order
+ * (results do not vary from run to run).  workspace: at least
+ * e8_mx4_gemm_codes_workspace_bytes(M, N, K) bytes, which is 0 (NULL is fine). */
 int e8_mx4_gemm_codes(const e8_codebook* cb, const uint8_t* a_codes, const uint8_t* a_scales,
                       int64_t M, const uint8_t* w_codes, const uint8_t* w_scales, int64_t N,
                       int64_t K, uint16_t* Y, void* workspace, size_t ws_bytes, void* stream);
 
-/* The same for activations X [M][K] of type dtype, row stride ldx >= K elements,
- * which are encoded into the workspace first (16-byte aligned or not).
- * workspace: at least e8_mx4_gemm_workspace_bytes(M, N, K) bytes. */
+/* The same for activations X [M][K] of type dtype, row stride ldx >= K elements
+ * (16-byte aligned rows or not), which are encoded on the way: into the workspace, or
+ * for M <= 8 inside the product.  workspace: at least
+ * e8_mx4_gemm_workspace_bytes(M, N, K) bytes at every M, contents ignored; not to be
+ * used by other work until the stream has passed this call. */
 int e8_mx4_gemm(const e8_codebook* cb, const void* X, int dtype, int64_t M, int64_t ldx,
                 const uint8_t* w_codes, const uint8_t* w_scales, int64_t N, int64_t K,
                 uint16_t* Y, void* workspace, size_t ws_bytes, void* stream);
 
-/* Workspace bytes of the two products (0 if the arguments are invalid or
- * nothing is needed). */
+/* Workspace bytes of the two products (0 if the arguments are invalid or nothing is
+ * needed). */
 size_t e8_mx4_gemm_codes_workspace_bytes(int64_t M, int64_t N, int64_t K);
 size_t e8_mx4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
