@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ SharedLists lists;
   __shared__ Unit units[kSlots];
   __shared__ uint64_t unit_full[kSlots], unit_empty[kSlots], told_full[2], told_empty[2];
-  __shared__ uint64_t weights_took;
+  __shared__ uint64_t weights_took[2];   // units by parity: two may be taken between looks
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drain;
   __shared__ uint32_t tmem_slot;
   __shared__ volatile uint32_t abort_flag;
@@ -508,7 +508,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&told_full[i], 4);
       mbar_init(&told_empty[i], 1);
     }
-    mbar_init(&weights_took, 1);
+    mbar_init(&weights_took[0], 1);
+    mbar_init(&weights_took[1], 1);
     mbar_init(&drain, 1);
     abort_flag = 0u;
     fence_mbar_init();
@@ -612,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int per_down = down_tiles * g.down_parts, n_down = n_up + nact * per_down;
       const int n_all = n_down + down_tiles * ((g.T + 3) / 4);
       int s = 0, ahead = 0;
-      uint32_t ph = 1, took_ph = 0;
+      uint32_t ph = 1, took = 0;   // units waited for: barrier in bit 0, phase in bit 1
       for (;;) {
         Unit u = {};
         u.kind = claim < n_up ? kUp : claim < n_down ? kDown : claim < n_all ? kSum : kEnd;
@@ -671,9 +672,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (u.kind < kSum && u.nk <= 8 && ahead == 0) {
           ahead = 1;
         } else {
-          if (!mbar_wait_lazy(&weights_took, took_ph, &abort_flag, g.status, kDevTimeoutEmpty))
+          if (!mbar_wait_lazy(&weights_took[took & 1u], took >> 1 & 1u, &abort_flag, g.status,
+                              kDevTimeoutEmpty))
             break;
-          took_ph ^= 1u;
+          ++took;
         }
         claim = atomicAdd(g.claimed, 1);
       }
@@ -684,8 +686,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       int s = 0;
       bool ok = true;
       Unit u;
-      while (ok && take(u)) {
-        mbar_arrive(&weights_took);
+      for (uint32_t i = 0; ok && take(u); ++i) {
+        mbar_arrive(&weights_took[i & 1u]);
         if (u.kind == kSum) continue;
         const bool down = u.kind == kDown;
         const int kqs = (down ? g.I : g.H) / kBK;
