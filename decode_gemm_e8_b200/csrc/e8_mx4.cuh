@@ -79,21 +79,32 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 // Eight values of a row from column c on (zeros past K), as they lie in memory; one
 // lane's share of a block, four lanes a block.
 template <int DT>
 struct Eight {
+  using T = typename Elem<DT>::T;
   uint32_t w[DT == 2 ? 8 : 4];
+  // all eight there, on 16 bytes
+  __device__ __forceinline__ void load(const T* __restrict__ at) {
+    const uint4 a = __ldcs(reinterpret_cast<const uint4*>(at));
+    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+    if constexpr (DT == 2) {
+      const uint4 b = __ldcs(reinterpret_cast<const uint4*>(at + 4));
+      w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+    }
+  }
   // wide: the row starts on 16 bytes
-  __device__ __forceinline__ void load(const typename Elem<DT>::T* __restrict__ row, int64_t c,
-                                       int64_t K, bool wide = true) {
+  __device__ __forceinline__ void load(const T* __restrict__ row, int64_t c, int64_t K,
+                                       bool wide = true) {
     if (wide && c + 8 <= K) {
-      const uint4 a = __ldcs(reinterpret_cast<const uint4*>(row + c));
-      w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-      if constexpr (DT == 2) {
-        const uint4 b = __ldcs(reinterpret_cast<const uint4*>(row + c + 4));
-        w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
-      }
+      load(row + c);
     } else {
       zero();
 #pragma unroll
@@ -108,34 +119,43 @@ struct Eight {
 #pragma unroll
     for (uint32_t& v : w) v = 0;
   }
-  // bits of the largest magnitude over the lanes of a block, as fp32: magnitudes
-  // compare as integers, and a NaN or an infinity wins
-  __device__ __forceinline__ float block_max() const {
+  // The block's scale byte, over its four lanes: magnitudes compare as integers, and a
+  // NaN or an infinity wins.
+  __device__ __forceinline__ uint32_t block_byte() const {
     uint32_t m = 0;
     if constexpr (DT == 2) {
 #pragma unroll
       for (uint32_t v : w) m = max(m, v & 0x7FFFFFFFu);
-      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-      return __uint_as_float(m);
     } else {
 #pragma unroll
       for (uint32_t v : w) m = max_u16x2(m, v & 0x7FFF7FFFu);
-      m = max_u16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-      m = max_u16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-      return to_float<DT>((uint16_t)max(m & 0xFFFFu, m >> 16));
+      m = max(m & 0xFFFFu, m >> 16);
     }
+    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+    return scale_byte(DT == 2 ? __uint_as_float(m) : to_float<DT == 2 ? 0 : DT>((uint16_t)m));
   }
-  __device__ __forceinline__ uint32_t codes(float inv) const {
+  // The codes under a scale byte (zeros under 255).  bf16 values are scaled as pairs in
+  // bf16: exactly, but for results below 2^-126, which are code 0 either way.
+  __device__ __forceinline__ uint32_t codes(uint32_t byte) const {
     float v[8];
+    if constexpr (DT == 0) {
+      const uint32_t inv = (254u - byte) * 0x00800080u;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if constexpr (DT == 2) v[i] = __uint_as_float(w[i]) * inv;
-      else if constexpr (DT == 0)
-        v[i] = ((i & 1) ? bf16_hi_to_f32(w[i / 2]) : bf16_lo_to_f32(w[i / 2])) * inv;
-      else v[i] = to_float<1>((uint16_t)(w[i / 2] >> (16 * (i & 1)))) * inv;
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t p = mul_bf16x2(w[i], inv);
+        v[2 * i] = bf16_lo_to_f32(p);
+        v[2 * i + 1] = bf16_hi_to_f32(p);
+      }
+    } else {
+      const float inv = inv_scale(byte);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        v[i] = (DT == 2 ? __uint_as_float(w[i % (DT == 2 ? 8 : 4)])
+                        : to_float<1>((uint16_t)(w[i / 2] >> (16 * (i & 1))))) * inv;
     }
-    return pack8(v);
+    const uint32_t c = pack8(v);
+    return byte == 255u ? 0u : c;
   }
 };
 

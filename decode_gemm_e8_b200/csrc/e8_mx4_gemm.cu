@@ -144,8 +144,7 @@ __global__ void __launch_bounds__(DT < 0 ? kStreamThreads : kStreamThreadsX, 1)
           if (g < a.M) {
 #pragma unroll
             for (int r = g; r < g + 4; ++r) {
-              const uint32_t byte = scale_byte(v[r].block_max());
-              const uint32_t code = byte == 255u ? 0u : v[r].codes(inv_scale(byte));
+              const uint32_t byte = v[r].block_byte(), code = v[r].codes(byte);
               uint32_t f = byte | __shfl_down_sync(0xFFFFFFFFu, byte, 4) << 8;
               f |= __shfl_down_sync(0xFFFFFFFFu, f, 8) << 16;
               const uint32_t at = st + (uint32_t)(r * 128 + (((lane >> 2) ^ (r & 7)) << 4)) +
@@ -276,13 +275,34 @@ __global__ void __launch_bounds__(DT < 0 ? kStreamThreads : kStreamThreadsX, 1)
     }
     cluster_arrive();
     cluster_wait();
-    const int row = (int)threadIdx.x;
-    if (row < kStreamRows && n0 + row < a.N) {
-      for (int c = rank; c < cols; c += S) {
-        const uint32_t at = smem_u32(part + c * 128 + row);
-        float y = ld_shared_cluster_f32(mapa_shared(at, 0));
-        for (int p = 1; p < S; ++p) y += ld_shared_cluster_f32(mapa_shared(at, (uint32_t)p));
-        a.Y[(size_t)(m0 + c) * a.N + n0 + row] = (uint16_t)(pack_bf16x2(y, 0.0f) & 0xFFFFu);
+    // a warp a column, four rows a lane; the loads of two columns in flight
+    const int n = n0 + lane * 4, warps = (int)(blockDim.x >> 5);
+    const bool four = (a.N & 3) == 0;   // (Y starts on 16 bytes)
+#pragma unroll 2
+    for (int c = rank + warp * S; c < cols; c += warps * S) {
+      const uint32_t at = smem_u32(part + c * 128 + lane * 4);
+      float4 v[8];
+#pragma unroll
+      for (int p = 0; p < 8; ++p)
+        if (p < S) v[p] = ld_shared_cluster_v4(mapa_shared(at, (uint32_t)p));
+      float4 y = v[0];
+#pragma unroll
+      for (int p = 1; p < 8; ++p)
+        if (p < S) {
+          y.x += v[p].x;
+          y.y += v[p].y;
+          y.z += v[p].z;
+          y.w += v[p].w;
+        }
+      const uint32_t lo = pack_bf16x2(y.x, y.y), hi = pack_bf16x2(y.z, y.w);
+      uint16_t* to = a.Y + (size_t)(m0 + c) * a.N + n;
+      if (four) {
+        if (n < a.N) *reinterpret_cast<uint2*>(to) = make_uint2(lo, hi);
+      } else {
+        if (n < a.N) to[0] = (uint16_t)lo;
+        if (n + 1 < a.N) to[1] = (uint16_t)(lo >> 16);
+        if (n + 2 < a.N) to[2] = (uint16_t)hi;
+        if (n + 3 < a.N) to[3] = (uint16_t)(hi >> 16);
       }
     }
     __syncwarp();
@@ -693,14 +713,18 @@ static cudaError_t launch_pair(const uint8_t* a_codes, const uint8_t* a_scales, 
 
 }  // namespace mx4
 
+// Tokens above which the pair kernel takes over.  In us, stream / pair, at N x K =
+// 4096 x 4096, 14336 x 4096 and 4096 x 14336: 128 tokens 9.1 / 10.7, 13.5 / 16.6 and
+// 12.5 / 22.2; 256 tokens 12.0 / 10.7, 18.6 / 16.8 and 16.6 / 22.2; 257 tokens 14.0 /
+// 10.7, 25.4 / 20.3 and 21.5 / 22.0.
+constexpr int kPairFrom = 256;
+
 cudaError_t launch_mx4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int64_t M,
                             const uint8_t* w_codes, const uint8_t* w_scales, int64_t N, int64_t K,
                             uint16_t* Y, uint32_t* status, int sm_count, int early,
                             cudaStream_t st) {
-  // The pair kernel where its 256 x 192 tiles occupy at least a quarter of the SM pairs.
-  const int64_t tiles = ((M + 255) / 256) * ((N + 191) / 192);
   const int64_t scale_rows = ((M > N ? M : N) + 127) / 128 * mx4::scale_tiles(K);
-  if (M > 256 && tiles * 8 >= sm_count && scale_rows <= INT32_MAX)
+  if (M > kPairFrom && scale_rows <= INT32_MAX / 2)
     return mx4::launch_pair(a_codes, a_scales, M, w_codes, w_scales, N, K, Y, status, sm_count,
                             early, st);
   return mx4::launch_stream<-1>(nullptr, 0, a_codes, a_scales, M, w_codes, w_scales, N, K, Y,

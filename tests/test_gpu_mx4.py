@@ -184,3 +184,80 @@ def test_streams_and_graph(cbk):
         ref = e8.e8_mx4_gemm(cbk, static, w)
         assert torch.equal(y, ref)
         assert torch.equal(z, e8.e8_mx4_decode_to_bf16(cbk, e8.e8_mx4_encode(cbk, ref)))
+
+
+@pytest.mark.parametrize("M,N,K", [(300, 8000, 100), (512, 5120, 320), (1000, 5000, 1000), (700, 16, 544),
+                                   (260, 8, 33), (2049, 768, 130), (9, 2048, 8200), (8, 2050, 4100),
+                                   (3, 130, 2049), (256, 1024, 2304)])
+def test_product_tiles_and_tails(cbk, M, N, K):
+    """Many tiles and few, columns that end inside one, K tails of one to four 64-column steps."""
+    x, v = _data(M, K, "bf16", M + N, pad=(M % 2) * 8)
+    w, wv = _data(N, K, "bf16", K)
+    m = e8.e8_mx4_encode(cbk, w)
+    buf = torch.full((M * N + 64,), 7.0, dtype=torch.bfloat16, device=dev())
+    Y = buf[:M * N].view(M, N)
+    e8.e8_mx4_gemm(cbk, x, m, Y=Y)
+    _check_product(Y, mx.roundtrip(v), mx.roundtrip(wv))
+    assert (buf[M * N:] == 7).all()
+    assert torch.equal(Y, e8.e8_mx4_gemm_codes(cbk, e8.e8_mx4_encode(cbk, x), m))
+    assert e8.e8_sync_status(cbk) == e8.E8_OK
+
+
+@pytest.mark.parametrize("M", [1, 5, 8, 9, 40, 300])
+def test_nan_and_unaligned_tokens_at_every_size(cbk, M):
+    K, N = 1000, 200
+    x, _ = _data(M, K + 3, "f16", M)
+    x[M - 1, 500] = float("nan")
+    w, _ = _data(N, K, "f32", 2)
+    w[9, 3] = float("inf")
+    part = x[:, 3:]                                   # rows start anywhere
+    Y = e8.e8_mx4_gemm(cbk, part, e8.e8_mx4_encode(cbk, w))
+    _check_product(Y, mx.roundtrip(part.cpu().double().numpy()), mx.roundtrip(w.cpu().double().numpy()))
+    assert Y[M - 1].isnan().all() and Y[:, 9].isnan().all()
+
+
+def test_products_on_two_streams_and_in_two_graphs(cbk):
+    x = [_data(M, 1024, "bf16", M)[0] for M in (4, 50, 400)]
+    m = e8.e8_mx4_encode(cbk, _data(1500, 1024, "bf16", 1)[0])
+    want = [e8.e8_mx4_gemm(cbk, v, m) for v in x]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(20):
+        for s in streams:
+            got.append([e8.e8_mx4_gemm(cbk, v, m, stream=s) for v in x])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for ys in got for a, b in zip(ys, want))
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            ys = [e8.e8_mx4_gemm(cbk, v, m) for v in x]
+        graphs.append((g, ys))
+    for (g, ys), s in zip(graphs, streams):
+        with torch.cuda.stream(s):
+            for _ in range(20):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for _, ys in graphs for a, b in zip(ys, want))
+    assert e8.e8_sync_status(cbk) == e8.E8_OK
+
+
+@pytest.mark.parametrize("rows,K", [(5, 8), (9, 31), (130, 241), (33, 248), (40, 249), (7, 255), (70, 257), (12, 263),
+                                    (3, 497), (200, 1000), (600, 1032)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("off", [0, 1, 2, 3, 5])
+def test_rows_at_any_alignment(cbk, rows, K, dtype, off):
+    """Rows that start at every place of a 16-byte word, values there and back, nothing
+    written behind the last row."""
+    t = dict(bf16=torch.bfloat16, f16=torch.float16, f32=torch.float32)[dtype]
+    flat = torch.randn(rows * K + off, device=dev(), generator=torch.Generator(device="cuda").manual_seed(K)).to(t)
+    x = flat[off:].view(rows, K)
+    m = e8.e8_mx4_encode(cbk, x)
+    want = e8.e8_mx4_encode(cbk, torch.cat([x, x.new_zeros(rows, -K % 8)], 1)[:, :K])   # rows on 16 bytes
+    assert torch.equal(m.codes, want.codes) and torch.equal(m.scales, want.scales)
+    buf = torch.full((rows * K + 64,), 7.0, dtype=torch.bfloat16, device=dev())
+    e8.e8_mx4_decode_to_bf16(cbk, m, out=buf[:rows * K].view(rows, K))
+    assert np.array_equal(buf[:rows * K].view(rows, K).float().cpu().numpy(),
+                          mx.roundtrip(x.cpu().double().numpy()).astype(np.float32))
+    assert (buf[rows * K:] == 7).all()
