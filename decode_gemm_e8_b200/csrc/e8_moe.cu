@@ -867,13 +867,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int col = u.tile * kRows + lane * 4;
             const float* at = g.part_down + (size_t)t * g.topk * g.H + col;
             float4 y = make_float4(0, 0, 0, 0);
-            for (int p = 0; p < g.down_parts; ++p) {
-#pragma unroll 8
-              for (int c = 0; c < g.topk; ++c) {
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(at + (size_t)c * g.H));
-                y.x += v.x; y.y += v.y; y.z += v.z; y.w += v.w;
+            // (eight loads under way at a time, added in the order of parts and choices)
+            const int terms = g.down_parts * g.topk;
+            int c = 0;
+            for (int i = 0; i < terms; i += 8) {
+              float4 v[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                v[k] = i + k < terms ? __ldcg(reinterpret_cast<const float4*>(at))
+                                     : make_float4(0, 0, 0, 0);
+                const bool wrap = ++c == g.topk;
+                at += (size_t)(wrap ? slots - g.topk + 1 : 1) * g.H;
+                if (wrap) c = 0;
               }
-              at += (size_t)slots * g.H;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                y.x += v[k].x; y.y += v[k].y; y.z += v[k].z; y.w += v[k].w;
+              }
             }
             *reinterpret_cast<uint2*>(g.Y + (size_t)t * g.H + col) =
                 make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
@@ -940,15 +950,19 @@ __global__ void __launch_bounds__(kThreads, 1)
               p1 = *reinterpret_cast<const float4*>(&stage_v[et / 16][q * 8 + 4]);
             } else if (mine) {
               const float* at = part + (size_t)j * kRows + q * 8;
+              float4 a[kMaxUpParts], b[kMaxUpParts];
 #pragma unroll
               for (int p = 0; p < kMaxUpParts; ++p) {
-                if (p < parts) {
-                  const float4 a = __ldcg(reinterpret_cast<const float4*>(at));
-                  const float4 b = __ldcg(reinterpret_cast<const float4*>(at + 4));
-                  p0.x += a.x; p0.y += a.y; p0.z += a.z; p0.w += a.w;
-                  p1.x += b.x; p1.y += b.y; p1.z += b.z; p1.w += b.w;
-                }
+                const bool in = p < parts;
+                a[p] = in ? __ldcg(reinterpret_cast<const float4*>(at)) : make_float4(0, 0, 0, 0);
+                b[p] = in ? __ldcg(reinterpret_cast<const float4*>(at + 4))
+                          : make_float4(0, 0, 0, 0);
                 at += (size_t)g.T * kRows;
+              }
+#pragma unroll
+              for (int p = 0; p < kMaxUpParts; ++p) {
+                p0.x += a[p].x; p0.y += a[p].y; p0.z += a[p].z; p0.w += a[p].w;
+                p1.x += b[p].x; p1.y += b[p].y; p1.z += b[p].z; p1.w += b[p].w;
               }
             }
             const float x = mine ? token_scale[lists.token[u.off + j]] : 0.0f;
