@@ -1092,37 +1092,15 @@ static Layout layout(int64_t T, int64_t H, int64_t E, int topk, int64_t I) {
 // 4-bit rows unpacked to 16 bytes for each 16 values on the way to shared memory
 // (row length and start a multiple of 128 values).
 static bool weights_map(CUtensorMap* map, const uint8_t* base, uint64_t rows, uint64_t K) {
-  // one matrix's map depends on these arguments alone; the last few are kept
-  struct Entry {
-    const void* base;
-    uint64_t rows, K;
-    CUtensorMap map;
-  };
-  constexpr int kEntries = 64;
-  thread_local Entry cache[kEntries];
-  thread_local int used = 0, next = 0;
-  for (int i = 0; i < used; ++i)
-    if (cache[i].base == base && cache[i].rows == rows && cache[i].K == K) {
-      *map = cache[i].map;
-      return true;
-    }
   EncodeTiledFn fn = encode_tiled_fn();
   if (!fn) return false;
   cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
   cuuint64_t strides[1] = {(cuuint64_t)(K / 2)};
   cuuint32_t box[2] = {128, (cuuint32_t)kRows};
   cuuint32_t estr[2] = {1, 1};
-  if (fn(map, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 2, const_cast<uint8_t*>(base), dims, strides,
-         box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-    return false;
-  cache[next].base = base;
-  cache[next].rows = rows;
-  cache[next].K = K;
-  cache[next].map = *map;
-  next = (next + 1) % kEntries;
-  if (used < kEntries) ++used;
-  return true;
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 2, const_cast<uint8_t*>(base), dims,
+            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace moe

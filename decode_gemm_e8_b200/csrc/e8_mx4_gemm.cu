@@ -349,9 +349,9 @@ static cudaError_t launch_stream(const void* X, int64_t ldx, const uint8_t* a_co
   if (tiles_m > 65535 || tiles_n * S > INT32_MAX) return cudaErrorInvalidValue;
   const int64_t cs = code_stride(K);
   CUtensorMap tw, ta = {};
-  if (!make_tmap_2d(&tw, w_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)N, (uint64_t)cs, 128,
+  if (!encode_tmap_2d(&tw, w_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)N, (uint64_t)cs, 128,
                     128, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      (DT < 0 && !make_tmap_2d(&ta, a_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)M,
+      (DT < 0 && !encode_tmap_2d(&ta, a_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)M,
                                (uint64_t)cs, (uint32_t)a.bn, 128, CU_TENSOR_MAP_SWIZZLE_128B)))
     return cudaErrorInvalidValue;
   cudaError_t e = ensure_smem_limit(k_mx4_stream<DT>, kMaxDynSmem);
@@ -644,7 +644,7 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
 
 // A map of [rows][row_bytes] bytes as 32-bit words: the scale tiles, 512 bytes each.
 static bool scale_map(CUtensorMap* map, const uint8_t* scales, int64_t rows, int64_t K) {
-  return make_tmap_2d(map, scales, CU_TENSOR_MAP_DATA_TYPE_INT32, 4,
+  return encode_tmap_2d(map, scales, CU_TENSOR_MAP_DATA_TYPE_INT32, 4,
                       (uint64_t)((rows + 127) / 128 * scale_tiles(K)), 128, 2, 128,
                       CU_TENSOR_MAP_SWIZZLE_NONE);
 }
@@ -679,12 +679,12 @@ static cudaError_t launch_pair(const uint8_t* a_codes, const uint8_t* a_scales, 
   a.status = status;
   const uint64_t cs = (uint64_t)code_stride(K);
   CUtensorMap ta, tw, tas, tws, ty = {};
-  if (!make_tmap_2d(&ta, a_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)M, cs, 64, 128,
+  if (!encode_tmap_2d(&ta, a_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)M, cs, 64, 128,
                     CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !make_tmap_2d(&tw, w_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)N, cs, kN / 2, 128,
+      !encode_tmap_2d(&tw, w_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)N, cs, kN / 2, 128,
                     CU_TENSOR_MAP_SWIZZLE_128B) ||
       !scale_map(&tas, a_scales, M, K) || !scale_map(&tws, w_scales, N, K) ||
-      ((N & 7) == 0 && !make_tmap_2d(&ty, Y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, (uint64_t)M,
+      ((N & 7) == 0 && !encode_tmap_2d(&ty, Y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, (uint64_t)M,
                                      (uint64_t)N, 32, 64, CU_TENSOR_MAP_SWIZZLE_128B)))
     return cudaErrorInvalidValue;
   cudaError_t e = ensure_smem_limit(k_mx4_pair, kMaxDynSmem);

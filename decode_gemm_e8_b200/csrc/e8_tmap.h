@@ -31,6 +31,21 @@ inline EncodeTiledFn encode_tiled_fn() {
 
 // Row-major [rows][cols] tensor of `elem_bytes`-byte elements; box = [box_rows][box_cols].
 // Returns false if the driver rejects the description.
+inline bool encode_tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType dtype,
+                           int elem_bytes, uint64_t rows, uint64_t cols, uint32_t box_rows,
+                           uint32_t box_cols, CUtensorMapSwizzle swizzle) {
+  EncodeTiledFn fn = encode_tiled_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)(cols * (uint64_t)elem_bytes)};
+  cuuint32_t box[2] = {box_cols, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(map, dtype, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The same for launches of a layer loop.
 // A map depends only on these arguments, so the last few encodings of each
 // host thread are kept and reused (the steady state of a layer loop encodes
 // nothing).
@@ -56,16 +71,8 @@ inline bool make_tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType
       return true;
     }
   }
-  EncodeTiledFn fn = encode_tiled_fn();
-  if (!fn) return false;
-  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)(cols * (uint64_t)elem_bytes)};
-  cuuint32_t box[2] = {box_cols, box_rows};
-  cuuint32_t estr[2] = {1, 1};
-  CUresult r = fn(map, dtype, 2, const_cast<void*>(base), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return false;
+  if (!encode_tmap_2d(map, base, dtype, elem_bytes, rows, cols, box_rows, box_cols, swizzle))
+    return false;
   Entry& e = cache[next];
   e.base = base;
   e.rows = rows;
