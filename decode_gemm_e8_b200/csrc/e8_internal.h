@@ -224,8 +224,8 @@ cudaError_t launch_ep_decode(const uint16_t* words, int64_t n_words, const uint3
 // the next kernel of the stream, launched programmatically, may start at once;
 // early: the weights may be read before the preceding kernel has ended.
 cudaError_t launch_mx4_encode(const void* X, int dtype, int64_t batch, int64_t rows, int64_t K,
-                              int64_t ldx, uint8_t* codes, uint8_t* scales, int release,
-                              int sm_count, cudaStream_t st);
+                              int64_t ldx, uint8_t* codes, uint8_t* scales, int sm_count,
+                              cudaStream_t st);
 cudaError_t launch_mx4_decode(const uint8_t* codes, const uint8_t* scales, int64_t batch,
                               int64_t rows, int64_t K, uint16_t* out, cudaStream_t st);
 cudaError_t launch_mx4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int64_t M,

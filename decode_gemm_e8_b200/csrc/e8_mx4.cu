@@ -137,9 +137,10 @@ template <int DT, bool WIDE, int R>
 __global__ void __launch_bounds__(kThreads, 4)
     k_mx4_encode(const typename Elem<DT>::T* __restrict__ X, int64_t batch, int64_t rows,
                  int64_t rows_padded, int64_t K, int64_t ldx, uint8_t* __restrict__ codes,
-                 uint8_t* __restrict__ scales, int release) {
+                 uint8_t* __restrict__ scales) {
   static_assert(32 % R == 0, "R rows are in one group of 32");
-  if (release) grid_dep_launch();
+  grid_dep_wait();
+  grid_dep_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t cs = code_stride(K), kqs = scale_tiles(K);
   const int64_t c0 = (int64_t)blockIdx.x * 256, c = c0 + lane * 8;
@@ -197,6 +198,8 @@ __global__ void __launch_bounds__(kThreads, 4)
                  int64_t batch, int64_t rows, int64_t K, uint16_t* __restrict__ out) {
   constexpr int kRows = kDecodeRows<VEC>;
   static_assert(32 % kRows == 0, "the rows are in one group of 32");
+  grid_dep_wait();
+  grid_dep_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t cs = code_stride(K), kqs = scale_tiles(K), sb = scale_bytes(rows, K);
   const int64_t c = (int64_t)blockIdx.x * kDecodeColumns<VEC> + (VEC ? lane : lane - 1) * 8;
@@ -275,21 +278,21 @@ static dim3 grid_of(int64_t batch, int64_t rows, int64_t chunks, int rows_a_bloc
 
 template <int DT, bool WIDE, int R>
 static cudaError_t encode_as(const void* X, int64_t batch, int64_t rows, int64_t K, int64_t ldx,
-                             uint8_t* codes, uint8_t* scales, int release, cudaStream_t st) {
+                             uint8_t* codes, uint8_t* scales, cudaStream_t st) {
   const int64_t padded = (rows + 127) / 128 * 128;
-  k_mx4_encode<DT, WIDE, R><<<grid_of(batch, padded, (K + 255) / 256, kWarps * R), kThreads, 0, st>>>(
-      static_cast<const typename Elem<DT>::T*>(X), batch, rows, padded, K, ldx, codes, scales,
-      release);
-  return cudaGetLastError();
+  return launch_after(k_mx4_encode<DT, WIDE, R>,
+                      grid_of(batch, padded, (K + 255) / 256, kWarps * R), dim3(kThreads), 0, st,
+                      static_cast<const typename Elem<DT>::T*>(X), batch, rows, padded, K, ldx,
+                      codes, scales);
 }
 
 }  // namespace mx4
 
 cudaError_t launch_mx4_encode(const void* X, int dtype, int64_t batch, int64_t rows, int64_t K,
-                              int64_t ldx, uint8_t* codes, uint8_t* scales, int release,
-                              int sm_count, cudaStream_t st) {
+                              int64_t ldx, uint8_t* codes, uint8_t* scales, int sm_count,
+                              cudaStream_t st) {
   using namespace mx4;
-  const auto go = [&](auto f) { return f(X, batch, rows, K, ldx, codes, scales, release, st); };
+  const auto go = [&](auto f) { return f(X, batch, rows, K, ldx, codes, scales, st); };
   const bool wide = aligned16(X) && (batch * rows == 1 || ldx * (dtype == 2 ? 4 : 2) % 16 == 0);
   // 8 rows in flight where that still fills the SMs (14336 x 4096 bf16: 27.9 us, with 4
   // rows 32.1; 1021 x 4096 5.0 and 4.4); 4 in fp32 (8 do not fit the registers), 2 with
@@ -308,12 +311,13 @@ cudaError_t launch_mx4_decode(const uint8_t* codes, const uint8_t* scales, int64
                               int64_t rows, int64_t K, uint16_t* out, cudaStream_t st) {
   using namespace mx4;
   if (K % 8 == 0)
-    k_mx4_decode<true><<<grid_of(batch, rows, (K + 255) / 256, kWarps * kDecodeRows<true>), kThreads,
-                         0, st>>>(codes, scales, batch, rows, K, out);
-  else   // up to 7 columns of the words before a row's first value
-    k_mx4_decode<false><<<grid_of(batch, rows, (K + 7 + 247) / 248, kWarps * kDecodeRows<false>),
-                          kThreads, 0, st>>>(codes, scales, batch, rows, K, out);
-  return cudaGetLastError();
+    return launch_after(k_mx4_decode<true>,
+                        grid_of(batch, rows, (K + 255) / 256, kWarps * kDecodeRows<true>),
+                        dim3(kThreads), 0, st, codes, scales, batch, rows, K, out);
+  // up to 7 columns of the words before a row's first value
+  return launch_after(k_mx4_decode<false>,
+                      grid_of(batch, rows, (K + 7 + 247) / 248, kWarps * kDecodeRows<false>),
+                      dim3(kThreads), 0, st, codes, scales, batch, rows, K, out);
 }
 
 }  // namespace e8

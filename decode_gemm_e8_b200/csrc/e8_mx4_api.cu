@@ -52,7 +52,7 @@ int e8_mx4_encode(const e8_codebook* cb, const void* X, int dtype, int64_t batch
   const int rc = check_device(cb);
   if (rc != E8_OK) return rc;
   return cuda_status(
-      e8::launch_mx4_encode(X, dtype, batch, rows, K, ldx, codes, scales, 0,
+      e8::launch_mx4_encode(X, dtype, batch, rows, K, ldx, codes, scales,
                             cb->sm_count, (cudaStream_t)stream));
 }
 
@@ -111,7 +111,7 @@ int e8_mx4_gemm(const e8_codebook* cb, const void* X, int dtype, int64_t M, int6
                                                  cb->status, cb->sm_count, st));
   uint8_t* codes = static_cast<uint8_t*>(workspace);
   uint8_t* scales = codes + round256((size_t)e8_mx4_code_bytes(M, K));
-  if (e8::launch_mx4_encode(X, dtype, 1, M, K, ldx, codes, scales, 1, cb->sm_count, st) != cudaSuccess)
+  if (e8::launch_mx4_encode(X, dtype, 1, M, K, ldx, codes, scales, cb->sm_count, st) != cudaSuccess)
     return E8_ECUDA;
   return cuda_status(e8::launch_mx4_gemm(codes, scales, M, w_codes, w_scales, N, K, Y, cb->status,
                                          cb->sm_count, 1, st));

@@ -95,7 +95,10 @@ __global__ void __launch_bounds__(DT < 0 ? kStreamThreads : kStreamThreadsX, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  if (!a.early) grid_dep_wait();
+  if (!a.early) {
+    grid_dep_wait();
+    grid_dep_launch();
+  }
 
   const uint32_t ring = smem_u32(smem);
   if (warp == 0) {
@@ -166,7 +169,10 @@ __global__ void __launch_bounds__(DT < 0 ? kStreamThreads : kStreamThreadsX, 1)
       }
     }
   } else if (DT < 0 && warp == 6) {
-    if (a.early) grid_dep_wait();
+    if (a.early) {
+      grid_dep_wait();
+      grid_dep_launch();
+    }
     if (elect_one()) {
       // codes and scales of the tokens
       const int tiles = min(nbt, (a.M - m0 + 127) / 128);
@@ -372,7 +378,7 @@ static cudaError_t launch_stream(const void* X, int64_t ldx, const uint8_t* a_co
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = early ? 2 : 1;
+  cfg.numAttrs = 2;
   e = cudaLaunchKernelEx(&cfg, k_mx4_stream<DT>, tw, ta, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

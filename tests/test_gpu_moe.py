@@ -223,3 +223,31 @@ def test_many_runs_of_short_units(cbk, T, E, topk, H, inner):
         g.replay()
     assert e8.e8_sync_status(cbk) == e8.E8_OK
     assert all(torch.equal(y, first) for y in ys)
+
+
+def test_layers_in_a_row(cbk):
+    """A layer's output is the next one's input, in one workspace, eagerly and captured."""
+    T, E, topk, H, inner = 8, 16, 4, 512, 256
+    layers = [_layer(cbk, E, H, inner, s) for s in (1, 2, 3)]
+    x = _tokens(T, H, 4)
+    size = e8.load_library().e8_mx4_moe_workspace_bytes(T, H, E, topk, inner)
+    ws = torch.empty(size, dtype=torch.uint8, device=dev())
+
+    def run(apart):
+        y = x
+        for layer in layers:
+            y = e8.e8_mx4_moe(cbk, y, *layer, topk, workspace=ws)
+            if apart:
+                torch.cuda.synchronize()
+        return y
+
+    want = run(True)
+    for _ in range(20):
+        assert torch.equal(run(False), want)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        y = run(False)
+    for _ in range(20):
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, want) and e8.e8_sync_status(cbk) == e8.E8_OK

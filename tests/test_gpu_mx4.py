@@ -261,3 +261,74 @@ def test_rows_at_any_alignment(cbk, rows, K, dtype, off):
     assert np.array_equal(buf[:rows * K].view(rows, K).float().cpu().numpy(),
                           mx.roundtrip(x.cpu().double().numpy()).astype(np.float32))
     assert (buf[rows * K:] == 7).all()
+
+
+def test_calls_in_a_row_and_between_other_work(cbk):
+    """Each kernel may start while the one before it ends: results of calls in a row, after
+    copies, fills, other kernels and other streams, eagerly and captured, are those of calls
+    apart from each other."""
+    w0, w1 = (_data(640, 640, "bf16", s)[0] for s in (1, 2))
+    x = {M: _data(M, 640, "bf16", M)[0] for M in (1, 8, 33, 300)}
+    m0 = e8.e8_mx4_encode(cbk, w0)
+    out = e8.Mx4Matrix(torch.empty_like(m0.codes), torch.empty_like(m0.scales), 640, 640)
+    side = torch.cuda.Stream()
+
+    def chain(M, apart):
+        gap = torch.cuda.synchronize if apart else (lambda: None)
+        a = x[M].clone()
+        gap()
+        src = torch.empty_like(w0).copy_(w1)                       # a copy before the encoder
+        gap()
+        e8.e8_mx4_encode(cbk, src, out=out)                        # weights that the next call reads
+        gap()
+        y = e8.e8_mx4_gemm(cbk, a, out)
+        gap()
+        z = e8.e8_mx4_gemm(cbk, y, m0)
+        gap()
+        back = e8.e8_mx4_decode_to_bf16(cbk, out)
+        gap()
+        e8.e8_mx4_encode(cbk, back + 1, out=out)                   # written again after it was read
+        gap()
+        src.zero_()
+        gap()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            u = e8.e8_mx4_gemm(cbk, z, out)
+        torch.cuda.current_stream().wait_stream(side)
+        gap()
+        v = e8.e8_mx4_gemm(cbk, u, m0)
+        u.record_stream(torch.cuda.current_stream())
+        e8.e8_mx4_encode(cbk, src, out=out)
+        return y, z, back, u, v
+
+    for M in x:
+        want = chain(M, True)
+        torch.cuda.synchronize()
+        for _ in range(10):
+            got = chain(M, False)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got = chain(M, False)
+        for _ in range(10):
+            g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert e8.e8_sync_status(cbk) == e8.E8_OK
+
+
+def test_a_captured_call_may_be_the_first_or_follow_a_fill(cbk):
+    x = _data(2, 256, "bf16", 1)[0]
+    m = e8.e8_mx4_encode(cbk, _data(128, 256, "bf16", 2)[0])
+    want = e8.e8_mx4_gemm(cbk, x, m)
+    pad = torch.empty(1 << 20, dtype=torch.uint8, device=dev())
+    for before in (lambda: None, lambda: pad.zero_(), lambda: pad[:1 << 19].copy_(pad[1 << 19:])):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            before()
+            y = e8.e8_mx4_gemm(cbk, x, m)
+            back = e8.e8_mx4_decode_to_bf16(cbk, m)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want) and torch.equal(back, e8.e8_mx4_decode_to_bf16(cbk, m))
