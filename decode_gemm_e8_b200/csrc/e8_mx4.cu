@@ -11,7 +11,9 @@
 // is the exponent field of the maximum, and the division by it is an exact
 // multiplication.  The decoder looks codes up as bf16 bytes (byte permutation) and
 // scales pairs.  Rows that do not start on 16 bytes still move in aligned 16-byte words,
-// which neighbouring lanes share by shuffles and a funnel shift.
+// which neighbouring lanes share by shuffles and a funnel shift.  14336 x 4096: encoded
+// in 42 us from fp32 (6.4 TB/s) and 27 us from bf16 (5.5), decoded in 28 us (5.3); 1021 x
+// 4099 fp16 7.1 and 6.6 us, 1021 x 4096 3.8 and 3.6.
 #include <type_traits>
 
 #include "e8_internal.h"
@@ -130,9 +132,9 @@ __device__ __forceinline__ void encode_rows(const typename Elem<DT>::T* __restri
 // Grid: x 256-column chunks, y blocks of 8 x R rows, z matrices.  Rows run to the
 // next multiple of 128 so that the padding rows' scales are written as zero.
 // WIDE: every row starts on 16 bytes.  With checks that are made once for R rows and
-// pointers that step from row to row a 256-column row of bf16 takes about 75 of a warp's
+// pointers that step from row to row a 256-column row of bf16 takes 81 of a warp's
 // instructions; with a check and 64-bit products for each it took 158, and the kernel
-// was bound by issuing them (14336 x 4096 bf16: 45 us).
+// was bound by issuing them (14336 x 4096 bf16: 45 us, now 27).
 template <int DT, bool WIDE, int R>
 __global__ void __launch_bounds__(kThreads, 4)
     k_mx4_encode(const typename Elem<DT>::T* __restrict__ X, int64_t batch, int64_t rows,

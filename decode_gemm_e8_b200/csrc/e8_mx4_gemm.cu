@@ -29,9 +29,11 @@ namespace mx4 {
 //   warps 2-5  epilogue
 //   warps 2-9  with up to 8 tokens that are not encoded yet (DT >= 0), instead of warp
 //              6: each encodes the tokens of one of the 8 ring slots, every CTA for
-//              itself.  Against the encoder's launch, in us at N x K = 4096 x 4096 and
-//              14336 x 4096: 1 token 6.9 / 7.6 and 10.2 / 11.7, 8 tokens 8.2 / 8.6 and
-//              11.1 / 11.8, 16 tokens 10.0 / 9.3 and 14.1 / 11.7
+//              itself.  With / without the encoder's launch, in us a call at N x K =
+//              4096 x 4096 and 14336 x 4096: 1 token 7.1 / 5.5 and 10.7 / 8.9, 8 tokens
+//              7.4 / 6.3 and 10.7 / 9.1; 16 tokens 7.6 / 8.1 and 10.7 / 11.6
+// Bound by HBM on W once it runs (16 x 14336 x 4096 10.7 us, 4.9 of them its bytes), the
+// rest is its start (5 us: launch, barriers, tensor memory, first tile) and its end.
 constexpr int kStreamThreads = 224, kStreamThreadsX = 320;
 constexpr int kStreamRows = 128;
 constexpr int kBK = 256;               // K of a stage: 128 bytes of codes
@@ -395,7 +397,8 @@ static cudaError_t launch_stream(const void* X, int64_t ldx, const uint8_t* a_co
 //   cycles for N = 256 that they were measured to take), and its 30 KB would take 700.
 //   The pairs share the rows of A: every CTA reads half of its 128 rows and multicasts
 //   them to its counterpart, 22 KB a stage and CTA from L2.
-// Persistent.
+// Persistent.  4096 x 14336 x 4096: 95 us, 5.1 PFLOP/s, the tensor pipe active 71 % of the
+// cycles at the 1.6 GHz that the power limit leaves; 33 clusters of four SMs fit.
 //   warp 0      TMA producer of each CTA; a pair's bytes are counted by its leader
 //   warp 1      tensor memory; in the leader scale copies, MMAs, commits: a stage is
 //               free when both pairs of the cluster have finished with it

@@ -466,13 +466,16 @@ size_t e8_mx4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
  * the gate's row i and row 2i + 1 the up-projection's; w2: batch of E matrices
  * [H][I]; Y bf16 [T][H].  Optional outputs (NULL to skip): experts int32
  * [T][topk], by falling logit, and probs fp32 [T][topk].
- * X enters the products as two 8-bit floats that hold it exactly within 2^-17 of
- * its block's largest value, h with 8 significant bits; all sums are fp32, added
- * in a fixed order.  An expert that no token chose is not read.
+ * X enters the products as two 8-bit floats a value with one power-of-two scale a
+ * token: exactly, but for values 2^14 times smaller than the token's largest, which
+ * are off by at most 2^-21 of that.  h enters likewise with a scale for each 64
+ * values, rounded to 8 significant bits.  All sums are fp32, added in a fixed order.
+ * A token with a NaN or an infinity gives a row of NaN and leaves the others alone.
+ * An expert that no token chose is not read.
  * Shapes: 0 <= T <= E8_MOE_MAX_TOKENS, 1 <= topk <= min(E, E8_MOE_MAX_TOPK),
- * E <= E8_MOE_MAX_EXPERTS, H and I positive multiples of 128, H <= 32768, I <= 65536.  workspace: at
- * least e8_mx4_moe_workspace_bytes(...) bytes, contents ignored; it must not be
- * used by other work until the stream passes this call. */
+ * E <= E8_MOE_MAX_EXPERTS, H and I positive multiples of 128, H <= 32768, I <= 65536.
+ * workspace: at least e8_mx4_moe_workspace_bytes(...) bytes, contents ignored; it must
+ * not be used by other work until the stream passes this call. */
 #define E8_MOE_MAX_TOKENS 64
 #define E8_MOE_MAX_EXPERTS 512
 #define E8_MOE_MAX_TOPK 16
