@@ -397,7 +397,7 @@ static cudaError_t launch_stream(const void* X, int64_t ldx, const uint8_t* a_co
 //   cycles for N = 256 that they were measured to take), and its 30 KB would take 700.
 //   The pairs share the rows of A: every CTA reads half of its 128 rows and multicasts
 //   them to its counterpart, 22 KB a stage and CTA from L2.
-// Persistent.  4096 x 14336 x 4096: 95 us, 5.1 PFLOP/s, the tensor pipe active 71 % of the
+// Persistent.  4096 x 14336 x 4096: 97 us, 5.0 PFLOP/s, the tensor pipe active 71 % of the
 // cycles at the 1.6 GHz that the power limit leaves; 33 clusters of four SMs fit.
 //   warp 0      TMA producer of each CTA; a pair's bytes are counted by its leader
 //   warp 1      tensor memory; in the leader scale copies, MMAs, commits: a stage is
