@@ -587,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp == 9) {
-    if (lane == 0) {
+    if (elect_one()) {
       Unit u;
       int i = 0;
       while (take(u)) {
@@ -608,7 +608,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 8) {
-    if (lane == 0) {
+    claim = __shfl_sync(0xFFFFFFFFu, claim, 0);
+    if (elect_one()) {
       const int nact = lists.nact, ups = nact * up_tiles, grid = (int)gridDim.x;
       const int whole = ups / grid * grid, rest = ups - whole;
       const int up_parts = rest ? min(min(kMaxUpParts, grid / rest), g.H / kBK) : 1;
