@@ -741,12 +741,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (down) {
         // every tile of the expert's h; once all experts' are there nothing is asked again
         if (!all_up) {
-          if (lane == 0) {
-            all_up = ld_acquire_gpu(g.up_total) == u.want_all;
-            ok = all_up || wait_gpu(&g.up_done[u.active], u.want, &abort_flag, g.status);
-          }
-          __syncwarp();
-          all_up = __shfl_sync(0xFFFFFFFFu, (int)all_up, 0) != 0;
+          all_up = ld_acquire_gpu(g.up_total) == u.want_all;
+          ok = all_up || wait_gpu(&g.up_done[u.active], u.want, &abort_flag, g.status);
+          all_up = __all_sync(0xFFFFFFFFu, all_up);
           ok = __all_sync(0xFFFFFFFFu, ok);
           if (!ok) break;
         }
@@ -862,7 +859,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (bar_red_or(1, 128, !got)) break;
         if (u.kind == kSum) {
           // Y: 128 columns of four tokens, a warp a token, four columns a lane
-          const bool ok = et != 0 || wait_gpu(&g.down_done[u.tile], lists.nact * g.down_parts,
+          const bool ok = wait_gpu(&g.down_done[u.tile], lists.nact * g.down_parts,
                                               &abort_flag, g.status);
           __syncwarp();
           if (bar_red_or(1, 128, !ok)) break;
