@@ -548,10 +548,10 @@ class Mx4Matrix:
     power-of-two scale each, as e8_mx4_encode writes it: codes uint8
     [(batch,) rows, 16 ceil(K / 32)] and scales uint8 [(batch,) bytes in tiles]."""
 
-    __slots__ = ("codes", "scales", "rows", "K", "batch")
+    __slots__ = ("rows", "K", "batch", "_codes", "_scales", "_both")
 
     def __init__(self, codes, scales, rows: int, K: int, batch: int | None = None):
-        self.codes, self.scales = codes, scales
+        self._codes, self._scales, self._both = codes, scales, None
         self.rows = rows = int(rows)
         self.K = K = int(K)
         self.batch = None if batch is None else int(batch)
@@ -560,6 +560,56 @@ class Mx4Matrix:
         if rows < 0 or K < 1 or codes.numel() != n * rows * ((K + 31) // 32 * 16) or \
                 scales.numel() != n * ((rows + 127) // 128) * ((K + 127) // 128) * 512:
             raise E8Error(E8_EINVAL, "Mx4Matrix")
+
+    @classmethod
+    def _new(cls, like, rows, K, batch, stream):
+        """Uninitialised, in one tensor: each new tensor costs a call two microseconds, and
+        most matrices are handed from one call to the next without a look at the parts."""
+        import torch
+        m = cls.__new__(cls)
+        m.rows, m.K, m.batch, m._codes, m._scales = rows, K, batch, None, None
+        at = m._scales_at()
+        n = (1 if batch is None else batch) * ((rows + 127) // 128) * ((K + 127) // 128) * 512
+        m._both = _mx4_new((at + n,), torch.uint8, like, stream)
+        return m
+
+    def _scales_at(self):
+        """Place of the scales behind the codes, a multiple of 512 bytes."""
+        n = 1 if self.batch is None else self.batch
+        return (n * self.rows * ((self.K + 31) // 32 * 16) + 511) // 512 * 512
+
+    def _split(self):
+        lead = () if self.batch is None else (self.batch,)
+        row = (self.K + 31) // 32 * 16
+        n = (1 if self.batch is None else self.batch) * self.rows * row
+        self._codes = self._both[:n].view(lead + (self.rows, row))
+        self._scales = self._both[self._scales_at():].view(
+            lead + (((self.rows + 127) // 128) * ((self.K + 127) // 128) * 512,))
+
+    @property
+    def codes(self):
+        if self._codes is None:
+            self._split()
+        return self._codes
+
+    @property
+    def scales(self):
+        if self._codes is None:
+            self._split()
+        return self._scales
+
+    def _pointers(self, cb, where):
+        both = self._both
+        if both is not None:
+            if both.get_device() != cb.device:
+                raise E8Error(E8_EDEVICE, where)
+            at = both.data_ptr()
+            return at, at + self._scales_at()
+        _mx4_check(cb, where, self._codes, self._scales)
+        return self._codes.data_ptr(), self._scales.data_ptr()
+
+    def _like(self):
+        return self._codes if self._both is None else self._both
 
 
 _mx4_dtypes = {}
@@ -628,11 +678,11 @@ def e8_mx4_encode(cb: Codebook, X, out: Mx4Matrix | None = None, stream=None) ->
     where = "e8_mx4_encode"
     shape = X.shape
     if len(shape) == 2:
-        batch, n, lead = None, 1, ()
+        batch, n = None, 1
         rows, K = shape
     elif len(shape) == 3:
         batch, rows, K = shape
-        n, lead = batch, (batch,)
+        n = batch
     else:
         raise E8Error(E8_EINVAL, where)
     ldx = _mx4_row_stride(cb, X, where)
@@ -644,17 +694,13 @@ def e8_mx4_encode(cb: Codebook, X, out: Mx4Matrix | None = None, stream=None) ->
     if out is None:
         if K < 1:
             raise E8Error(E8_EINVAL, where)
-        u8 = torch.uint8
-        out = Mx4Matrix(_mx4_new(lead + (rows, (K + 31) // 32 * 16), u8, X, stream),
-                        _mx4_new(lead + (((rows + 127) // 128) * ((K + 127) // 128) * 512,), u8, X,
-                                 stream), rows, K, batch)
-    else:
-        if (out.rows, out.K, out.batch) != (rows, K, batch):
-            raise E8Error(E8_EINVAL, where)
-        _mx4_check(cb, where, out.codes, out.scales)
+        out = Mx4Matrix._new(X, rows, K, batch, stream)
+    elif (out.rows, out.K, out.batch) != (rows, K, batch):
+        raise E8Error(E8_EINVAL, where)
+    codes, scales = out._pointers(cb, where)
     rc = (_lib or load_library()).e8_mx4_encode(
-        cb.handle, X.data_ptr(), _mx4_dtype(X), n, rows, K, ldx, out.codes.data_ptr(),
-        out.scales.data_ptr(), _mx4_stream(cb, stream))
+        cb.handle, X.data_ptr(), _mx4_dtype(X), n, rows, K, ldx, codes, scales,
+        _mx4_stream(cb, stream))
     if rc:
         _check(rc, where)
     return out
@@ -665,14 +711,15 @@ def e8_mx4_decode_to_bf16(cb: Codebook, m: Mx4Matrix, out=None, stream=None):
     import torch
     where = "e8_mx4_decode_to_bf16"
     shape = (m.rows, m.K) if m.batch is None else (m.batch, m.rows, m.K)
-    _mx4_check(cb, where, m.codes, m.scales, out)
+    codes, scales = m._pointers(cb, where)
     if out is None:
-        out = _mx4_new(shape, torch.bfloat16, m.codes, stream)
+        out = _mx4_new(shape, torch.bfloat16, m._like(), stream)
     else:
+        _mx4_check(cb, where, out)
         _mx4_out(out, shape, torch.bfloat16, where)
     rc = (_lib or load_library()).e8_mx4_decode_to_bf16(
-        cb.handle, m.codes.data_ptr(), m.scales.data_ptr(), 1 if m.batch is None else m.batch,
-        m.rows, m.K, out.data_ptr(), _mx4_stream(cb, stream))
+        cb.handle, codes, scales, 1 if m.batch is None else m.batch, m.rows, m.K, out.data_ptr(),
+        _mx4_stream(cb, stream))
     if rc:
         _check(rc, where)
     return out
@@ -687,7 +734,8 @@ def e8_mx4_gemm(cb: Codebook, X, m: Mx4Matrix, Y=None, workspace=None, stream=No
         raise E8Error(E8_EINVAL, where)
     M, N, K = shape[0], m.rows, m.K
     ldx = _mx4_row_stride(cb, X, where)
-    _mx4_check(cb, where, m.codes, m.scales, Y, workspace)
+    codes, scales = m._pointers(cb, where)
+    _mx4_check(cb, where, Y, workspace)
     if Y is None:
         Y = _mx4_new((M, N), torch.bfloat16, X, stream)
     else:
@@ -696,8 +744,8 @@ def e8_mx4_gemm(cb: Codebook, X, m: Mx4Matrix, Y=None, workspace=None, stream=No
         workspace = _mx4_new((_mx4_ws_bytes("e8_mx4_gemm_workspace_bytes", M, N, K),), torch.uint8,
                              X, stream)
     rc = (_lib or load_library()).e8_mx4_gemm(
-        cb.handle, X.data_ptr(), _mx4_dtype(X), M, ldx, m.codes.data_ptr(), m.scales.data_ptr(), N,
-        K, Y.data_ptr(), workspace.data_ptr(), workspace.numel(), _mx4_stream(cb, stream))
+        cb.handle, X.data_ptr(), _mx4_dtype(X), M, ldx, codes, scales, N, K, Y.data_ptr(),
+        workspace.data_ptr(), workspace.numel(), _mx4_stream(cb, stream))
     if rc:
         _check(rc, where)
     return Y
@@ -709,14 +757,16 @@ def e8_mx4_gemm_codes(cb: Codebook, a: Mx4Matrix, m: Mx4Matrix, Y=None, workspac
     where = "e8_mx4_gemm_codes"
     if a.K != m.K or a.batch is not None or m.batch is not None:
         raise E8Error(E8_EINVAL, where)
-    _mx4_check(cb, where, a.codes, a.scales, m.codes, m.scales, Y, workspace)
+    a_codes, a_scales = a._pointers(cb, where)
+    codes, scales = m._pointers(cb, where)
+    _mx4_check(cb, where, Y, workspace)
     if Y is None:
-        Y = _mx4_new((a.rows, m.rows), torch.bfloat16, a.codes, stream)
+        Y = _mx4_new((a.rows, m.rows), torch.bfloat16, a._like(), stream)
     else:
         _mx4_out(Y, (a.rows, m.rows), torch.bfloat16, where)
     rc = (_lib or load_library()).e8_mx4_gemm_codes(
-        cb.handle, a.codes.data_ptr(), a.scales.data_ptr(), a.rows, m.codes.data_ptr(),
-        m.scales.data_ptr(), m.rows, m.K, Y.data_ptr(), _ptr(workspace),
+        cb.handle, a_codes, a_scales, a.rows, codes, scales, m.rows, m.K, Y.data_ptr(),
+        _ptr(workspace),
         0 if workspace is None else workspace.numel(), _mx4_stream(cb, stream))
     if rc:
         _check(rc, where)
@@ -745,8 +795,9 @@ def e8_mx4_moe(cb: Codebook, X, router, w13: Mx4Matrix, w2: Mx4Matrix, topk: int
         _mx4_out(experts, (T, topk), torch.int32, where)
     if probs is not None:
         _mx4_out(probs, (T, topk), torch.float32, where)
-    _mx4_check(cb, where, X, router, w13.codes, w13.scales, w2.codes, w2.scales, Y, experts, probs,
-               workspace)
+    codes13, scales13 = w13._pointers(cb, where)
+    codes2, scales2 = w2._pointers(cb, where)
+    _mx4_check(cb, where, X, router, Y, experts, probs, workspace)
     if Y is None:
         Y = _mx4_new(shape, bf16, X, stream)
     else:
@@ -756,9 +807,8 @@ def e8_mx4_moe(cb: Codebook, X, router, w13: Mx4Matrix, w2: Mx4Matrix, topk: int
                              torch.uint8, X, stream)
     rc = (_lib or load_library()).e8_mx4_moe(
         cb.handle, X.data_ptr(), T, H, router.data_ptr(), E, topk, 1 if renormalize else 0,
-        w13.codes.data_ptr(), w13.scales.data_ptr(), inner, w2.codes.data_ptr(),
-        w2.scales.data_ptr(), Y.data_ptr(), _ptr(experts), _ptr(probs), workspace.data_ptr(),
-        workspace.numel(), _mx4_stream(cb, stream))
+        codes13, scales13, inner, codes2, scales2, Y.data_ptr(), _ptr(experts), _ptr(probs),
+        workspace.data_ptr(), workspace.numel(), _mx4_stream(cb, stream))
     if rc:
         _check(rc, where)
     return Y
