@@ -13,7 +13,8 @@
 // scales pairs.  Rows that do not start on 16 bytes still move in aligned 16-byte words,
 // which neighbouring lanes share by shuffles and a funnel shift.  14336 x 4096: encoded
 // in 42 us from fp32 (6.4 TB/s) and 27 us from bf16 (5.5), decoded in 28 us (5.3); 1021 x
-// 4099 fp16 7.1 and 6.6 us, 1021 x 4096 3.8 and 3.6.
+// 4099 fp16 6.2 and 5.8 us, 1021 x 4096 3.8 and 3.6: there instructions bound it, 180
+// of a warp for 256 values instead of 80 to 95.
 #include <type_traits>
 
 #include "e8_internal.h"
@@ -25,9 +26,15 @@ namespace mx4 {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
+// What a warp's R rows of 256 columns touch: kFull, the matrix alone, and with rows that
+// start anywhere a word more on either side, of other rows; kTail, its right end too, past
+// which nothing is kept; kEnds, rows so near to an end of the matrix that words around them
+// may lie outside of it.
+enum : int { kFull = 0, kTail = 1, kEnds = 2 };
+
 // Rows that start anywhere.  Lane l reads the 16-byte words (2 of them in fp32) that
 // hold its first value; what is missing at their end it gets from lane l + 1, lane 31
-// from memory.  A word that is not wholly inside the row is read value by value.
+// from memory.  What lies before the row is shifted out, what lies behind it cleared (get).
 template <int DT>
 struct Shifted {
   using T = typename Elem<DT>::T;
@@ -36,29 +43,34 @@ struct Shifted {
   uint32_t w[4 * kWords], next[4];
   int shift;   // values between the word's start and the lane's first value: one for a row
 
-  template <bool FULL>
+  // (loads under a predicate: in a branch each would be waited for before the next)
+  template <int MODE>
   static __device__ __forceinline__ void word(const T* __restrict__ row, int64_t c, int64_t K,
-                                              uint32_t* to) {
-    if (FULL || (c >= 0 && c + kPer <= K)) {
-      const uint4 a = __ldcs(reinterpret_cast<const uint4*>(row + c));
-      to[0] = a.x; to[1] = a.y; to[2] = a.z; to[3] = a.w;
+                                              bool on, uint32_t* to) {
+    if constexpr (MODE != kEnds) {
+      const uint32_t in = on && (MODE == kFull || c < K);
+      asm volatile(
+          "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+          "mov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
+          "@p ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}\n"
+          : "=&r"(to[0]), "=&r"(to[1]), "=&r"(to[2]), "=&r"(to[3])
+          : "l"(row + c), "r"(in));
     } else {
       to[0] = to[1] = to[2] = to[3] = 0;
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
-        if (c + i >= 0 && c + i < K) {
+        if (on && c + i >= 0 && c + i < K) {
           if constexpr (DT == 2) to[i] = __float_as_uint(row[c + i]);
           else to[i / 2] |= (uint32_t)row[c + i] << (16 * (i & 1));
         }
     }
   }
-  template <bool FULL>
+  template <int MODE>
   __device__ __forceinline__ void load(const T* __restrict__ row, int64_t c, int64_t K) {
     shift = (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) word<FULL>(row, c - shift + i * kPer, K, w + 4 * i);
-    next[0] = next[1] = next[2] = next[3] = 0;
-    if ((threadIdx.x & 31) == 31) word<FULL>(row, c - shift + kWords * kPer, K, next);
+    for (int i = 0; i < kWords; ++i) word<MODE>(row, c - shift + i * kPer, K, true, w + 4 * i);
+    word<MODE>(row, c - shift + kWords * kPer, K, (threadIdx.x & 31) == 31, next);
   }
   __device__ __forceinline__ void zero() {
     shift = 0;
@@ -66,7 +78,9 @@ struct Shifted {
     for (uint32_t& v : w) v = 0;
     next[0] = next[1] = next[2] = next[3] = 0;
   }
-  __device__ __forceinline__ Eight<DT> get() const {
+  // `left`: values of the row from the lane's first on, if fewer than 8
+  template <int MODE>
+  __device__ __forceinline__ Eight<DT> get(int left) const {
     constexpr int n = 4 * kWords;
     uint32_t t[n + 4];
 #pragma unroll
@@ -76,28 +90,34 @@ struct Shifted {
       const uint32_t v = __shfl_down_sync(0xFFFFFFFFu, w[i], 1);
       t[n + i] = (threadIdx.x & 31) == 31 ? next[i] : v;
     }
-    // by 4-byte words first, then by half a word
-    const int words = DT == 2 ? shift : shift >> 1;
-    if (words & 2) {
-#pragma unroll
-      for (int i = 0; i < n + 2; ++i) t[i] = t[i + 2];
-    }
-    if (words & 1) {
-#pragma unroll
-      for (int i = 0; i < n + 1; ++i) t[i] = t[i + 1];
-    }
+    // (one shift for a row: a branch costs less than choosing word by word)
     Eight<DT> e;
+    const auto from = [&](auto words) {
 #pragma unroll
-    for (int i = 0; i < n; ++i)
-      e.w[i] = DT == 2 ? t[i] : __funnelshift_r(t[i], t[i + 1], 16 * (shift & 1));
+      for (int i = 0; i < n; ++i)
+        e.w[i] = DT == 2 ? t[i + words]
+                         : __funnelshift_r(t[i + words], t[i + words + 1], 16 * (shift & 1));
+    };
+    switch (DT == 2 ? shift : shift >> 1) {
+      case 0: from(std::integral_constant<int, 0>()); break;
+      case 1: from(std::integral_constant<int, 1>()); break;
+      case 2: from(std::integral_constant<int, 2>()); break;
+      default: from(std::integral_constant<int, 3>());
+    }
+    if constexpr (MODE != kFull) {
+#pragma unroll
+      for (int i = 0; i < n; ++i) {
+        if constexpr (DT == 2) e.w[i] = i < left ? e.w[i] : 0u;
+        else e.w[i] = 2 * i + 1 < left ? e.w[i] : 2 * i < left ? e.w[i] & 0xFFFFu : 0u;
+      }
+    }
     return e;
   }
 };
 
-// R rows of 256 columns, c the lane's first.  FULL: all of them are in the matrix (and,
-// unless WIDE, so is a word on either side).  x, to and sc point at the first row; `to`
-// and `sc` at the lane's column.
-template <int DT, bool WIDE, int R, bool FULL>
+// R rows of 256 columns, c the lane's first; x, to and sc point at the first row, `to` and
+// `sc` at the lane's column; `rows` are left in the matrix.
+template <int DT, bool WIDE, int R, int MODE>
 __device__ __forceinline__ void encode_rows(const typename Elem<DT>::T* __restrict__ x,
                                             int64_t ldx, int64_t c, int64_t K, int64_t rows,
                                             uint8_t* __restrict__ to, int64_t cs,
@@ -105,24 +125,25 @@ __device__ __forceinline__ void encode_rows(const typename Elem<DT>::T* __restri
   std::conditional_t<WIDE, Eight<DT>, Shifted<DT>> in[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    if (FULL || r < rows) {
-      if constexpr (!WIDE) in[r].template load<FULL>(x, c, K);
-      else if constexpr (FULL) in[r].load(x + c);
+    if (MODE == kFull || r < rows) {
+      if constexpr (!WIDE) in[r].template load<MODE>(x, c, K);
+      else if constexpr (MODE == kFull) in[r].load(x + c);
       else in[r].load(x, c, K);
     } else {
       in[r].zero();
     }
     x += ldx;
   }
-  const bool code_lane = FULL || c / 2 < cs;
-  const bool scale_lane = (threadIdx.x & 3) == 0 && (FULL || c / 128 < kqs);
+  const int left = K - c < 8 ? (int)(K - c) : 8;
+  const bool code_lane = MODE == kFull || c / 2 < cs;
+  const bool scale_lane = (threadIdx.x & 3) == 0 && (MODE == kFull || c / 128 < kqs);
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     Eight<DT> v;
     if constexpr (WIDE) v = in[r];
-    else v = in[r].get();
+    else v = in[r].template get<MODE>(left);
     const uint32_t byte = v.block_byte(), code = v.codes(byte);
-    if (code_lane && (FULL || r < rows)) *reinterpret_cast<uint32_t*>(to) = code;
+    if (code_lane && (MODE == kFull || r < rows)) *reinterpret_cast<uint32_t*>(to) = code;
     to += cs;
     // (blocks past the matrix hold zeros, whose byte is 0)
     if (scale_lane) sc[16 * r] = (uint8_t)byte;
@@ -146,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, 4)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t cs = code_stride(K), kqs = scale_tiles(K);
   const int64_t c0 = (int64_t)blockIdx.x * 256, c = c0 + lane * 8;
-  const bool full = WIDE ? c0 + 256 <= K : c0 > 0 && c0 + 264 <= K;
+  const bool full = c0 + (WIDE ? 256 : 264) <= K;
   for (int64_t b = blockIdx.z; b < batch; b += gridDim.z) {
     for (int64_t row0 = ((int64_t)blockIdx.y * kWarps + warp) * R; row0 < rows_padded;
          row0 += (int64_t)gridDim.y * kWarps * R) {
@@ -154,10 +175,14 @@ __global__ void __launch_bounds__(kThreads, 4)
       uint8_t* to = codes + (b * rows + row0) * cs + c / 2;
       uint8_t* sc = scales + b * rows_padded / 128 * kqs * 512 + scale_at(row0, c >> 7, kqs) +
                     ((lane >> 2) & 3);
-      if (full && row0 + R <= rows)
-        encode_rows<DT, WIDE, R, true>(x, ldx, c, K, rows - row0, to, cs, sc, kqs);
+      // eight rows on are eight values on, at least: a word
+      const int64_t before = b * rows + row0, behind = (batch - b) * rows - row0 - R;
+      if (!WIDE && ((c0 == 0 && before < 8) || behind < 8))
+        encode_rows<DT, WIDE, R, WIDE ? kTail : kEnds>(x, ldx, c, K, rows - row0, to, cs, sc, kqs);
+      else if (full && row0 + R <= rows)
+        encode_rows<DT, WIDE, R, kFull>(x, ldx, c, K, rows - row0, to, cs, sc, kqs);
       else
-        encode_rows<DT, WIDE, R, false>(x, ldx, c, K, rows - row0, to, cs, sc, kqs);
+        encode_rows<DT, WIDE, R, kTail>(x, ldx, c, K, rows - row0, to, cs, sc, kqs);
     }
   }
 }
@@ -206,6 +231,7 @@ __global__ void __launch_bounds__(kThreads, 4)
   const int64_t cs = code_stride(K), kqs = scale_tiles(K), sb = scale_bytes(rows, K);
   const int64_t c = (int64_t)blockIdx.x * kDecodeColumns<VEC> + (VEC ? lane : lane - 1) * 8;
   const bool in = c >= 0 && c / 2 < cs;
+  const int left = K - c < 16 ? (int)(K - c) : 16;   // values from the lane's first on
   for (int64_t b = blockIdx.z; b < batch; b += gridDim.z) {
     for (int64_t row0 = ((int64_t)blockIdx.y * kWarps + warp) * kRows; row0 < rows;
          row0 += (int64_t)gridDim.y * kWarps * kRows) {
@@ -239,29 +265,28 @@ __global__ void __launch_bounds__(kThreads, 4)
             t[4 + i] = v[i];
           }
           t[8] = 0;
-          if (skip & 8) {
+          uint32_t o[4];
+          const auto from = [&](auto words) {
 #pragma unroll
-            for (int i = 0; i < 5; ++i) t[i] = t[i + 4];
+            for (int i = 0; i < 4; ++i)
+              o[i] = __funnelshift_r(t[i + words], t[i + words + 1], 16 * (skip & 1));
+          };
+          switch (skip >> 1) {
+            case 0: from(std::integral_constant<int, 0>()); break;
+            case 1: from(std::integral_constant<int, 1>()); break;
+            case 2: from(std::integral_constant<int, 2>()); break;
+            case 3: from(std::integral_constant<int, 3>()); break;
+            default: from(std::integral_constant<int, 4>());
           }
-          if (skip & 4) {
-#pragma unroll
-            for (int i = 0; i < 6; ++i) t[i] = t[i + 2];
-          }
-          if (skip & 2) {
-#pragma unroll
-            for (int i = 0; i < 5; ++i) t[i] = t[i + 1];
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) t[i] = __funnelshift_r(t[i], t[i + 1], 16 * (skip & 1));
-          const int64_t at = c - shift;
+          // the word's values lo .. hi - 1 are the row's
+          const int lo = c == 0 ? shift : 0, hi = left + shift < 8 ? left + shift : 8;
           if (lane > 0) {
-            if (at >= 0 && at + 8 <= K) {
-              __stcs(reinterpret_cast<uint4*>(to - shift), make_uint4(t[0], t[1], t[2], t[3]));
+            if (lo == 0 && hi == 8) {
+              __stcs(reinterpret_cast<uint4*>(to - shift), make_uint4(o[0], o[1], o[2], o[3]));
             } else {
 #pragma unroll
               for (int i = 0; i < 8; ++i)
-                if (at + i >= 0 && at + i < K)
-                  to[i - shift] = (uint16_t)(t[i / 2] >> (16 * (i & 1)));
+                if (i >= lo && i < hi) to[i - shift] = (uint16_t)(o[i / 2] >> (16 * (i & 1)));
             }
           }
         }
@@ -296,16 +321,17 @@ cudaError_t launch_mx4_encode(const void* X, int dtype, int64_t batch, int64_t r
   using namespace mx4;
   const auto go = [&](auto f) { return f(X, batch, rows, K, ldx, codes, scales, st); };
   const bool wide = aligned16(X) && (batch * rows == 1 || ldx * (dtype == 2 ? 4 : 2) % 16 == 0);
-  // 8 rows in flight where that still fills the SMs (14336 x 4096 bf16: 27.9 us, with 4
-  // rows 32.1; 1021 x 4096 5.0 and 4.4); 4 in fp32 (8 do not fit the registers), 2 with
-  // words of a neighbour to hold
+  // Rows in flight, 16-bit types: 8 where that still fills the SMs (14336 x 4096 bf16: 27.9
+  // us, with 4 rows 32.1; 1021 x 4096 5.0 and 4.4); with words of a neighbour to hold half
+  // as many (14336 x 4099 bf16 44 us, with 2 rows 54).  In fp32 4 and 2, all that fit the
+  // registers.
   const bool many = (K + 255) / 256 * ((rows + 63) / 64) * batch >= 4 * sm_count;
   if (dtype == 0)
-    return !wide ? go(encode_as<0, false, 2>) : many ? go(encode_as<0, true, 8>)
-                                                     : go(encode_as<0, true, 4>);
+    return many ? (wide ? go(encode_as<0, true, 8>) : go(encode_as<0, false, 4>))
+                : (wide ? go(encode_as<0, true, 4>) : go(encode_as<0, false, 2>));
   if (dtype == 1)
-    return !wide ? go(encode_as<1, false, 2>) : many ? go(encode_as<1, true, 8>)
-                                                     : go(encode_as<1, true, 4>);
+    return many ? (wide ? go(encode_as<1, true, 8>) : go(encode_as<1, false, 4>))
+                : (wide ? go(encode_as<1, true, 4>) : go(encode_as<1, false, 2>));
   return wide ? go(encode_as<2, true, 4>) : go(encode_as<2, false, 2>);
 }
 
