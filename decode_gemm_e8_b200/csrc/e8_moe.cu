@@ -27,8 +27,8 @@
 // Few up units are split over K, their partial sums added in order by the unit that
 // arrives last; the down units' parts are added with the slots.  No result depends on
 // timing or on which block claimed what.
-// 64 tokens, 8 of 128 experts (2048, 768): 81 us for 317 MB, 6.2 TB/s in the up products and
-// 4.8 in the down products; 1 token, 8 of 64 (2048, 1024): 25 us, of which the router 5,
+// 64 tokens, 8 of 128 experts (2048, 768): 80 us for 317 MB, 6.2 TB/s in the up products and
+// 4.8 in the down products; 1 token, 8 of 64 (2048, 1024): 24 us, of which the router 5,
 // the way to the first products 4, h to the other blocks 4, the sums 5.
 #include "e8_internal.h"
 #include "e8_mx4.cuh"
@@ -472,7 +472,9 @@ struct Unit {
 // scheduler, 9 tells other blocks of finished units (a release to the whole GPU takes a
 // microsecond or two under load, which the epilogue does not wait for).  At 16 KB of
 // weights a stage the SM's share of HBM leaves each role some 700 cycles a stage: one
-// elected thread runs a role's whole loop with its addresses in registers.
+// elected thread runs a role's whole loop with its addresses in registers, and what a whole
+// warp waits for all its lanes poll (64 tokens 80 us; with branches on lane 0 instead of
+// elected threads 81.6, with polls by lane 0 87.8).
 __global__ void __launch_bounds__(kThreads, 1)
     k_moe_experts(const __grid_constant__ CUtensorMap tm13, const __grid_constant__ CUtensorMap tm2,
                   const __grid_constant__ ExpertArgs g) {
@@ -721,8 +723,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp >= 6) {
-    // The two warps take turns, a stage each.  16 lanes copy the 256 bytes of each of a token's two rows, 16 bytes a lane, to
-    // where the 128-byte swizzle has them
+    // The two warps take turns, a stage each.  16 lanes copy the 256 bytes of each of a
+    // token's two rows, 16 bytes a lane, to where the 128-byte swizzle has them
     const int r = lane >> 4, c = lane & 15;
     const uint32_t to = (c >> 3) * b_bytes + (uint32_t)r * 128u;
     uint32_t st = ring + 2u * kWBytes, ph = 1;
