@@ -201,7 +201,7 @@ __device__ __forceinline__ bool mbar_wait_lazy(uint64_t* bar, uint32_t parity,
       if (ld_shared_volatile(abort_flag)) return false;
       const uint64_t t = global_timer_ns();
       if (t0 == 0) t0 = t;
-      if (t - t0 > kWaitLimitNs) {
+      if ((int64_t)(t - t0) > (int64_t)kWaitLimitNs) {
         st_shared_volatile(abort_flag, 1u);
         if (status) atomicOr(status, code);
         return false;
