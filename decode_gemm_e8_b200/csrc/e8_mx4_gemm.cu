@@ -387,25 +387,23 @@ static cudaError_t launch_stream(const void* X, int64_t ldx, const uint8_t* a_co
 
 // ----------------------------------------------------------- many tokens ---
 // Two CTAs compute a 256 x 192 tile (cta_group::2), each holding 128 rows of A and 96
-// of W; a cluster of two such pairs side by side a tile of 256 x 384.
+// of W.
 //   Why 192 columns: reading an fp32 accumulator of 128 x 256 out of tensor memory
 //   takes an SM about 2000 cycles, a fifth of the 16 stages of K = 4096, so it has to
 //   overlap the next tile's MMAs; two accumulators of 192 columns (384) and the scales
 //   of five stages (120) fit the 512 columns, two of 256 do not.
-//   Why two pairs: an SM gets about 43 bytes a cycle from L2 (measured: 12 TB/s over
-//   all SMs); a stage's MMAs take about 480 cycles (four of 256 x 192 x 64 at the 160
-//   cycles for N = 256 that they were measured to take), and its 30 KB would take 700.
-//   The pairs share the rows of A: every CTA reads half of its 128 rows and multicasts
-//   them to its counterpart, 22 KB a stage and CTA from L2.
-// Persistent.  4096 x 14336 x 4096: 97 us, 5.0 PFLOP/s, the tensor pipe active 71 % of the
-// cycles at the 1.6 GHz that the power limit leaves; 33 clusters of four SMs fit.
+//   Every copy reads global memory into its own CTA: no TMA multicast, as in the
+//   library's other kernels, which also serve runs on several GPUs.
+//   An SM's 31 KB a stage come from L2 (about 43 bytes a cycle, measured over all SMs)
+//   while the stage's MMAs take some 480 cycles, so L2 bounds it before the tensor cores
+//   do.  Clusters of two pairs that shared A by multicast read 22 KB, but only 33 of them,
+//   132 SMs, fit: 105 us for 4096 x 14336 x 4096 with the encoder's launch, 103 this way.
+// Persistent, one pair of SMs a cluster.
 //   warp 0      TMA producer of each CTA; a pair's bytes are counted by its leader
-//   warp 1      tensor memory; in the leader scale copies, MMAs, commits: a stage is
-//               free when both pairs of the cluster have finished with it
+//   warp 1      tensor memory; in the leader scale copies, MMAs, commits
 //   warps 2-9   epilogue: 64 columns at a time to bf16, shared memory and TMA stores
 namespace pair {
 constexpr int kThreads = 320;
-constexpr int kPairs = 2, kCtas = 2 * kPairs;
 constexpr int kN = 192;                            // columns of a pair's tile
 constexpr int kStages = 5;
 constexpr uint32_t kWTile = kN / 2 * 128;
@@ -438,16 +436,16 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
   __shared__ volatile uint32_t abort_flag;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int crank = (int)cluster_ctarank(), rank = crank & 1, pr = crank >> 1;
-  const int first = (int)blockIdx.x / kCtas, step = (int)gridDim.x / kCtas;
+  const int rank = (int)cluster_ctarank();
+  const int first = (int)blockIdx.x / 2, step = (int)gridDim.x / 2;
   const int tiles_m = (a.M + 255) / 256;
-  const int tiles = tiles_m * ((a.N + kPairs * kN - 1) / (kPairs * kN));
+  const int tiles = tiles_m * ((a.N + kN - 1) / kN);
   const int kblocks = (a.K + kBK - 1) / kBK, kqs = (int)scale_tiles(a.K);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&full[s], 1);         // the leader's producer; the copies add bytes
-      mbar_init(&empty[s], kPairs);   // every leader's commit, to all CTAs
+      mbar_init(&full[s], 1);    // the leader's producer; the copies add bytes
+      mbar_init(&empty[s], 1);   // the leader's commit, to both CTAs
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
@@ -465,7 +463,7 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
     tmem_alloc_2sm(&tmem_slot, 512);
     tmem_relinquish_2sm();
   }
-  // all CTAs' barriers are initialised before any copy or commit reaches them
+  // both CTAs' barriers are initialised before any copy or commit reaches them
   __syncwarp();
   tc_fence_before();
   cluster_arrive();
@@ -482,23 +480,20 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
       bool ok = true;
       for (int tile = first; tile < tiles && ok; tile += step) {
         const int tn = tile / tiles_m, tm = tile - tn * tiles_m;
-        const int n0 = (tn * kPairs + pr) * kN;   // first column of the pair's tile
-        const int tr = tm * 2 + rank;             // this CTA's 128 rows of A
-        const int fa = tr * kqs, fw = ((n0 >> 7) + rank) * kqs;
+        const int n0 = tn * kN, tr = tm * 2 + rank;   // this CTA's 128 rows of A
+        const int fa = tr * kqs, fw = (n0 >> 7) * kqs;
         for (int kb = 0; kb < kblocks; ++kb) {
           ok = mbar_wait_lazy(&empty[s], ph, &abort_flag, a.status, kDevTimeoutEmpty);
           if (!ok) break;
           if (rank == 0) mbar_arrive_expect_tx(&full[s], 2u * kStageBytes);
           const uint32_t bar = smem_u32(&full[s]) & kPeerBitMask;
-          load_2d_2sm_mc(st + (uint32_t)pr * 8192u, &tmA, bar, kb * 128, tr * 128 + pr * 64,
-                         (uint16_t)(0x5 << rank));
+          load_2d_2sm(st, &tmA, bar, kb * 128, tr * 128);
           load_2d_2sm(st + kCodeTile, &tmW, bar, kb * 128, n0 + rank * (kN / 2));
-          // scale tiles of 128 rows: two 512-byte rows of the map, the stage's columns;
-          // A's for both pairs, W's two tiles for both CTAs of the pair
-          if (pr == 0)
-            load_2d_2sm_mc(st + kScaleOff, &tmAs, bar, 0, fa + 2 * kb, (uint16_t)(0x5 << rank));
-          load_2d_2sm_mc(st + kScaleOff + 1024u + (uint32_t)rank * 1024u, &tmWs, bar, 0,
-                         fw + 2 * kb, (uint16_t)(0x3 << (2 * pr)));
+          // scale tiles of 128 rows: two 512-byte rows of the map, the stage's columns; W's
+          // two tiles go to both CTAs
+          load_2d_2sm(st + kScaleOff, &tmAs, bar, 0, fa + 2 * kb);
+          load_2d_2sm(st + kScaleOff + 1024u, &tmWs, bar, 0, fw + 2 * kb);
+          load_2d_2sm(st + kScaleOff + 2048u, &tmWs, bar, 0, fw + kqs + 2 * kb);
           st += kStageBytes;
           if (++s == kStages) {
             s = 0;
@@ -523,7 +518,7 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
         const uint32_t d = tmem + (uint32_t)(buf * kN);
         // a tile of 192 rows of W starts at row 0 or 64 of a scale tile; a tensor-memory
         // column holds the scales of 32 rows
-        const uint32_t skip = (uint32_t)((tile / tiles_m * kPairs + pr) & 1) * 2u;
+        const uint32_t skip = (uint32_t)((tile / tiles_m) & 1) * 2u;
         int left = a.K;   // columns from here on
         for (int kb = 0; kb < kblocks; ++kb) {
           ok = mbar_wait_lazy(&full[s], ph, &abort_flag, a.status, kDevTimeoutFull);
@@ -548,7 +543,7 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
             mma_mxf4_2sm(d, code_desc(x + 4u), code_desc(w + 4u), idesc0, cols + 4u, sfb_at + 8u, 1);
           if (left > 192)
             mma_mxf4_2sm(d, code_desc(x + 6u), code_desc(w + 6u), idesc1, cols + 4u, sfb_at + 8u, 1);
-          mma_commit_2sm_mc(&empty[s], (uint16_t)((1 << kCtas) - 1));
+          mma_commit_2sm_mc(&empty[s], 0x3);
           left -= kBK;
           st += kStageBytes >> 4;
           cols += kSfCols;
@@ -559,7 +554,7 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
             cols = tmem + kSfCol0;
           }
         }
-        if (ok) mma_commit_2sm_mc(&acc_full[buf], (uint16_t)(0x3 << (2 * pr)));
+        if (ok) mma_commit_2sm_mc(&acc_full[buf], 0x3);
       }
       // every MMA of this thread has finished once `drain` flips
       mma_commit_2sm(&drain);
@@ -569,7 +564,7 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
     }
   } else {
     const int quarter = warp & 3, half = (warp - 2) >> 2;
-    const uint32_t release = mapa_shared(smem_u32(&acc_empty[0]), (uint32_t)(2 * pr));
+    const uint32_t release = mapa_shared(smem_u32(&acc_empty[0]), 0u);
     const bool vec = (a.N & 7) == 0;
     uint8_t* piece = smem + kStages * kStageBytes + (warp - 2) * 4096;
     uint16_t* staged =
@@ -599,7 +594,7 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
 #pragma unroll
         for (int j = 0; j < 32; ++j)
           v[j] = pack_bf16x2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
-        const int col = (tn * kPairs + pr) * kN + c;
+        const int col = tn * kN + c;
         if (vec) {
           // 128-byte swizzle and a TMA store: stores of each lane's own row would fill
           // the queue that the barriers and the MMAs' issue go through
@@ -658,23 +653,6 @@ static bool scale_map(CUtensorMap* map, const uint8_t* scales, int64_t rows, int
                       CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
-// Clusters of this kernel that can be resident at once (kept per device; 0 if the
-// runtime does not say).
-static int resident_clusters(cudaLaunchConfig_t cfg, int sm_count) {
-  constexpr int kMaxDev = 64;
-  static int kept[kMaxDev];
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return 0;
-  if (kept[dev] > 0) return kept[dev];
-  cfg.gridDim = dim3((unsigned)(sm_count / pair::kCtas * pair::kCtas));
-  cfg.numAttrs = 1;
-  if (cudaOccupancyMaxActiveClusters(&n, k_mx4_pair, &cfg) != cudaSuccess) {
-    (void)cudaGetLastError();
-    return 0;
-  }
-  return kept[dev] = n;
-}
-
 static cudaError_t launch_pair(const uint8_t* a_codes, const uint8_t* a_scales, int64_t M,
                                const uint8_t* w_codes, const uint8_t* w_scales, int64_t N,
                                int64_t K, uint16_t* Y, uint32_t* status, int sm_count, int early,
@@ -688,7 +666,7 @@ static cudaError_t launch_pair(const uint8_t* a_codes, const uint8_t* a_scales, 
   a.status = status;
   const uint64_t cs = (uint64_t)code_stride(K);
   CUtensorMap ta, tw, tas, tws, ty = {};
-  if (!encode_tmap_2d(&ta, a_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)M, cs, 64, 128,
+  if (!encode_tmap_2d(&ta, a_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)M, cs, 128, 128,
                     CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode_tmap_2d(&tw, w_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)N, cs, kN / 2, 128,
                     CU_TENSOR_MAP_SWIZZLE_128B) ||
@@ -698,23 +676,21 @@ static cudaError_t launch_pair(const uint8_t* a_codes, const uint8_t* a_scales, 
     return cudaErrorInvalidValue;
   cudaError_t e = ensure_smem_limit(k_mx4_pair, kMaxDynSmem);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = ((M + 255) / 256) * ((N + kPairs * kN - 1) / (kPairs * kN));
+  const int64_t tiles = ((M + 255) / 256) * ((N + kN - 1) / kN);
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = 1024 + (size_t)kStages * kStageBytes + kStaged;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kCtas;
+  attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  int clusters = resident_clusters(cfg, sm_count);
-  if (clusters < 1) clusters = sm_count / kCtas;
-  if (tiles < clusters) clusters = (int)tiles;
-  cfg.gridDim = dim3((unsigned)(kCtas * clusters));
+  const int64_t pairs = tiles < sm_count / 2 ? tiles : sm_count / 2;
+  cfg.gridDim = dim3((unsigned)(2 * pairs));
   cfg.numAttrs = early ? 2 : 1;
   e = cudaLaunchKernelEx(&cfg, k_mx4_pair, ta, tw, tas, tws, ty, a);
   return e != cudaSuccess ? e : cudaGetLastError();
