@@ -299,8 +299,8 @@ __global__ void __launch_bounds__(512, 4) k_act_q8(const uint16_t* __restrict__ 
   // the GEMM that follows may start at once: it touches nothing that this
   // kernel or its predecessor writes until its own wait for this grid.  A
   // kernel that releases its dependents early writes nothing that this one
-  // reads (X comes from a finished kernel), so everything up to the stores
-  // overlaps the tail of the preceding kernel.
+  // reads (X comes from a finished kernel; the rule stands at mx4::launch_after),
+  // so everything up to the stores overlaps the tail of the preceding kernel.
   grid_dep_launch();
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int nc = (K + 4095) >> 12;                          // chunks of the row

@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kThreads, 4)
                  int64_t rows_padded, int64_t K, int64_t ldx, uint8_t* __restrict__ codes,
                  uint8_t* __restrict__ scales) {
   static_assert(32 % R == 0, "R rows are in one group of 32");
-  grid_dep_wait();
+  grid_dep_wait();   // before anything is read or written: launch_after
   grid_dep_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t cs = code_stride(K), kqs = scale_tiles(K);
@@ -225,8 +225,7 @@ __global__ void __launch_bounds__(kThreads, 4)
                  int64_t batch, int64_t rows, int64_t K, uint16_t* __restrict__ out) {
   constexpr int kRows = kDecodeRows<VEC>;
   static_assert(32 % kRows == 0, "the rows are in one group of 32");
-  grid_dep_wait();
-  grid_dep_launch();
+  grid_dep_wait();   // (values are tokens to other calls: launch_after)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t cs = code_stride(K), kqs = scale_tiles(K), sb = scale_bytes(rows, K);
   const int64_t c = (int64_t)blockIdx.x * kDecodeColumns<VEC> + (VEC ? lane : lane - 1) * 8;

@@ -11,15 +11,18 @@
 namespace e8 {
 namespace mx4 {
 
-// Launches a kernel that may start while the one before it in the stream ends.  A kernel
-// launched so waits for the one before (grid_dep_wait) and only then lets the next one
-// start (grid_dep_launch): whatever came before the kernel before is then over when a
-// kernel runs its first instruction, and weights may be read ahead of the wait if not the
-// kernel before, but one before that, may have written them.  A call on its own gains
-// nothing; calls in a row gain about a microsecond each (1 x 4096 x 4096 product 5.8 us
-// instead of 7.1, 1 x 4096 encoded and decoded 3.0 instead of 3.7).  The kernels that fill
-// the SMs for longer lose one to the next kernel's early blocks (a layer of 64 tokens
-// 82.5 us instead of 81.6) and do not let it start.
+// Launches a kernel that may start while the one before it in the stream ends, if that one
+// lets it (grid_dep_launch); it waits for it (grid_dep_wait) before it reads or writes.
+// The rule of the library on who may let the next kernel start:
+//   - only a kernel that writes nothing a call takes as X, idx1 or idx2: the int8
+//     transform of e8_gemm (k_act_q8) and the product behind it read those before their
+//     own waits, so the kernel that wrote them must be over when they start;
+//   - and only behind its own wait, if the next one reads weights ahead of its wait: what
+//     came before this kernel is then over (the encoder in front of a product).
+// Of the microscaled kernels the encoder does (it writes codes and scales, which nothing
+// reads ahead); products and the decoder write bf16, which is X to e8_gemm, and do not.
+// (Products of 1 x 4096 x 4096 in a row take 6.9 us each, and 5.7 if they did; one behind
+// an encoder still starts while that one ends.)
 template <typename... P, typename... A>
 inline cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem,
                                 cudaStream_t st, A... args) {

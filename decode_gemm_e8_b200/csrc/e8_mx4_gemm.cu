@@ -97,10 +97,7 @@ __global__ void __launch_bounds__(DT < 0 ? kStreamThreads : kStreamThreadsX, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  if (!a.early) {
-    grid_dep_wait();
-    grid_dep_launch();
-  }
+  if (!a.early) grid_dep_wait();
 
   const uint32_t ring = smem_u32(smem);
   if (warp == 0) {
@@ -171,10 +168,7 @@ __global__ void __launch_bounds__(DT < 0 ? kStreamThreads : kStreamThreadsX, 1)
       }
     }
   } else if (DT < 0 && warp == 6) {
-    if (a.early) {
-      grid_dep_wait();
-      grid_dep_launch();
-    }
+    if (a.early) grid_dep_wait();
     if (elect_one()) {
       // codes and scales of the tokens
       const int tiles = min(nbt, (a.M - m0 + 127) / 128);

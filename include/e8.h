@@ -153,9 +153,9 @@ int e8_act_rht(const uint16_t* X, int64_t M, int64_t K, uint64_t rht_seed, uint1
  * before the kernel that precedes the call on the stream has finished, if
  * that kernel releases its dependents early (griddepcontrol.launch_dependents).
  * Kernels that do not release early (every kernel of this library that writes
- * X-sized inputs or indices included) are waited for in full.  Y, the
- * workspace and everything else are written only after the preceding kernel
- * has finished. */
+ * tokens, X of any call, or indices included: the microscaled products, decoder
+ * and experts below too) are waited for in full.  Y, the workspace and everything
+ * else are written only after the preceding kernel has finished. */
 int e8_gemm(const e8_codebook* cb, const uint16_t* X, int64_t M, const uint16_t* idx1,
             const void* idx2, int64_t N, int64_t K, int bpw, uint64_t rht_seed, float scale,
             float* Y, int mode, void* workspace, size_t ws_bytes, void* stream);

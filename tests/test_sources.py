@@ -21,3 +21,23 @@ def test_no_copy_is_multicast_to_a_cluster():
         for line in text.splitlines():
             if "multicast::cluster" in line:
                 assert "tcgen05.commit" in line and "cp.async" not in line, (name, line)
+
+
+# kernels that let the next kernel of the stream start before they have ended: they write
+# workspaces, fp32 results, codes or scales, but nothing that a call takes as X or as indices
+RELEASE = {"k_act_rht_fast", "k_act_q8", "k_gemm_q8", "k_mx4_encode", "k_moe_route"}
+
+
+def test_kernels_whose_output_is_an_input_of_e8_gemm_end_before_the_next_starts():
+    """e8_gemm reads X, idx1 and idx2 before it waits for the kernel in front of it, so a
+    kernel that writes tokens (bf16) may not release its dependents early."""
+    found = set()
+    for name, text in _sources().items():
+        text = re.sub(r"//[^\n]*", "", text)
+        kernel = None
+        for m in re.finditer(r"__global__[^;{]*?\b(k_\w+)\s*\(|\bgrid_dep_launch\(\);", text):
+            if m.group(1):
+                kernel = m.group(1)
+            else:
+                found.add(kernel)
+    assert found == RELEASE
