@@ -533,13 +533,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   unsigned long long* mask = reinterpret_cast<unsigned long long*>(smem);
   int16_t* chosen = reinterpret_cast<int16_t*>(mask + kMaxExperts);
-  for (int i = threadIdx.x; i < g.E; i += kThreads) mask[i] = 0ull;
+  // in the ring's bytes, hence only for build_lists, which fences its writes from the
+  // copies that follow them there
+  const int slots = g.T * g.topk;
+  if (slots > 32)
+    for (int i = threadIdx.x; i < g.E; i += kThreads) mask[i] = 0ull;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
   grid_dep_wait();
-  const int slots = g.T * g.topk;
   int claim = 0;
   if (threadIdx.x == 256) claim = atomicAdd(g.claimed, 1);
   if (threadIdx.x < g.T) token_scale[threadIdx.x] = g.xs[threadIdx.x];

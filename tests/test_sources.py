@@ -41,3 +41,16 @@ def test_kernels_whose_output_is_an_input_of_e8_gemm_end_before_the_next_starts(
             else:
                 found.add(kernel)
     assert found == RELEASE
+
+
+def test_the_experts_ring_is_not_written_without_a_proxy_fence():
+    """The lists' scratch space lies where copies of the async proxy land next: ordinary
+    writes to it happen only on the path that ends with a fence of the two."""
+    text = _sources()["e8_moe.cu"]
+    lists = text[text.index("void build_lists("):text.index("// A unit as the scheduler")]
+    assert lists.rstrip().endswith("fence_proxy_async_smem();   // the scratch space becomes the copies' ring\n"
+                                   "  __syncthreads();\n}")
+    kernel = text[text.index("k_moe_experts(const"):]
+    assert kernel.count("mask[") == 1
+    assert re.search(r"if \(slots > 32\)\s*for \([^)]*\) mask\[i\] = 0ull;", kernel)
+    assert re.search(r"if \(slots > 32\)\s*build_lists\(", kernel)
