@@ -36,6 +36,15 @@ __device__ __forceinline__ uint64_t global_timer_ns() {
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
   return t;
 }
+// Nanoseconds from one reading to another.  Two readings of the timer may come out in the
+// wrong order: that is no time at all, and not the 2^64 less a little of an unsigned
+// difference, after which every bounded wait would end.
+__host__ __device__ __forceinline__ uint64_t ns_between(uint64_t since, uint64_t now) {
+  return (int64_t)(now - since) > 0 ? now - since : 0;
+}
+__device__ __forceinline__ uint64_t ns_since(uint64_t since) {
+  return ns_between(since, global_timer_ns());
+}
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -148,7 +157,7 @@ __device__ __forceinline__ bool mbar_wait_sleep(uint64_t* bar, uint32_t parity,
   for (;;) {
     if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
     if (ld_shared_volatile(abort_flag)) return false;
-    if (global_timer_ns() - t0 > kWaitLimitNs) {
+    if (ns_since(t0) > kWaitLimitNs) {
       st_shared_volatile(abort_flag, 1u);
       if (status) atomicOr(status, code);
       return false;
@@ -179,7 +188,7 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
     if (mbar_try_wait(bar, parity)) return true;
     if ((it & 63u) == 0) {
       if (*abort_flag) return false;
-      if (global_timer_ns() - t0 > kWaitLimitNs) {
+      if (ns_since(t0) > kWaitLimitNs) {
         *abort_flag = 1u;
         if (status) atomicOr(status, code);
         return false;
@@ -201,7 +210,7 @@ __device__ __forceinline__ bool mbar_wait_lazy(uint64_t* bar, uint32_t parity,
       if (ld_shared_volatile(abort_flag)) return false;
       const uint64_t t = global_timer_ns();
       if (t0 == 0) t0 = t;
-      if ((int64_t)(t - t0) > (int64_t)kWaitLimitNs) {
+      if (ns_between(t0, t) > kWaitLimitNs) {
         st_shared_volatile(abort_flag, 1u);
         if (status) atomicOr(status, code);
         return false;

@@ -300,11 +300,11 @@ __global__ void __launch_bounds__(dtc::THREADS, 1)
         // let the copies in flight land before the CTA exits
         uint64_t t0 = global_timer_ns();
         while (!mbar_try_wait(table_full, 0))
-          if (global_timer_ns() - t0 > 100000000ull) break;
+          if (ns_since(t0) > 100000000ull) break;
         for (int64_t j = issued > CSTAGES ? issued - CSTAGES : 0; j < issued; ++j) {
           t0 = global_timer_ns();
           while (!mbar_try_wait(&code_full[j % CSTAGES], (uint32_t)(j / CSTAGES) & 1u))
-            if (global_timer_ns() - t0 > 100000000ull) break;
+            if (ns_since(t0) > 100000000ull) break;
         }
       }
     }
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(dtc::THREADS, 1)
       mma_commit(drain);
       const uint64_t t1 = global_timer_ns();
       while (!mbar_try_wait(drain, 0))
-        if (global_timer_ns() - t1 > 200000000ull) break;
+        if (ns_since(t1) > 200000000ull) break;
     }
     __syncwarp();
   } else if (warp < RD_WARP0) {

@@ -15,7 +15,7 @@ __global__ void k_wait_never_signalled(uint32_t* status, uint64_t limit_ns) {
   fence_mbar_init();
   uint64_t t0 = global_timer_ns();
   while (!mbar_try_wait(&bar, 0)) {
-    if (global_timer_ns() - t0 > limit_ns) {
+    if (ns_since(t0) > limit_ns) {
       atomicOr(status, kDevTimeoutFull);
       return;
     }

@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(ag::THREADS, 1)
           uint32_t idx = issued - 1 - j;
           uint64_t t0 = global_timer_ns();
           while (!mbar_try_wait(&full_load[idx % S], (idx / S) & 1u))
-            if (global_timer_ns() - t0 > 100000000ull) break;
+            if (ns_since(t0) > 100000000ull) break;
         }
       }
     }
@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(ag::THREADS, 1)
       mma_commit(drain);
       uint64_t t0 = global_timer_ns();
       while (!mbar_try_wait(drain, 0))
-        if (global_timer_ns() - t0 > 200000000ull) break;
+        if (ns_since(t0) > 200000000ull) break;
     }
   } else {
     // ---------------------------------------------------------- decoders --

@@ -35,7 +35,7 @@ constexpr size_t SMEM_BYTES = 1024 + (size_t)STAGES * STAGE_BYTES + 256;
 __device__ __forceinline__ bool mbar_wait_drain(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
   uint64_t t0 = global_timer_ns();
   while (!mbar_try_wait(bar, parity)) {
-    if (global_timer_ns() - t0 > limit_ns) return false;
+    if (ns_since(t0) > limit_ns) return false;
   }
   return true;
 }
@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(dg2::THREADS, 1)
       if (*abort_flag) {
         // copies in flight may still land: give them time before the CTA exits
         const uint64_t t0 = global_timer_ns();
-        while (global_timer_ns() - t0 < 1000000ull) {
+        while (ns_since(t0) < 1000000ull) {
         }
       }
     }

@@ -411,9 +411,9 @@ __global__ void __maxnreg__(64)
         // a stage's barrier may never complete once the other roles stopped)
         uint64_t t0 = global_timer_ns();
         while (!mbar_try_wait(table_full, 0))
-          if (global_timer_ns() - t0 > 100000000ull) break;
+          if (ns_since(t0) > 100000000ull) break;
         t0 = global_timer_ns();
-        while (global_timer_ns() - t0 < 1000000ull) {
+        while (ns_since(t0) < 1000000ull) {
         }
       }
     }
@@ -492,7 +492,7 @@ __global__ void __maxnreg__(64)
       mma_commit(&drain[par]);
       const uint64_t t0 = global_timer_ns();
       while (!mbar_try_wait(&drain[par], 0))
-        if (global_timer_ns() - t0 > 200000000ull) break;
+        if (ns_since(t0) > 200000000ull) break;
     }
     __syncwarp();
   } else if (warp == XQ_WARP) {
@@ -532,7 +532,7 @@ __global__ void __maxnreg__(64)
       if (ld_shared_volatile(abort_flag)) {
         // let the copies in flight land before the CTA exits
         const uint64_t t0 = global_timer_ns();
-        while (global_timer_ns() - t0 < 1000000ull) {
+        while (ns_since(t0) < 1000000ull) {
         }
       }
     }

@@ -324,7 +324,7 @@ __device__ __forceinline__ bool wait_gpu(const int* counter, int want,
       if (ld_shared_volatile(abort_flag)) return false;
       const uint64_t t = global_timer_ns();
       if (t0 == 0) t0 = t;
-      if ((int64_t)(t - t0) > (int64_t)kWaitLimitNs) {
+      if (ns_between(t0, t) > kWaitLimitNs) {
         st_shared_volatile(abort_flag, 1u);
         if (status) atomicOr(status, kDevTimeoutCluster);
         return false;
@@ -844,7 +844,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // every MMA of this thread has finished once `drain` flips
       mma_commit(&drain);
       const uint64_t t0 = global_timer_ns();
-      while (!mbar_try_wait(&drain, 0) && global_timer_ns() - t0 < 200000000ull) {
+      while (!mbar_try_wait(&drain, 0) && ns_since(t0) < 200000000ull) {
       }
     }
   } else {
@@ -1041,7 +1041,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (abort_flag) {
     // copies in flight may still land: give them time before the CTA exits
     const uint64_t t0 = global_timer_ns();
-    while (global_timer_ns() - t0 < 1000000ull) {
+    while (ns_since(t0) < 1000000ull) {
     }
   }
   __syncwarp();

@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(DT < 0 ? kStreamThreads : kStreamThreadsX, 1)
   if (abort_flag) {
     // copies in flight may still land: give them time before the CTA exits
     const uint64_t t0 = global_timer_ns();
-    while (global_timer_ns() - t0 < 1000000ull) {
+    while (ns_since(t0) < 1000000ull) {
     }
   }
   if (S == 1) {
@@ -553,7 +553,7 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
       // every MMA of this thread has finished once `drain` flips
       mma_commit_2sm(&drain);
       const uint64_t t0 = global_timer_ns();
-      while (!mbar_try_wait(&drain, 0) && global_timer_ns() - t0 < 200000000ull) {
+      while (!mbar_try_wait(&drain, 0) && ns_since(t0) < 200000000ull) {
       }
     }
   } else {
@@ -625,7 +625,7 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
   if (abort_flag) {
     // copies in flight may still land: give them time before the CTA exits
     const uint64_t t0 = global_timer_ns();
-    while (global_timer_ns() - t0 < 1000000ull) {
+    while (ns_since(t0) < 1000000ull) {
     }
   }
   // no CTA frees its tensor memory or leaves while the pair's MMAs, another CTA's

@@ -2,6 +2,9 @@
 import glob
 import os
 import re
+import subprocess
+
+from decode_gemm_e8_b200 import build as e8build
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "decode_gemm_e8_b200", "csrc")
 
@@ -54,3 +57,27 @@ def test_the_experts_ring_is_not_written_without_a_proxy_fence():
     assert kernel.count("mask[") == 1
     assert re.search(r"if \(slots > 32\)\s*for \([^)]*\) mask\[i\] = 0ull;", kernel)
     assert re.search(r"if \(slots > 32\)\s*build_lists\(", kernel)
+
+
+def test_a_timer_that_reads_backwards_ends_no_wait(tmp_path):
+    """Every bounded wait measures its time with ns_between, which answers 0 when the later
+    reading is the smaller one."""
+    for name, text in _sources().items():
+        assert not re.search(r"global_timer_ns\(\)\s*-", text), name
+        assert not re.search(r"\bt - t0\b", text), name
+    src = tmp_path / "t.cu"
+    src.write_text('''#include <cstdio>
+#include "e8_common.cuh"
+int main() {
+  const uint64_t top = 1ull << 63;
+  const uint64_t pair[][2] = {{5, 5}, {5, 9}, {9, 5}, {1ull << 60, (1ull << 60) - 1}, {7, 7 + e8::kWaitLimitNs},
+                              {top - 2, top + 3}, {~0ull, 2}};
+  for (const auto& p : pair) std::printf("%llu\\n", (unsigned long long)e8::ns_between(p[0], p[1]));
+}
+''')
+    exe = tmp_path / "t"
+    root = os.path.dirname(os.path.dirname(CSRC))
+    subprocess.run([e8build.NVCC, *e8build.ARCH, "-std=c++17", "--expt-relaxed-constexpr", "-I", CSRC, "-I",
+                    os.path.join(root, "include"), "-o", str(exe), str(src)], check=True)
+    out = subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()
+    assert [int(v) for v in out] == [0, 4, 0, 0, 2000000000, 5, 3]
