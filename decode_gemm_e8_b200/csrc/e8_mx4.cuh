@@ -40,6 +40,10 @@ inline cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, siz
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+// Tiles of `size` in n >= 1 (n may be 2^31 - 1: no sum of the two).
+__host__ __device__ __forceinline__ constexpr int tiles_of(int n, int size) {
+  return (n - 1) / size + 1;
+}
 // Bytes of one row of codes: 16 for each block of 32.
 __host__ __device__ __forceinline__ int64_t code_stride(int64_t K) { return (K + 31) / 32 * 16; }
 // Tiles of 128 columns in a row of scale tiles.

@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(DT < 0 ? kStreamThreads : kStreamThreadsX, 1)
   const int n0 = (int)blockIdx.x / S * kStreamRows, m0 = (int)blockIdx.y * a.bn;
   const int nbt = (a.bn + 127) / 128;
   const int stage_bytes = stream_stage_bytes(a.bn);
-  const int kblocks = (a.K + kBK - 1) / kBK, kqs = (int)scale_tiles(a.K);
+  const int kblocks = tiles_of(a.K, kBK), kqs = (int)scale_tiles(a.K);
   const int kb0 = (int)((int64_t)kblocks * rank / S);
   const int nkb = (int)((int64_t)kblocks * (rank + 1) / S) - kb0;
 
@@ -432,9 +432,8 @@ __global__ void __launch_bounds__(pair::kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_ctarank();
   const int first = (int)blockIdx.x / 2, step = (int)gridDim.x / 2;
-  const int tiles_m = (a.M + 255) / 256;
-  const int tiles = tiles_m * ((a.N + kN - 1) / kN);
-  const int kblocks = (a.K + kBK - 1) / kBK, kqs = (int)scale_tiles(a.K);
+  const int tiles_m = tiles_of(a.M, 256), tiles = tiles_m * tiles_of(a.N, kN);
+  const int kblocks = tiles_of(a.K, kBK), kqs = (int)scale_tiles(a.K);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {

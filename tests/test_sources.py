@@ -81,3 +81,22 @@ int main() {
                     os.path.join(root, "include"), "-o", str(exe), str(src)], check=True)
     out = subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()
     assert [int(v) for v in out] == [0, 4, 0, 0, 2000000000, 5, 3]
+
+
+def test_tile_counts_at_the_largest_sizes(tmp_path):
+    """Sizes go up to 2^31 - 1; the product's kernels count their tiles in 32 bits."""
+    text = re.sub(r"//[^\n]*", "", _sources()["e8_mx4_gemm.cu"])
+    assert not re.search(r"\(a\.[MNK] \+ ", text)
+    src = tmp_path / "t.cu"
+    src.write_text('''#include <cstdio>
+#include "e8_mx4.cuh"
+int main() {
+  for (int n : {1, 256, 257, 2147483391, 2147483392, 2147483393, 2147483647})
+    std::printf("%d\\n", e8::mx4::tiles_of(n, 256));
+}
+''')
+    exe = tmp_path / "t"
+    subprocess.run([e8build.NVCC, *e8build.ARCH, "-std=c++17", "--expt-relaxed-constexpr", "-I", CSRC, "-I",
+                    e8build.INCLUDE, "-o", str(exe), str(src)], check=True)
+    out = subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()
+    assert [int(v) for v in out] == [1, 1, 2, 2 ** 23 - 1, 2 ** 23 - 1, 2 ** 23, 2 ** 23]
