@@ -546,7 +546,8 @@ def e8_ep_gemm(cb: Codebook, X, m: EpMatrix, Y=None, workspace=None, stream=None
 class Mx4Matrix:
     """A [rows, K] matrix (or a batch of them) in blocks of 32 e2m1 values with a
     power-of-two scale each, as e8_mx4_encode writes it: codes uint8
-    [(batch,) rows, 16 ceil(K / 32)] and scales uint8 [(batch,) bytes in tiles]."""
+    [(batch,) rows, 16 ceil(K / 32)] and scales uint8 [(batch,) bytes in tiles] (other
+    one-byte types are taken as their bytes)."""
 
     __slots__ = ("rows", "K", "batch", "_codes", "_scales", "_both")
 
@@ -557,6 +558,8 @@ class Mx4Matrix:
         self.batch = None if batch is None else int(batch)
         n = 1 if batch is None else self.batch
         # e8_mx4_code_bytes and e8_mx4_scale_bytes
+        if codes.element_size() != 1 or scales.element_size() != 1:
+            raise E8Error(E8_EINVAL, "Mx4Matrix")
         if rows < 0 or K < 1 or codes.numel() != n * rows * ((K + 31) // 32 * 16) or \
                 scales.numel() != n * ((rows + 127) // 128) * ((K + 127) // 128) * 512:
             raise E8Error(E8_EINVAL, "Mx4Matrix")
