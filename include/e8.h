@@ -467,9 +467,13 @@ size_t e8_mx4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
  * [H][I]; Y bf16 [T][H].  Optional outputs (NULL to skip): experts int32
  * [T][topk], by falling logit, and probs fp32 [T][topk].
  * X enters the products as two 8-bit floats a value with one power-of-two scale a
- * token: exactly, but for values 2^14 times smaller than the token's largest, which
- * are off by at most 2^-21 of that.  h enters likewise with a scale for each 64
- * values, rounded to 8 significant bits.  All sums are fp32, added in a fixed order.
+ * token: exactly down to 2^-13 of the token's largest; smaller ones are off by at most
+ * 2^-21 of that.  h enters likewise with a scale for each 64 values (those of rows 128 i
+ * .. 128 i + 127 of w13): off by at most 2^-9 of itself (rounding to bf16: 2^-8) down
+ * to 2^-12 of the 64 values' largest, below by at most 2^-21 of that, or 2^-137.  All
+ * sums are fp32, added in a fixed order.  The up products' sums hold X divided by its
+ * scale, up to 256: weights up to 2^104 cannot overflow them.  Where h overflows fp32,
+ * the token's row of Y is NaN.
  * A token with a NaN or an infinity gives a row of NaN and leaves the others alone.
  * An expert that no token chose is not read.
  * Shapes: 0 <= T <= E8_MOE_MAX_TOKENS, 1 <= topk <= min(E, E8_MOE_MAX_TOPK),
