@@ -220,9 +220,8 @@ cudaError_t launch_ep_decode(const uint16_t* words, int64_t n_words, const uint3
                              const float* t, const uint16_t* tables, int64_t N, int64_t K,
                              uint16_t* out, uint32_t* status, int sm_count, cudaStream_t st);
 
-// Microscaled 4-bit form (e8_mx4.cu, e8_mx4_gemm.cu).  dtype: E8_DT_*; release:
-// the next kernel of the stream, launched programmatically, may start at once;
-// early: the weights may be read before the preceding kernel has ended.
+// Microscaled 4-bit form (e8_mx4.cu, e8_mx4_gemm.cu).  dtype: E8_DT_*; early: the
+// weights may be read before the preceding kernel has ended.
 cudaError_t launch_mx4_encode(const void* X, int dtype, int64_t batch, int64_t rows, int64_t K,
                               int64_t ldx, uint8_t* codes, uint8_t* scales, int sm_count,
                               cudaStream_t st);

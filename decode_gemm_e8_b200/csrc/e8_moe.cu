@@ -1061,11 +1061,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ------------------------------------------------------------------- host ---
 // K parts of the down product's units: at most eight stages a unit, so that the end is
 // even and a block that waits for one expert's h has other units to do; more when even so
-// there are not two units for three SMs, down to two stages each.
+// there are not two units for three SMs, down to two stages each.  The SMs are a B200's:
+// the workspace's size depends on the split and is asked for without a device.
+constexpr int kSms = 148;
 static int choose_splits(int64_t T, int64_t E, int topk, int64_t tiles, int64_t K) {
   const int kq = (int)(K / kBK);
   const int64_t slots = T * topk, units = (slots < E ? slots : E) * tiles;
-  int64_t s = (kq + 15) / 16, few = 148 * 2 / 3 / units;
+  int64_t s = (kq + 15) / 16, few = kSms * 2 / 3 / units;
   if (few > kq / 4) few = kq / 4;
   if (s < few) s = few;
   return s > kMaxDownParts ? kMaxDownParts : (int)s;

@@ -87,12 +87,6 @@ __device__ __forceinline__ uint32_t pack8(const float (&v)[8]) {
   return r;
 }
 
-// Value of one code (low four bits of c) as fp32: the two exponent bits and the
-// mantissa bit at the top of fp32's fields read as value * 2^-126, exactly.
-__device__ __forceinline__ float code_value(uint32_t c) {
-  return __uint_as_float(((c & 8u) << 28) | ((c & 7u) << 22)) * 0x1p126f;
-}
-
 // ------------------------------------------------------------ encoding ---
 // DT: E8_DT_* (0 bf16, 1 fp16, 2 fp32).
 template <int DT> struct Elem;
