@@ -783,7 +783,8 @@ def e8_mx4_moe(cb: Codebook, X, router, w13: Mx4Matrix, w2: Mx4Matrix, topk: int
 
     X bf16 [T, H]; router bf16 [E, H]; w13: E matrices [2 I, H] whose even rows are
     the gate's and odd rows the up-projection's; w2: E matrices [H, I].  experts
-    (int32 [T, topk]) and probs (fp32 [T, topk]) are filled when given."""
+    (int32 [T, topk]) and probs (fp32 [T, topk]) are filled when given.  All tensors are
+    contiguous and start on 16 bytes."""
     import torch
     where = "e8_mx4_moe"
     bf16 = torch.bfloat16

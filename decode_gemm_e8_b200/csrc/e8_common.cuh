@@ -220,16 +220,6 @@ __device__ __forceinline__ bool mbar_wait_lazy(uint64_t* bar, uint32_t parity,
 }
 
 // ------------------------------------------------------------------ TMA ---
-__device__ __forceinline__ void tma_load_2d(void* smem_dst, const CUtensorMap* map, uint64_t* bar,
-                                            int32_t x, int32_t y) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(smem_dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y)
-      : "memory");
-}
-
-// The same, and a plain bulk copy, to a shared-memory address.
 __device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap* map, uint64_t* bar,
                                         int32_t x, int32_t y) {
   asm volatile(
@@ -238,6 +228,11 @@ __device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap* map, ui
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y)
       : "memory");
 }
+__device__ __forceinline__ void tma_load_2d(void* smem_dst, const CUtensorMap* map, uint64_t* bar,
+                                            int32_t x, int32_t y) {
+  load_2d(smem_u32(smem_dst), map, bar, x, y);
+}
+// A plain bulk copy.
 __device__ __forceinline__ void load_bulk(uint32_t dst, const void* src, uint32_t bytes,
                                           uint64_t* bar) {
   asm volatile(
@@ -382,14 +377,6 @@ __device__ __forceinline__ void mma_commit_2sm(uint64_t* bar) {
 }
 // 2-D tile load into this CTA's shared memory whose completion is counted on
 // the barrier at shared::cluster address `bar` (the leader's).
-__device__ __forceinline__ void tma_load_2d_2sm(void* smem_dst, const CUtensorMap* map,
-                                                uint32_t bar, int32_t x, int32_t y) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(smem_dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
-      : "memory");
-}
 __device__ __forceinline__ void load_2d_2sm(uint32_t dst, const CUtensorMap* map, uint32_t bar,
                                             int32_t x, int32_t y) {
   asm volatile(
@@ -398,6 +385,12 @@ __device__ __forceinline__ void load_2d_2sm(uint32_t dst, const CUtensorMap* map
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
       : "memory");
 }
+__device__ __forceinline__ void tma_load_2d_2sm(void* smem_dst, const CUtensorMap* map,
+                                                uint32_t bar, int32_t x, int32_t y) {
+  load_2d_2sm(smem_u32(smem_dst), map, bar, x, y);
+}
+// The address of a leader's barrier: a shared::cluster address of the pair's even CTA.
+constexpr uint32_t kPeerBitMask = 0xFEFFFFFFu;
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");

@@ -213,7 +213,6 @@ constexpr int STAGE_BYTES = 2 * HALF_BYTES;         // X half + W half, per CTA
 constexpr int THREADS = 192;
 constexpr int TMEM_COLS = 512;                      // two 256-column fp32 accumulators
 constexpr size_t SMEM_BYTES = 1024 + (size_t)STAGES * STAGE_BYTES + 256;
-constexpr uint32_t kPeerBitMask = 0xFEFFFFFFu;      // shared::cluster address -> the even CTA
 }  // namespace dg2
 
 __device__ __forceinline__ void mma_ss_2sm(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,

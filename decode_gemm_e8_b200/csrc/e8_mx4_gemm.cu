@@ -29,10 +29,10 @@ namespace mx4 {
 //   warps 2-5  epilogue
 //   warps 2-9  with up to 8 tokens that are not encoded yet (DT >= 0), instead of warp
 //              6: each encodes the tokens of one of the 8 ring slots, every CTA for
-//              itself.  With / without the encoder's launch, in us a call at N x K =
-//              4096 x 4096 and 14336 x 4096: 1 token 7.1 / 5.5 and 10.7 / 8.9, 8 tokens
-//              7.4 / 6.3 and 10.7 / 9.1; 16 tokens 7.6 / 8.1 and 10.7 / 11.6
-// Bound by HBM on W once it runs (16 x 14336 x 4096 10.7 us, 4.9 of them its bytes), the
+//              itself.  With / without the encoder's launch, in us a call in a row of
+//              them at N x K = 4096 x 4096 and 14336 x 4096: 1 token 7.2 / 6.4 and 11.0 /
+//              10.0, 8 tokens 7.4 / 7.2 and 11.1 / 10.3; 16 tokens 7.6 / 8.9 and 11.2 / 13.1
+// Bound by HBM on W once it runs (16 x 14336 x 4096 11.1 us, 4.9 of them its bytes), the
 // rest is its start (5 us: launch, barriers, tensor memory, first tile) and its end.
 constexpr int kStreamThreads = 224, kStreamThreadsX = 320;
 constexpr int kStreamRows = 128;
@@ -392,7 +392,8 @@ static cudaError_t launch_stream(const void* X, int64_t ldx, const uint8_t* a_co
 //   while the stage's MMAs take some 480 cycles, so L2 bounds it before the tensor cores
 //   do.  Clusters of two pairs that shared A by multicast read 22 KB, but only 33 of them,
 //   132 SMs, fit: 105 us for 4096 x 14336 x 4096 with the encoder's launch, 103 this way.
-// Persistent, one pair of SMs a cluster.
+// Persistent, one pair of SMs a cluster.  4096 x 14336 x 4096: 95.6 us, 5.0 PFLOP/s, the
+// tensor pipe active 70 % of the cycles on all 148 SMs.
 //   warp 0      TMA producer of each CTA; a pair's bytes are counted by its leader
 //   warp 1      tensor memory; in the leader scale copies, MMAs, commits
 //   warps 2-9   epilogue: 64 columns at a time to bf16, shared memory and TMA stores
@@ -406,7 +407,6 @@ constexpr uint32_t kStageBytes = kScaleOff + 1024 + 2048;
 constexpr int kSfCol0 = 2 * kN, kSfCols = 24;
 constexpr int kPitch = 66;                         // elements of a staged row
 constexpr int kStaged = 8 * 4352;                  // bytes, a piece of each epilogue warp
-constexpr uint32_t kPeerBitMask = 0xFEFFFFFFu;     // shared::cluster address -> the even CTA
 static_assert(kSfCol0 + kStages * kSfCols <= 512, "tensor memory");
 static_assert(32 * kPitch * 2 <= 4352, "staging");
 }  // namespace pair
@@ -691,10 +691,18 @@ static cudaError_t launch_pair(const uint8_t* a_codes, const uint8_t* a_scales, 
 
 }  // namespace mx4
 
-// Tokens above which the pair kernel takes over.  In us, stream / pair, at N x K =
-// 4096 x 4096, 14336 x 4096 and 4096 x 14336: 128 tokens 9.1 / 10.7, 13.5 / 16.6 and
-// 12.5 / 22.2; 256 tokens 12.0 / 10.7, 18.6 / 16.8 and 16.6 / 22.2; 257 tokens 14.0 /
-// 10.7, 25.4 / 20.3 and 21.5 / 22.0.
+// Tokens above which the pair kernel takes over: the stream kernel then reads W for a
+// second tile of tokens.  In us a product of encoded matrices, stream / pair, by N x K:
+//                  128 tokens     256     |     257          512         1000
+//    4096 x 4096   9.4 / 11.2  12.5 / 11.3 | 14.6 / 11.3  15.0 / 11.5  17.7 / 16.1
+//   14336 x 4096  13.8 / 16.7  19.1 / 17.1 | 26.2 / 20.7  34.0 / 21.4  63.3 / 30.5
+//    4096 x 1024   7.1 /  6.6   9.9 /  6.8 | 11.2 /  6.8  12.0 /  7.5  12.9 /  9.9
+//     512 x 4096   7.1 /  9.7   9.9 /  9.6 |  9.9 /  9.7  10.2 /  9.6  19.3 /  9.8
+//   4096 x 14336  13.1 / 22.5  17.2 / 22.8 | 22.3 / 22.5  22.8 / 22.9  32.3 / 37.8
+//    512 x 14336   8.9 / 19.8  12.2 / 20.0 | 12.4 / 20.0  13.0 / 21.2  23.8 / 21.4
+// What tokens alone do not say: short sums would be faster in pairs from fewer tokens on,
+// and with few columns and a long K, which the pair kernel does not split, the stream
+// kernel would be up to some 800.
 constexpr int kPairFrom = 256;
 
 cudaError_t launch_mx4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int64_t M,

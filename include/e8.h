@@ -410,7 +410,8 @@ int e8_ep_gemm(const e8_codebook* cb, const uint16_t* X, int64_t M, const uint16
  *     This is the order the tensor cores take scales in.
  * A batch of matrices is stored matrix after matrix, each with its own tiles.
  * The codebook handle selects the device and carries the status word.
- * Code and scale buffers must be 16-byte (for e8_mx4_moe 32-byte) aligned. */
+ * Code and scale buffers must be 16-byte (for e8_mx4_moe 32-byte) aligned, and so must
+ * out, Y, workspaces, and X, router, experts and probs of e8_mx4_moe (16-byte). */
 #define E8_DT_BF16 0
 #define E8_DT_F16 1
 #define E8_DT_F32 2
